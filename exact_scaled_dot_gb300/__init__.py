@@ -13,4 +13,7 @@ from ._binding import (  # noqa: F401
     attn_get_status, attn_selftest_wait_timeout, attn_visible_pairs, load, make_shape, strerror,
     AttnVarlen, attn_bwd_varlen, attn_bwd_varlen_workspace_bytes, attn_fwd_varlen, attn_varlen_visible_pairs,
     attn_proj_bwd_input, attn_proj_bwd_weight, attn_proj_fwd, attn_rope, attn_rope_qk,
+    ATTN_CACHE_PAGE_TOKENS, ATTN_ERR_PAGE, ATTN_MAX_AXES, QuantCache, RotaryAxes, attn_cache_append,
+    attn_cache_page_bytes, attn_cache_read, attn_fwd_decode_cache, attn_fwd_decode_cache_workspace_bytes,
+    attn_qk_norm_rope, attn_qk_norm_rope_bwd, attn_qk_norm_rope_bwd_workspace_bytes, attn_rope_axes,
 )

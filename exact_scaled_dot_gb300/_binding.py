@@ -13,6 +13,7 @@ decode forward takes contiguous tensors only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from pathlib import Path
@@ -35,6 +36,9 @@ ATTN_ERR_CUDA = 8
 ATTN_ERR_TIMEOUT = 9
 ATTN_ERR_DEVICE = 10
 ATTN_ERR_RANGE = 11
+ATTN_ERR_PAGE = 12
+ATTN_MAX_AXES = 3
+ATTN_CACHE_PAGE_TOKENS = 32
 ATTN_MAX_BATCH = 512
 ATTN_OFFSET_DEFAULT = -(2 ** 63)
 
@@ -44,7 +48,10 @@ EXPORTS = ("attn_fwd", "attn_fwd_workspace_bytes", "attn_fwd_varlen_workspace_by
            "attn_selftest_wait_timeout", "attn_strerror", "attn_abi_version", "attn_bwd_noalloc",
            "attn_bwd_noalloc_max_scratch_bytes", "attn_varlen_visible_pairs", "attn_fwd_varlen",
            "attn_bwd_varlen_workspace_bytes", "attn_bwd_varlen", "attn_proj_fwd", "attn_proj_bwd_weight",
-           "attn_proj_bwd_input", "attn_rope", "attn_rope_qk", "attn_bwd_head_split", "attn_bwd_persistent")
+           "attn_proj_bwd_input", "attn_rope", "attn_rope_qk", "attn_bwd_head_split", "attn_bwd_persistent",
+           "attn_rope_axes", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes",
+           "attn_cache_page_bytes", "attn_cache_append", "attn_cache_read", "attn_fwd_decode_cache",
+           "attn_fwd_decode_cache_workspace_bytes")
 
 
 class AttnError(RuntimeError):
@@ -75,6 +82,20 @@ class AttnStrides(ctypes.Structure):
 class AttnRotary(ctypes.Structure):
     _fields_ = [("base", ctypes.c_float), ("pos_q", ctypes.c_void_p), ("pos_k", ctypes.c_void_p),
                 ("q_rot", ctypes.c_void_p), ("k_rot", ctypes.c_void_p)]
+
+
+class AttnRotaryAxes(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_float), ("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * ATTN_MAX_AXES),
+                ("restart", ctypes.c_int32), ("pos", ctypes.c_void_p)]
+
+
+class AttnQkStrides(ctypes.Structure):
+    _fields_ = [(n, AttnTensorStrides) for n in ("q", "k", "yq", "yk", "dyq", "dyk", "dq", "dk")]
+
+
+class AttnCache(ctypes.Structure):
+    _fields_ = [("Hkv", ctypes.c_int32), ("d_h", ctypes.c_int32), ("d_v", ctypes.c_int32), ("pages", ctypes.c_int64),
+                ("pool", ctypes.c_void_p)]
 
 
 class AttnVarlen(ctypes.Structure):
@@ -146,10 +167,24 @@ def load(path: Optional[Path] = None) -> ctypes.CDLL:
                                         ctypes.POINTER(_vp), _vp, _vp]
     lib.attn_rope.argtypes = [i64, i32, i32, f, _vp, i32, _vp, _vp, _vp]
     lib.attn_rope_qk.argtypes = [i64, i32, i32, i32, f, _vp, i32, _vp, _vp, _vp, _vp, _vp]
+    RA, QS, CA = ctypes.POINTER(AttnRotaryAxes), ctypes.POINTER(AttnQkStrides), ctypes.POINTER(AttnCache)
+    lib.attn_rope_axes.argtypes = [i64, i32, i32, i32, RA, i32, QS, _vp, _vp, _vp, _vp, _vp]
+    lib.attn_qk_norm_rope.argtypes = [i64, i32, i32, i32, f, RA, QS, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_qk_norm_rope_bwd.argtypes = [i64, i32, i32, i32, f, RA, QS] + [_vp] * 11 + [ctypes.c_size_t, _vp]
+    lib.attn_cache_page_bytes.argtypes = [i32, i32, i32]
+    lib.attn_cache_page_bytes.restype = ctypes.c_size_t
+    lib.attn_cache_append.argtypes = [CA, i64, ST, _vp, _vp, _vp, _vp]
+    lib.attn_cache_read.argtypes = [CA, i64, ST, _vp, _vp, _vp, _vp]
+    lib.attn_fwd_decode_cache_workspace_bytes.argtypes = [CA, i32, i32, i32, i32]
+    lib.attn_fwd_decode_cache_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_fwd_decode_cache.argtypes = [CA, i32, i32, i32, i32, f, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     for name in ("attn_fwd", "attn_fwd_decode", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main", "attn_bwd_finalize",
                  "attn_get_status", "attn_clear_status", "attn_selftest_wait_timeout", "attn_fwd_varlen",
                  "attn_bwd_varlen", "attn_proj_fwd", "attn_proj_bwd_weight", "attn_proj_bwd_input",
-                 "attn_rope", "attn_rope_qk"):
+                 "attn_rope", "attn_rope_qk", "attn_rope_axes", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
+                 "attn_cache_append", "attn_cache_read", "attn_fwd_decode_cache"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -809,3 +844,284 @@ def attn_rope_qk(Q, K, positions, *, base: float = 10000.0, inverse: bool = Fals
                              _ptr(Yq), _ptr(K), _ptr(Yk), _stream(dev, stream))
     _check(rc, "attn_rope_qk")
     return Yq, Yk
+
+
+# ---------------------------------------------------------------------------
+# Query/key norm and rotation over several position axes (token-major rows)
+# ---------------------------------------------------------------------------
+class RotaryAxes:
+    """Rotary position embedding over one to three position axes
+    (attn_rotary_axes): positions is an int32 device tensor [axes, tokens]
+    ([tokens] for one axis), sections the number of two-element blocks of the
+    head width that each axis turns (default for one axis: all of them;
+    blocks past the last section keep their value).  restart: every section
+    has frequencies of its own (base^(-k/section)) instead of sharing
+    base^(-2k/d)."""
+
+    def __init__(self, positions: torch.Tensor, sections: Optional[Sequence[int]] = None, base: float = 10000.0,
+                 restart: bool = False):
+        self.positions = positions
+        self.sections = None if sections is None else tuple(int(s) for s in sections)
+        self.base, self.restart = float(base), bool(restart)
+
+    def arg(self, tokens: int, d: int, device):
+        pos, sections = self.positions, self.sections
+        if sections is None:
+            sections = (d // 2,)
+        n = len(sections)
+        if not 1 <= n <= ATTN_MAX_AXES:
+            raise ValueError(f"sections must name 1 to {ATTN_MAX_AXES} axes")
+        _check_tensor(pos, "positions", torch.int32, (tokens,) if n == 1 and pos.dim() == 1 else (n, tokens), device)
+        r = AttnRotaryAxes(self.base, n, (ctypes.c_int32 * ATTN_MAX_AXES)(*sections), 1 if self.restart else 0,
+                           pos.data_ptr())
+        return ctypes.byref(r)
+
+
+def _scope(dev, stream):
+    """Where a call allocates and launches: on the caller's stream (so that the
+    allocator ties outputs and workspaces created here to the work that uses
+    them), and on the tensors' device, which need not be the current one."""
+    if not dev.type == "cuda":
+        raise ValueError(f"CUDA tensors are required, got {dev}")
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _check_rows(t, name, shape, dev):
+    """A token-major bf16 view [tokens, heads, d] with contiguous rows."""
+    _check_tensor(t, name, torch.bfloat16, shape, dev, strided=True)
+    return t
+
+
+def _qk_dims(Q, K):
+    if Q.dim() != 3 or (K is not None and K.dim() != 3):
+        raise ValueError("Q and K must be 3-D [tokens, heads, d]")
+    T, Hq, d = (int(x) for x in Q.shape)
+    Hk = 0 if K is None else int(K.shape[1])
+    dev = Q.device
+    _check_rows(Q, "Q", (T, Hq, d), dev)
+    if K is not None:
+        _check_rows(K, "K", (T, Hk, d), dev)
+    return T, Hq, Hk, d, dev
+
+
+def _qk_strides(**tensors):
+    """attn_qk_strides of the given token-major tensors, or None when all are contiguous."""
+    st = None
+    for field, t in tensors.items():
+        if t is None or t.is_contiguous():
+            continue
+        if st is None:
+            st = AttnQkStrides()
+        setattr(st, field, AttnTensorStrides(*_packed_strides(t)))
+    return None if st is None else ctypes.byref(st)
+
+
+def _rows_like(Y, name, like, dev):
+    """The caller's output for rows `like`, or a new contiguous one."""
+    if like is None:
+        if Y is not None:
+            raise ValueError(f"{name} was given without its input")
+        return None
+    if Y is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=dev)
+    return _check_rows(Y, name, tuple(like.shape), dev)
+
+
+def _check_weight(g, name, d, dev, rows):
+    if g is not None:
+        if rows is None:
+            raise ValueError(f"{name} was given without its rows")
+        _check_tensor(g, name, torch.bfloat16, (d,), dev)
+
+
+def _weight_grad(t, name, g, d, dev):
+    if g is None:
+        if t is not None:
+            raise ValueError(f"{name} was given without its weight")
+        return None
+    if t is None:
+        return torch.empty((d,), dtype=torch.float32, device=dev)
+    _check_tensor(t, name, torch.float32, (d,), dev)
+    return t
+
+
+def attn_rope_axes(Q, K, rotary: RotaryAxes, *, inverse: bool = False, Yq=None, Yk=None, stream=None):
+    """The rotation of queries Q [tokens, Hq, d] and keys K [tokens, Hkv, d]
+    (or None) over the axes of ``rotary``, in one launch; returns (Yq, Yk).
+    inverse=True turns back (the gradient map).  Views with contiguous rows
+    are read and written in place; Yq may be Q and Yk may be K."""
+    T, Hq, Hk, d, dev = _qk_dims(Q, K)
+    with _scope(dev, stream):
+        Yq, Yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
+        rc = load().attn_rope_axes(T, Hq, Hk, d, rotary.arg(T, d, dev), 1 if inverse else 0,
+                                   _qk_strides(q=Q, k=K, yq=Yq, yk=Yk), _ptr(Q), _ptr(K), _ptr(Yq), _ptr(Yk),
+                                   _stream(dev, stream))
+    _check(rc, "attn_rope_axes")
+    return Yq, Yk
+
+
+def attn_qk_norm_rope(Q, K, gq=None, gk=None, rotary: Optional[RotaryAxes] = None, *, eps: float = 1e-6, Yq=None,
+                      Yk=None, stream=None):
+    """RMS norm over the head width of every row of Q [tokens, Hq, d] and
+    K [tokens, Hkv, d] (or None), times the bf16 weights gq, gk [d] (None:
+    ones), then the rotation (None: none), in one pass; returns (Yq, Yk)."""
+    T, Hq, Hk, d, dev = _qk_dims(Q, K)
+    _check_weight(gq, "gq", d, dev, Q)
+    _check_weight(gk, "gk", d, dev, K)
+    with _scope(dev, stream):
+        Yq, Yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
+        rc = load().attn_qk_norm_rope(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
+                                      _qk_strides(q=Q, k=K, yq=Yq, yk=Yk), _ptr(Q), _ptr(K), _ptr(gq), _ptr(gk),
+                                      _ptr(Yq), _ptr(Yk), _stream(dev, stream))
+    _check(rc, "attn_qk_norm_rope")
+    return Yq, Yk
+
+
+def attn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hkv, d) -> int:
+    return int(load().attn_qk_norm_rope_bwd_workspace_bytes(int(tokens), int(Hq), int(Hkv), int(d)))
+
+
+def attn_qk_norm_rope_bwd(Q, K, gq, gk, dYq, dYk, rotary: Optional[RotaryAxes] = None, *, eps: float = 1e-6, dQ=None,
+                          dK=None, dgq=None, dgk=None, workspace=None, stream=None):
+    """Gradients of attn_qk_norm_rope with the forward's Q, K, weights, rotary
+    and eps: returns (dQ, dK) in bf16 and (dgq, dgk) in fp32 [d] (None for a
+    weight that is None)."""
+    T, Hq, Hk, d, dev = _qk_dims(Q, K)
+    _check_weight(gq, "gq", d, dev, Q)
+    _check_weight(gk, "gk", d, dev, K)
+    _check_rows(dYq, "dYq", (T, Hq, d), dev)
+    if K is not None:
+        _check_rows(dYk, "dYk", (T, Hk, d), dev)
+    elif dYk is not None:
+        raise ValueError("dYk was given without its input")
+    lib = load()
+    with _scope(dev, stream):
+        dQ, dK = _rows_like(dQ, "dQ", Q, dev), _rows_like(dK, "dK", K, dev)
+        dgq, dgk = (_weight_grad(t, name, g, d, dev) for t, name, g in ((dgq, "dgq", gq), (dgk, "dgk", gk)))
+        if workspace is None:
+            need = int(lib.attn_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d))
+            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+        rc = lib.attn_qk_norm_rope_bwd(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
+                                       _qk_strides(q=Q, k=K, dyq=dYq, dyk=dYk, dq=dQ, dk=dK), _ptr(Q), _ptr(K),
+                                       _ptr(gq), _ptr(gk), _ptr(dYq), _ptr(dYk), _ptr(dQ), _ptr(dK), _ptr(dgq),
+                                       _ptr(dgk), *_ws(workspace), _stream(dev, stream))
+    _check(rc, "attn_qk_norm_rope_bwd")
+    return dQ, dK, dgq, dgk
+
+
+# ---------------------------------------------------------------------------
+# The paged 4-bit key/value cache
+# ---------------------------------------------------------------------------
+class QuantCache:
+    """A key/value cache held in 4 bits (attn_cache): pool is a contiguous
+    uint8 device tensor [pages, Hkv, block] of the layout in the C header, a
+    page holding ATTN_CACHE_PAGE_TOKENS tokens.  Which page belongs to which
+    sequence is the caller's page table."""
+
+    def __init__(self, pool: torch.Tensor, d_h: int, d_v: int):
+        if not isinstance(pool, torch.Tensor) or pool.dim() != 3:
+            raise ValueError("pool must be a [pages, Hkv, block] tensor")
+        self.pool, self.d_h, self.d_v = pool, int(d_h), int(d_v)
+        self.pages, self.Hkv, block = (int(x) for x in pool.shape)
+        self.device = pool.device
+        _check_tensor(pool, "pool", torch.uint8, tuple(pool.shape), pool.device)
+        # Bytes of one page of one head: codes and a 32-bit word per 64 elements.
+        want = ATTN_CACHE_PAGE_TOKENS * (self.d_h + self.d_v) * 9 // 16
+        if block != want:
+            raise ValueError(f"pool blocks must have {want} bytes for widths ({d_h}, {d_v}), got {block}")
+        self._arg = AttnCache(self.Hkv, self.d_h, self.d_v, self.pages, pool.data_ptr())
+
+    @classmethod
+    def empty(cls, pages: int, Hkv: int, d_h: int, d_v: int, device="cuda"):
+        n = attn_cache_page_bytes(Hkv, d_h, d_v)
+        if n == 0:
+            raise AttnError(ATTN_ERR_UNSUPPORTED, "QuantCache.empty")
+        return cls(torch.empty((int(pages), int(Hkv), n // int(Hkv)), dtype=torch.uint8, device=device), d_h, d_v)
+
+    def arg(self):
+        return ctypes.byref(self._arg)
+
+
+def attn_cache_page_bytes(Hkv, d_h, d_v) -> int:
+    """Bytes of one page over all heads (0 for invalid sizes)."""
+    return int(load().attn_cache_page_bytes(int(Hkv), int(d_h), int(d_v)))
+
+
+def _cache_strides(K, V):
+    if K.is_contiguous() and V.is_contiguous():
+        return None
+    return _strides_arg(True, k=K, v=V)
+
+
+def attn_cache_append(cache: QuantCache, K, V, slots, *, stream=None) -> None:
+    """Write new tokens K [tokens, Hkv, d_h], V [tokens, Hkv, d_v] (bf16) into
+    the cache, rounded to 4 bits: token i into slots[i] = page * 32 + place
+    (int64, device; negative: skipped).  The slots of a call are distinct."""
+    dev = cache.device
+    T = int(K.shape[0]) if K.dim() == 3 else -1
+    _check_rows(K, "K", (T, cache.Hkv, cache.d_h), dev)
+    _check_rows(V, "V", (T, cache.Hkv, cache.d_v), dev)
+    _check_tensor(slots, "slots", torch.int64, (T,), dev)
+    with _scope(dev, stream):
+        rc = load().attn_cache_append(cache.arg(), T, _cache_strides(K, V), _ptr(slots), _ptr(K), _ptr(V),
+                                      _stream(dev, stream))
+    _check(rc, "attn_cache_append")
+
+
+def attn_cache_read(cache: QuantCache, slots, *, K=None, V=None, stream=None):
+    """The tokens of slots [tokens] as the values that the cache stands for,
+    rounded to bf16: returns (K [tokens, Hkv, d_h], V [tokens, Hkv, d_v]);
+    negative slots give zeros."""
+    dev = cache.device
+    T = int(slots.shape[0]) if slots.dim() == 1 else -1
+    _check_tensor(slots, "slots", torch.int64, (T,), dev)
+    ks, vs = (T, cache.Hkv, cache.d_h), (T, cache.Hkv, cache.d_v)
+    with _scope(dev, stream):
+        K = torch.empty(ks, dtype=torch.bfloat16, device=dev) if K is None else _check_rows(K, "K", ks, dev)
+        V = torch.empty(vs, dtype=torch.bfloat16, device=dev) if V is None else _check_rows(V, "V", vs, dev)
+        rc = load().attn_cache_read(cache.arg(), T, _cache_strides(K, V), _ptr(slots), _ptr(K), _ptr(V),
+                                    _stream(dev, stream))
+    _check(rc, "attn_cache_read")
+    return K, V
+
+
+def attn_fwd_decode_cache_workspace_bytes(cache: QuantCache, B, Hq, n_q, max_pages) -> int:
+    return int(load().attn_fwd_decode_cache_workspace_bytes(cache.arg(), int(B), int(Hq), int(n_q), int(max_pages)))
+
+
+def attn_fwd_decode_cache(Q, cache: QuantCache, page_table, lengths, *, scale: Optional[float] = None, O=None,
+                          LSE=None, workspace=None, stream=None):
+    """attn_fwd_decode over the 4-bit cache: Q [B, Hq, n_q, d_h] (bf16, n_q <= 16),
+    page_table int32 [B, max_pages] and lengths int32 [B] on the device (the
+    n_q new tokens counted).  Row i of sequence b sees the keys
+    j <= lengths[b] - n_q + i; a row that sees none gets O = 0, LSE = -inf.
+    Returns (O [B, Hq, n_q, d_v] bf16, LSE [B, Hq, n_q] fp32)."""
+    if Q.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("Q must be 4-D [B, Hq, n_q, d_h] and page_table 2-D [B, max_pages]")
+    B, Hq, n_q, d_h = (int(x) for x in Q.shape)
+    dev = cache.device
+    max_pages = int(page_table.shape[1])
+    _check_tensor(Q, "Q", torch.bfloat16, (B, Hq, n_q, cache.d_h), dev)
+    _check_tensor(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    _check_tensor(lengths, "lengths", torch.int32, (B,), dev)
+    scale = 1.0 / math.sqrt(d_h) if scale is None else float(scale)
+    lib = load()
+    with _scope(dev, stream):
+        if O is None:
+            O = torch.empty((B, Hq, n_q, cache.d_v), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_tensor(O, "O", torch.bfloat16, (B, Hq, n_q, cache.d_v), dev)
+        if LSE is None:
+            LSE = torch.empty((B, Hq, n_q), dtype=torch.float32, device=dev)
+        else:
+            _check_tensor(LSE, "LSE", torch.float32, (B, Hq, n_q), dev)
+        if workspace is None:
+            need = int(lib.attn_fwd_decode_cache_workspace_bytes(cache.arg(), B, Hq, n_q, max_pages))
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        ws_ptr, ws_bytes = (_ws(workspace) if workspace is not None else (None, ctypes.c_size_t(0)))
+        rc = lib.attn_fwd_decode_cache(cache.arg(), B, Hq, n_q, max_pages, scale, _ptr(Q), _ptr(page_table),
+                                       _ptr(lengths), _ptr(O), _ptr(LSE), ws_ptr, ws_bytes, _stream(dev, stream))
+    _check(rc, "attn_fwd_decode_cache")
+    return O, LSE

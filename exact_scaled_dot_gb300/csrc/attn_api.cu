@@ -18,6 +18,7 @@
 #include "common.cuh"
 #include "f16range.cuh"
 #include "ptx.cuh"
+#include "quant_cache.cuh"
 
 namespace esd {
 namespace {
@@ -839,6 +840,147 @@ int rope_launch(int64_t tokens, int32_t heads_a, int32_t heads_b, int32_t d, flo
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------------------
+// Query/key norm and rotation over several axes; the 4-bit cache
+// ---------------------------------------------------------------------------
+int check_axes(const attn_rotary_axes* r, int d) {
+  if (!r) return ATTN_OK;
+  if (r->axes < 1 || r->axes > ATTN_MAX_AXES || (r->restart != 0 && r->restart != 1)) return ATTN_ERR_SHAPE;
+  int64_t sum = 0;
+  for (int a = 0; a < r->axes; ++a) {
+    if (r->sections[a] < 1) return ATTN_ERR_SHAPE;
+    sum += r->sections[a];
+  }
+  if (sum > d / 2) return ATTN_ERR_SHAPE;
+  if (!std::isfinite(r->base) || !(r->base > 1.f)) return ATTN_ERR_SCALE;
+  if (!r->pos) return ATTN_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(r->pos) & 3u) != 0) return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+int check_qk_dims(int64_t tokens, int hq, int hk, int d) {
+  if (tokens <= 0 || tokens > (int64_t{1} << 31) - 1 || hq <= 0 || hk < 0 || hq > 65535 || hk > 65535) return ATTN_ERR_SHAPE;
+  if (d <= 0 || d % 8 != 0 || d > 128) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+// Required pointers of the query tensors, and of the key tensors when there
+// are key heads (none may be given otherwise).
+int check_qk_ptrs(std::initializer_list<const void*> q, std::initializer_list<const void*> k, int hk) {
+  int rc = check_ptrs(q);
+  if (rc) return rc;
+  if (hk > 0) return check_ptrs(k);
+  for (const void* p : k)
+    if (p) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+// The frequency and axis of every block.
+void fill_axes(QkParams* p, const attn_rotary_axes* r, int d) {
+  std::memset(p->w_hi, 0, sizeof(p->w_hi));
+  std::memset(p->w_lo, 0, sizeof(p->w_lo));
+  std::memset(p->axis, 0, sizeof(p->axis));
+  p->axes = r ? r->axes : 0;
+  p->pos = r ? r->pos : nullptr;
+  if (!r) return;
+  int first = 0;
+  for (int a = 0; a < r->axes; ++a) {
+    for (int i = 0; i < r->sections[a]; ++i) {
+      const int k = first + i;
+      const double power = r->restart ? static_cast<double>(i) / r->sections[a] : 2.0 * k / d;
+      const double w = std::pow(static_cast<double>(r->base), -power);
+      p->w_hi[k] = static_cast<float>(w);
+      p->w_lo[k] = static_cast<float>(w - static_cast<double>(p->w_hi[k]));
+      p->axis[k] = static_cast<uint8_t>(a);
+    }
+    first += r->sections[a];
+  }
+}
+
+int qk_strides(const attn_tensor_strides* user, int heads, int d, TensorStrides* out) {
+  return one_strides(user, static_cast<int64_t>(heads) * d, d, d, out);
+}
+
+int check_cache(const attn_cache* c) {
+  if (!c) return ATTN_ERR_NULL;
+  if (c->Hkv <= 0 || c->Hkv > 65535 || c->d_h <= 0 || c->d_v <= 0) return ATTN_ERR_SHAPE;
+  if (c->pages <= 0 || c->pages > (int64_t{1} << 31) - 1) return ATTN_ERR_SHAPE;
+  if (!supported_dims(c->d_h, c->d_v)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int cache_io(const attn_cache* c, int64_t tokens, const attn_strides* strides, const int64_t* slots, const void* K,
+             const void* V, bool append, void* stream) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  if (tokens <= 0 || tokens > (int64_t{1} << 31) - 1) return ATTN_ERR_SHAPE;
+  CacheIoParams p;
+  rc = qk_strides(strides ? &strides->k : nullptr, c->Hkv, c->d_h, &p.sk);
+  if (rc) return rc;
+  rc = qk_strides(strides ? &strides->v : nullptr, c->Hkv, c->d_v, &p.sv);
+  if (rc) return rc;
+  if (!slots) return ATTN_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return ATTN_ERR_ALIGN;
+  rc = check_ptrs({c->pool, K, V});
+  if (rc) return rc;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  p.tokens = tokens;
+  p.Hkv = c->Hkv;
+  p.dh = c->d_h;
+  p.dv = c->d_v;
+  p.pages = c->pages;
+  p.pool = static_cast<uint8_t*>(c->pool);
+  p.slots = slots;
+  p.K = K;
+  p.V = V;
+  p.status = status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = append ? launch_cache_append(p, st) : launch_cache_read(p, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// How attn_fwd_decode_cache divides the work: CTAs of 8 query rows (16 when a
+// KV head has more), each over a range of pages of one sequence.
+struct DecodeCachePlan {
+  int tile_rows, chunks, split_pages, splits;
+  size_t opart_bytes, bytes;
+};
+
+// CTAs that a launch over full-length sequences aims at: four on each SM.
+constexpr int64_t kDecodeCacheCtas = 4 * 152;
+constexpr int kMinSplitPages = 8;
+
+DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int max_pages) {
+  DecodeCachePlan d;
+  const int64_t R = static_cast<int64_t>(Hq / c->Hkv) * n_q;
+  d.tile_rows = R > 8 ? 16 : 8;
+  d.chunks = static_cast<int>((R + d.tile_rows - 1) / d.tile_rows);
+  const int64_t tiles = static_cast<int64_t>(B) * c->Hkv * d.chunks;
+  const int64_t want = std::max<int64_t>(1, (kDecodeCacheCtas + tiles - 1) / tiles);
+  int64_t pages = (max_pages + want - 1) / want;
+  pages = std::max<int64_t>(pages, kMinSplitPages);
+  pages = (pages + 3) / 4 * 4;     // a page for every warp of the CTA
+  d.split_pages = static_cast<int>(pages);
+  d.splits = static_cast<int>((max_pages + pages - 1) / pages);
+  const size_t rows = static_cast<size_t>(B) * Hq * n_q;
+  d.opart_bytes = d.splits > 1 ? round256(d.splits * rows * c->d_v * sizeof(float)) : 0;
+  d.bytes = d.splits > 1 ? d.opart_bytes + round256(d.splits * rows * sizeof(float)) : 0;
+  return d;
+}
+
+int check_decode_cache(const attn_cache* c, int B, int Hq, int n_q, int max_pages) {
+  const int rc = check_cache(c);
+  if (rc) return rc;
+  if (B <= 0 || Hq <= 0 || n_q <= 0 || max_pages <= 0 || Hq % c->Hkv != 0) return ATTN_ERR_SHAPE;
+  if (max_pages > (1 << 26) - 1) return ATTN_ERR_SHAPE;                          // key numbers are int32
+  if (static_cast<int64_t>(B) * Hq > (int64_t{1} << 31) / 16 - 1) return ATTN_ERR_SHAPE;
+  if (n_q > 16) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
 }  // namespace
 }  // namespace esd
 
@@ -862,6 +1004,7 @@ const char* attn_strerror(int status) {
     case ATTN_ERR_TIMEOUT: return "a kernel's bounded wait ran out";
     case ATTN_ERR_DEVICE: return "the current device is not an sm_103 GPU";
     case ATTN_ERR_RANGE: return "an input tile's magnitude (2^46 or more) was beyond the fp16 operands";
+    case ATTN_ERR_PAGE: return "a slot, page number or length reached past the 4-bit cache";
     default: return "unknown status";
   }
 }
@@ -1560,6 +1703,202 @@ int attn_bwd_varlen(const attn_varlen* v, const attn_strides* strides, const att
   e = launch_attn_bwd_finalize(d.total_q * v->Hq * v->d_h, v->d_h, v->Hq, d.lay.sdq.row, d.lay.sdq.head,
                                contiguous_strides(d.lay, d.lay.sdq, v->Hq, 0, v->d_h), scale, w.dQacc, dQ,
                                rotary ? &rq : nullptr, true, v->Hq, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Query/key norm and rotation over several axes; the 4-bit cache
+// ---------------------------------------------------------------------------
+int attn_rope_axes(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, const attn_rotary_axes* rotary,
+                   int32_t inverse, const attn_qk_strides* strides, const void* Xq, const void* Xk, void* Yq,
+                   void* Yk, void* stream) {
+  int rc = check_qk_dims(tokens, heads_q, heads_k, d);
+  if (rc) return rc;
+  if (!rotary) return ATTN_ERR_NULL;
+  rc = check_axes(rotary, d);
+  if (rc) return rc;
+  if (inverse != 0 && inverse != 1) return ATTN_ERR_SHAPE;
+  QkParams p{};
+  const int32_t heads[2] = {heads_q, heads_k};
+  const attn_tensor_strides* sx[2] = {strides ? &strides->q : nullptr, strides ? &strides->k : nullptr};
+  const attn_tensor_strides* sy[2] = {strides ? &strides->yq : nullptr, strides ? &strides->yk : nullptr};
+  for (int i = 0; i < 2; ++i) {
+    p.heads[i] = heads[i];
+    if ((rc = qk_strides(sx[i], heads[i], d, &p.sx[i]))) return rc;
+    if ((rc = qk_strides(sy[i], heads[i], d, &p.sy[i]))) return rc;
+  }
+  rc = check_qk_ptrs({Xq, Yq}, {Xk, Yk}, heads_k);
+  if (rc) return rc;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  p.tokens = tokens;
+  p.d = d;
+  p.x[0] = Xq;
+  p.x[1] = Xk;
+  p.y[0] = Yq;
+  p.y[1] = Yk;
+  p.inverse = inverse;
+  fill_axes(&p, rotary, d);
+  return launch_qk_fwd(p, false, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_qk_norm_rope(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, float eps,
+                      const attn_rotary_axes* rotary, const attn_qk_strides* strides, const void* Q, const void* K,
+                      const void* gq, const void* gk, void* Yq, void* Yk, void* stream) {
+  int rc = check_qk_dims(tokens, heads_q, heads_k, d);
+  if (rc) return rc;
+  rc = check_scale(eps);
+  if (rc) return rc;
+  rc = check_axes(rotary, d);
+  if (rc) return rc;
+  QkParams p{};
+  const int32_t heads[2] = {heads_q, heads_k};
+  const attn_tensor_strides* sx[2] = {strides ? &strides->q : nullptr, strides ? &strides->k : nullptr};
+  const attn_tensor_strides* sy[2] = {strides ? &strides->yq : nullptr, strides ? &strides->yk : nullptr};
+  for (int i = 0; i < 2; ++i) {
+    p.heads[i] = heads[i];
+    if ((rc = qk_strides(sx[i], heads[i], d, &p.sx[i]))) return rc;
+    if ((rc = qk_strides(sy[i], heads[i], d, &p.sy[i]))) return rc;
+  }
+  rc = check_qk_ptrs({Q, Yq}, {K, Yk}, heads_k);
+  if (rc) return rc;
+  if (!aligned16(gq) || !aligned16(gk)) return ATTN_ERR_ALIGN;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  p.tokens = tokens;
+  p.d = d;
+  p.eps = eps;
+  p.x[0] = Q;
+  p.x[1] = K;
+  p.y[0] = Yq;
+  p.y[1] = Yk;
+  p.g[0] = gq;
+  p.g[1] = gk;
+  fill_axes(&p, rotary, d);
+  return launch_qk_fwd(p, true, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d) {
+  if (check_qk_dims(tokens, heads_q, heads_k, d) != ATTN_OK) return 0;
+  return round256(static_cast<size_t>(2) * qk_bwd_blocks(tokens, heads_q, heads_k, d) * d * sizeof(float));
+}
+
+int attn_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, float eps,
+                          const attn_rotary_axes* rotary, const attn_qk_strides* strides, const void* Q, const void* K,
+                          const void* gq, const void* gk, const void* dYq, const void* dYk, void* dQ, void* dK,
+                          float* dgq, float* dgk, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_qk_dims(tokens, heads_q, heads_k, d);
+  if (rc) return rc;
+  rc = check_scale(eps);
+  if (rc) return rc;
+  rc = check_axes(rotary, d);
+  if (rc) return rc;
+  QkParams p{};
+  const int32_t heads[2] = {heads_q, heads_k};
+  const attn_tensor_strides* sx[2] = {strides ? &strides->q : nullptr, strides ? &strides->k : nullptr};
+  const attn_tensor_strides* sdy[2] = {strides ? &strides->dyq : nullptr, strides ? &strides->dyk : nullptr};
+  const attn_tensor_strides* sy[2] = {strides ? &strides->dq : nullptr, strides ? &strides->dk : nullptr};
+  for (int i = 0; i < 2; ++i) {
+    p.heads[i] = heads[i];
+    if ((rc = qk_strides(sx[i], heads[i], d, &p.sx[i]))) return rc;
+    if ((rc = qk_strides(sdy[i], heads[i], d, &p.sdy[i]))) return rc;
+    if ((rc = qk_strides(sy[i], heads[i], d, &p.sy[i]))) return rc;
+  }
+  rc = check_qk_ptrs({Q, dYq, dQ}, {K, dYk, dK}, heads_k);
+  if (rc) return rc;
+  if ((dgq && !gq) || (dgk && (!gk || heads_k == 0))) return ATTN_ERR_NULL;
+  if (!aligned16(gq) || !aligned16(gk) || !aligned16(dgq) || !aligned16(dgk)) return ATTN_ERR_ALIGN;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(tokens, heads_q, heads_k, d))
+    return ATTN_ERR_WORKSPACE;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  p.tokens = tokens;
+  p.d = d;
+  p.eps = eps;
+  p.x[0] = Q;
+  p.x[1] = K;
+  p.dy[0] = dYq;
+  p.dy[1] = dYk;
+  p.y[0] = dQ;
+  p.y[1] = dK;
+  p.g[0] = gq;
+  p.g[1] = gk;
+  p.partial = static_cast<float*>(workspace);
+  fill_axes(&p, rotary, d);
+  return launch_qk_bwd(p, dgq, dgk, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_cache_page_bytes(int32_t Hkv, int32_t d_h, int32_t d_v) {
+  if (Hkv <= 0 || Hkv > 65535 || !supported_dims(d_h, d_v)) return 0;
+  return static_cast<size_t>(Hkv) * page_head_bytes(d_h, d_v);
+}
+
+int attn_cache_append(const attn_cache* cache, int64_t tokens, const attn_strides* strides, const int64_t* slots,
+                      const void* K, const void* V, void* stream) {
+  return cache_io(cache, tokens, strides, slots, K, V, true, stream);
+}
+
+int attn_cache_read(const attn_cache* cache, int64_t tokens, const attn_strides* strides, const int64_t* slots,
+                    void* K, void* V, void* stream) {
+  return cache_io(cache, tokens, strides, slots, K, V, false, stream);
+}
+
+size_t attn_fwd_decode_cache_workspace_bytes(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q,
+                                             int32_t max_pages) {
+  if (check_decode_cache(cache, B, Hq, n_q, max_pages) != ATTN_OK) return 0;
+  return decode_cache_plan(cache, B, Hq, n_q, max_pages).bytes;
+}
+
+int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q, int32_t max_pages, float scale,
+                          const void* Q, const int32_t* page_table, const int32_t* lengths, void* O, float* LSE,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_decode_cache(cache, B, Hq, n_q, max_pages);
+  if (rc) return rc;
+  rc = check_scale(scale);
+  if (rc) return rc;
+  rc = check_ptrs({cache->pool, Q, O, LSE});
+  if (rc) return rc;
+  if (!page_table || !lengths) return ATTN_ERR_NULL;
+  if (((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(lengths)) & 3u) != 0)
+    return ATTN_ERR_ALIGN;
+  const DecodeCachePlan plan = decode_cache_plan(cache, B, Hq, n_q, max_pages);
+  if (plan.bytes > 0 &&
+      (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.bytes))
+    return ATTN_ERR_WORKSPACE;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  DecCacheParams p;
+  p.B = B;
+  p.Hkv = cache->Hkv;
+  p.group = Hq / cache->Hkv;
+  p.n_q = n_q;
+  p.max_pages = max_pages;
+  p.pages = cache->pages;
+  p.pool = static_cast<const uint8_t*>(cache->pool);
+  p.table = page_table;
+  p.lengths = lengths;
+  p.scale_log2 = scale * kLog2e;
+  p.wait_limit_ns = kDefaultWaitLimitNs;
+  p.Q = Q;
+  p.O = O;
+  p.LSE = LSE;
+  p.Opart = plan.bytes > 0 ? static_cast<float*>(workspace) : nullptr;
+  p.Lpart = plan.bytes > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.opart_bytes) : nullptr;
+  p.tile_rows = plan.tile_rows;
+  p.chunks = plan.chunks;
+  p.split_pages = plan.split_pages;
+  p.splits = plan.splits;
+  p.status = status;
+  const cudaError_t e = launch_decode_cache(cache->d_h, cache->d_v, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -310,6 +310,62 @@ struct GemmParams {
   unsigned int* status;
 };
 
+// Query and key rows normalised and rotated (qk_norm.cu): tensors 0 (queries)
+// and 1 (keys; heads[1] = 0: none) share tokens, width and positions.
+constexpr int kMaxAxes = ATTN_MAX_AXES;
+struct QkParams {
+  int64_t tokens;
+  int32_t d;                   // row width, a multiple of 8
+  int32_t heads[2];
+  const void* x[2];            // bf16 rows
+  const void* dy[2];           // backward: upstream gradients
+  void* y[2];                  // forward: results; backward: dx
+  TensorStrides sx[2], sdy[2], sy[2];   // row = between tokens
+  const void* g[2];            // bf16 weights [d], or nullptr (ones)
+  float eps;
+  int32_t inverse;             // rotation alone: by -a
+  int32_t axes;                // position axes (0: no rotation)
+  const int32_t* pos;          // [axes][tokens]
+  float* partial;              // backward: [2][blocks][d] shares of the weight gradients
+  float w_hi[64], w_lo[64];    // frequency of each block (0 past the sections), as in RotaryAngles
+  uint8_t axis[64];            // axis of each block
+};
+
+// Tokens written to or read from the 4-bit cache (quant_cache.cuh).
+struct CacheIoParams {
+  int64_t tokens;
+  int32_t Hkv, dh, dv;
+  int64_t pages;
+  uint8_t* pool;
+  const int64_t* slots;        // [tokens] page * 32 + place in the page; negative: no token
+  const void* K;               // bf16 rows (the read's outputs)
+  const void* V;
+  TensorStrides sk, sv;
+  unsigned int* status;
+};
+
+// Attention over the 4-bit cache (decode_cache.cu).
+struct DecCacheParams {
+  int32_t B, Hkv, group, n_q;
+  int32_t max_pages;           // row length of the page table
+  int64_t pages;
+  const uint8_t* pool;
+  const int32_t* table;        // [B][max_pages]
+  const int32_t* lengths;      // [B]
+  float scale_log2;            // scale * log2(e)
+  uint64_t wait_limit_ns;
+  const void* Q;               // bf16 [B][Hq][n_q][d_h]
+  void* O;                     // bf16 [B][Hq][n_q][d_v]
+  float* LSE;                  // fp32 [B][Hq][n_q]
+  float* Opart;                // fp32 [splits][B Hq n_q][d_v] (splits > 1)
+  float* Lpart;                // fp32 [splits][B Hq n_q]
+  int32_t tile_rows;           // query rows of one CTA: 8 or 16
+  int32_t chunks;              // row tiles per KV head
+  int32_t split_pages;         // pages of one CTA
+  int32_t splits;              // ranges of a sequence of max_pages pages
+  unsigned int* status;
+};
+
 // Default limit of every bounded wait inside the kernels.
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s
 
@@ -340,6 +396,14 @@ cudaError_t launch_rope_prep(const RopePrepParams& p, cudaStream_t stream);
 // heads_b = 0: one tensor (xb, yb unused).
 cudaError_t launch_rope(int64_t tokens, int d, int heads_a, int heads_b, const int32_t* pos, const float* w_hi,
                         const float* w_lo, int inverse, const void* xa, void* ya, const void* xb, void* yb, cudaStream_t stream);
+// norm: RMS norm before the rotation; else the rotation alone.
+cudaError_t launch_qk_fwd(const QkParams& p, bool norm, cudaStream_t stream);
+// Blocks of the backward, the number of partial weight gradients per tensor.
+int qk_bwd_blocks(int64_t tokens, int heads_q, int heads_k, int d);
+cudaError_t launch_qk_bwd(const QkParams& p, float* dgq, float* dgk, cudaStream_t stream);
+cudaError_t launch_cache_append(const CacheIoParams& p, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheIoParams& p, cudaStream_t stream);
+cudaError_t launch_decode_cache(int dh, int dv, const DecCacheParams& p, cudaStream_t stream);
 // Zero n floats (n a multiple of 4, 16-byte aligned).
 cudaError_t launch_zero_f32(float* p, int64_t n, cudaStream_t stream);
 // dK, dV (bf16, caller strides) from the fp32 sums of a query-head split:

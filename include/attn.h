@@ -58,7 +58,9 @@
  * ATTN_ERR_TIMEOUT (a bounded wait ran out; while it is set, the kernels
  * return immediately without writing outputs) or ATTN_ERR_RANGE (an input
  * tile was too large for the fp16 operands, below; the outputs of that call
- * are not to be trusted, later calls run normally).
+ * are not to be trusted, later calls run normally), or ATTN_ERR_PAGE (an
+ * index of the 4-bit cache was out of range and left out; later calls run
+ * normally).
  *
  * Precision.  Inputs and outputs are bf16 with fp32 accumulation.  Q K^T in
  * the forward runs on bf16 operands; P V and every backward product run on
@@ -102,6 +104,14 @@ extern "C" {
 #define ATTN_ERR_DEVICE      10  /* the current device is not an sm_103 GPU            */
 #define ATTN_ERR_RANGE       11  /* an input tile held a magnitude of 2^46 or more,    */
                                  /* beyond the scaled fp16 operands (device status)    */
+#define ATTN_ERR_PAGE        12  /* a slot, page number or length reached past the     */
+                                 /* 4-bit cache's pool or page table (device status)   */
+
+/* Most position axes of one rotation (time, height, width). */
+#define ATTN_MAX_AXES 3
+
+/* Tokens in a page of the 4-bit cache. */
+#define ATTN_CACHE_PAGE_TOKENS 32
 
 /* Largest batch whose per-batch key lengths travel with the launch. */
 #define ATTN_MAX_BATCH 512
@@ -473,6 +483,132 @@ int attn_rope(int64_t tokens, int32_t heads, int32_t d, float base, const int32_
 int attn_rope_qk(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, float base,
                  const int32_t* positions, int32_t inverse, const void* Xq, void* Yq, const void* Xk, void* Yk,
                  void* stream);
+
+/* Rotary position embedding with several position axes (time, height and
+ * width of image and video tokens).  The d/2 blocks (x_2k, x_2k+1) of a row
+ * are divided into `axes` consecutive sections of sections[a] blocks; a block
+ * k of section a turns by pos[a][token] w_k.  restart = 0: the sections share
+ * one row of frequencies, w_k = base^(-2k/d); restart = 1: every section has
+ * its own, w_k = base^(-(k - first)/sections[a]) from its first block on.
+ * Blocks past the last section keep their value (a rotation of part of the
+ * width).  One section of d/2 blocks is attn_rope's rotation.
+ * pos: device int32 [axes][tokens], |pos| < 2^24; base finite and > 1. */
+typedef struct {
+  float base;
+  int32_t axes;                      /* 1..ATTN_MAX_AXES                              */
+  int32_t sections[ATTN_MAX_AXES];   /* blocks of each axis, >= 1, sum <= d/2         */
+  int32_t restart;                   /* 0 or 1                                        */
+  const int32_t* pos;                /* DEVICE [axes][tokens]                         */
+} attn_rotary_axes;
+
+/* Strides of the tensors of the calls below, all token-major [tokens][heads][d]
+ * (row = between tokens, head = between heads; the rules of attn_strides).
+ * q, k: the rows; yq, yk: the results; dyq, dyk: their gradients; dq, dk: the
+ * rows' gradients.  {0, 0}, or NULL for the struct: contiguous. */
+typedef struct {
+  attn_tensor_strides q, k, yq, yk, dyq, dyk, dq, dk;
+} attn_qk_strides;
+
+/* The rotation alone, of queries Xq [tokens][heads_q][d] and keys
+ * Xk [tokens][heads_k][d] (heads_k = 0 and Xk = Yk = NULL: queries only), in
+ * one launch.  inverse = 1 turns back by the opposite angles, which maps the
+ * gradients of rotated rows to those of the rows.  bf16; d a multiple of 8
+ * and <= 128.  Y may be X with the same strides; no other overlap.  With one
+ * section of d/2 blocks the results are attn_rope_qk's, bit for bit.
+ * Uses strides q, k, yq, yk. */
+int attn_rope_axes(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, const attn_rotary_axes* rotary,
+                   int32_t inverse, const attn_qk_strides* strides, const void* Xq, const void* Xk, void* Yq,
+                   void* Yk, void* stream);
+
+/* RMS norm of every query and key row over its width, then the rotation, in
+ * one pass: n = x / sqrt(mean(x^2) + eps), y = R(n o g).  gq, gk: bf16 [d]
+ * weights shared by the heads, or NULL (ones).  rotary NULL: no rotation.
+ * eps finite and > 0 (ATTN_ERR_SCALE).  Sums and products in fp32, one
+ * rounding to bf16; x^2 must stay in fp32's range (|x| < 2^60).  heads_k = 0
+ * and K = Yk = NULL: queries only.  Y may be X with the same strides.  Uses
+ * strides q, k, yq, yk. */
+int attn_qk_norm_rope(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, float eps,
+                      const attn_rotary_axes* rotary, const attn_qk_strides* strides, const void* Q, const void* K,
+                      const void* gq, const void* gk, void* Yq, void* Yk, void* stream);
+
+/* Bytes of workspace of attn_qk_norm_rope_bwd (at most 0.6 MB); 0 for invalid sizes. */
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d);
+
+/* Gradients of attn_qk_norm_rope: dQ, dK (bf16, like Q and K) and the weight
+ * gradients dgq, dgk (fp32 [d], summed over tokens and heads in a fixed order;
+ * NULL to skip, and required to be NULL where the weight or the tensor is).
+ * Q, K, gq, gk, eps and rotary are the forward's; dYq, dYk (bf16) the
+ * upstream gradients.  dQ may be Q or dYq with the same strides (likewise
+ * dK).  `workspace`: device memory, 256-byte aligned.  Uses strides q, k,
+ * dyq, dyk, dq, dk. */
+int attn_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, float eps,
+                          const attn_rotary_axes* rotary, const attn_qk_strides* strides, const void* Q, const void* K,
+                          const void* gq, const void* gk, const void* dYq, const void* dYk, void* dQ, void* dK,
+                          float* dgq, float* dgk, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A key/value cache held in 4 bits, in pages of ATTN_CACHE_PAGE_TOKENS tokens.
+ * pool: device bytes [pages][Hkv][block], 16-byte aligned, owned by the caller; the block of
+ * one page and head holds, in this order,
+ *   K codes [32][d_h / 2], V codes [32][d_v / 2],
+ *   K words [32][d_h / 64], V words [32][d_v / 64]  (32 bits each).
+ * Byte i of a row of codes has element 2i in its low and 2i + 1 in its high
+ * half.  The word of a group of 64 elements has its scale s (bf16) in the
+ * upper 16 bits and its zero point z in the lowest byte (0..15); an element
+ * stands for s (code - z).  attn_cache_append writes, for a group with
+ * lo = min(0, min x) and hi = max(0, max x):
+ *   s = bf16((hi - lo) / 15), z = min(15, rint(-lo / s)),
+ *   code = clamp(rint(x / s) + z, 0, 15)        (s = 0: codes and z are 0)
+ * in fp32, so that an element is off by at most about s / 2 (s where z's
+ * rounding and that of the range's end meet).  Inputs are finite, |x| < 2^126.
+ * The pool's contents need no initialisation: only the tokens that a call
+ * names are read. */
+typedef struct {
+  int32_t Hkv;      /* key/value heads                                     */
+  int32_t d_h;      /* key width; (d_h, d_v) as for attention              */
+  int32_t d_v;      /* value width                                         */
+  int64_t pages;    /* pages of the pool, 1..2^31 - 1                      */
+  void* pool;       /* DEVICE                                              */
+} attn_cache;
+
+/* Bytes of one page over all heads; 0 for invalid sizes. */
+size_t attn_cache_page_bytes(int32_t Hkv, int32_t d_h, int32_t d_v);
+
+/* Write `tokens` new tokens, K [tokens][Hkv][d_h] and V [tokens][Hkv][d_v]
+ * (bf16; strides k and v of `strides`, packed layout, or NULL), into the slots
+ * slots[i] = page * 32 + place (device int64 [tokens]).  A negative slot
+ * skips its token (padding); one past the pool skips it and records
+ * ATTN_ERR_PAGE in the status word.  The slots of one call are distinct: a
+ * slot named twice is left with a mixture of its tokens. */
+int attn_cache_append(const attn_cache* cache, int64_t tokens, const attn_strides* strides, const int64_t* slots,
+                      const void* K, const void* V, void* stream);
+
+/* Read the tokens of slots[i] back, as the values they stand for rounded to
+ * bf16, into K [tokens][Hkv][d_h] and V [tokens][Hkv][d_v] (for a prefill
+ * over a cached history, and to see what later calls will attend to).
+ * Negative slots give zeros, slots past the pool zeros and ATTN_ERR_PAGE.
+ * Slots may repeat. */
+int attn_cache_read(const attn_cache* cache, int64_t tokens, const attn_strides* strides, const int64_t* slots,
+                    void* K, void* V, void* stream);
+
+/* attn_fwd_decode over the 4-bit cache: Q [B][Hq][n_q][d_h] (bf16), n_q <= 16
+ * (ATTN_ERR_UNSUPPORTED above: read the history back and use attn_fwd), to
+ * O [B][Hq][n_q][d_v] (bf16) and LSE [B][Hq][n_q] (fp32, natural log), all
+ * contiguous and fully overwritten.  Sequence b has lengths[b] keys (the
+ * n_q new tokens among them), key j in page page_table[b][j / 32] at place
+ * j % 32; row i sees j <= lengths[b] - n_q + i.  page_table: device int32
+ * [B][max_pages]; lengths: device int32 [B]; both are read when the call
+ * runs, so that a captured call follows them.  Since the host does not see
+ * them, a row without a visible key is not refused: its O is 0 and its LSE
+ * -inf (a sequence of length 0, or rows before its first token).  A page
+ * number outside the pool leaves that page's keys out, and a length above
+ * 32 max_pages is cut; both record ATTN_ERR_PAGE in the status word.
+ * `workspace`: attn_fwd_decode_cache_workspace_bytes() bytes, 256-byte
+ * aligned (may be NULL when that is 0); it depends on the sizes only. */
+size_t attn_fwd_decode_cache_workspace_bytes(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q,
+                                             int32_t max_pages);
+int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q, int32_t max_pages, float scale,
+                          const void* Q, const int32_t* page_table, const int32_t* lengths, void* O, float* LSE,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* Device status word of the current device: ATTN_OK, or the first failure a
  * kernel recorded (ATTN_ERR_TIMEOUT).  Synchronises the device.  Writes the

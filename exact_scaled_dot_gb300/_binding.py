@@ -13,8 +13,8 @@ decode forward takes contiguous tensors only.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from pathlib import Path
 from typing import Optional, Sequence, Tuple, Union
@@ -310,8 +310,9 @@ def _padded_strides(t: torch.Tensor, name: str) -> Tuple[int, int]:
 
 def _packed_strides(t: torch.Tensor) -> Tuple[int, int]:
     """(row = token, head) element strides of a [T, H, d] view."""
-    T, H, d = (int(x) for x in t.shape)
-    return (int(t.stride(0)) if T > 1 else H * d), (int(t.stride(1)) if H > 1 else d)
+    T, H, d = t.shape
+    row, head, _ = t.stride()
+    return (row if T > 1 else H * d), (head if H > 1 else d)
 
 
 def _strides_arg(packed: bool, **tensors):
@@ -871,34 +872,52 @@ class RotaryAxes:
         n = len(sections)
         if not 1 <= n <= ATTN_MAX_AXES:
             raise ValueError(f"sections must name 1 to {ATTN_MAX_AXES} axes")
-        _check_tensor(pos, "positions", torch.int32, (tokens,) if n == 1 and pos.dim() == 1 else (n, tokens), device)
+        _check_flat(pos, "positions", torch.int32, (tokens,) if n == 1 and pos.dim() == 1 else (n, tokens), device)
         r = AttnRotaryAxes(self.base, n, (ctypes.c_int32 * ATTN_MAX_AXES)(*sections), 1 if self.restart else 0,
                            pos.data_ptr())
         return ctypes.byref(r)
 
 
-def _scope(dev, stream):
-    """Where a call allocates and launches: on the caller's stream (so that the
-    allocator ties outputs and workspaces created here to the work that uses
-    them), and on the tensors' device, which need not be the current one."""
-    if not dev.type == "cuda":
-        raise ValueError(f"CUDA tensors are required, got {dev}")
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+def _launch(dev, stream, body):
+    """body(stream handle) with its allocations and launches on the caller's
+    stream (so that the allocator ties the outputs and workspaces made here to
+    the work that uses them) and on the tensors' device, which need not be the
+    current one.  The common case, neither differing from the current ones,
+    enters no context: these calls may take less time on the GPU than that."""
+    if stream is None:
+        if dev.index == torch._C._cuda_getDevice():
+            return body(torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(dev):
+            return body(torch._C._cuda_getCurrentRawStream(dev.index))
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _check_rows(t, name, shape, dev):
     """A token-major bf16 view [tokens, heads, d] with contiguous rows."""
-    _check_tensor(t, name, torch.bfloat16, shape, dev, strided=True)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.bfloat16 and t.shape == shape
+            and t.device == dev and t.stride(2) == 1):
+        _check_tensor(t, name, torch.bfloat16, shape, dev, strided=True)
+    return t
+
+
+def _check_flat(t, name, dtype, shape, dev):
+    """A contiguous tensor."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _check_tensor(t, name, dtype, shape, dev)
     return t
 
 
 def _qk_dims(Q, K):
     if Q.dim() != 3 or (K is not None and K.dim() != 3):
         raise ValueError("Q and K must be 3-D [tokens, heads, d]")
-    T, Hq, d = (int(x) for x in Q.shape)
-    Hk = 0 if K is None else int(K.shape[1])
+    T, Hq, d = Q.shape
+    Hk = 0 if K is None else K.shape[1]
     dev = Q.device
     _check_rows(Q, "Q", (T, Hq, d), dev)
     if K is not None:
@@ -906,16 +925,30 @@ def _qk_dims(Q, K):
     return T, Hq, Hk, d, dev
 
 
-def _qk_strides(**tensors):
-    """attn_qk_strides of the given token-major tensors, or None when all are contiguous."""
-    st = None
-    for field, t in tensors.items():
-        if t is None or t.is_contiguous():
-            continue
-        if st is None:
-            st = AttnQkStrides()
-        setattr(st, field, AttnTensorStrides(*_packed_strides(t)))
-    return None if st is None else ctypes.byref(st)
+@functools.lru_cache(maxsize=256)
+def _stride_struct(cls, fields, strides):
+    """A reference to the stride struct `cls` with these (row, head) pairs (None: contiguous)."""
+    st = cls()
+    for field, pair in zip(fields, strides):
+        if pair is not None:
+            setattr(st, field, AttnTensorStrides(*pair))
+    return ctypes.byref(st)
+
+
+def _stride_arg(cls, fields, *tensors):
+    """The stride struct of token-major tensors, or None when all are contiguous."""
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            break
+    else:
+        return None
+    return _stride_struct(cls, fields, tuple([None if t is None or t.is_contiguous() else _packed_strides(t)
+                                              for t in tensors]))
+
+
+_FWD_FIELDS = ("q", "k", "yq", "yk")
+_BWD_FIELDS = ("q", "k", "dyq", "dyk", "dq", "dk")
+_KV_FIELDS = ("k", "v")
 
 
 def _rows_like(Y, name, like, dev):
@@ -925,15 +958,15 @@ def _rows_like(Y, name, like, dev):
             raise ValueError(f"{name} was given without its input")
         return None
     if Y is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=dev)
-    return _check_rows(Y, name, tuple(like.shape), dev)
+        return torch.empty(like.shape, dtype=torch.bfloat16, device=dev)
+    return _check_rows(Y, name, like.shape, dev)
 
 
 def _check_weight(g, name, d, dev, rows):
     if g is not None:
         if rows is None:
             raise ValueError(f"{name} was given without its rows")
-        _check_tensor(g, name, torch.bfloat16, (d,), dev)
+        _check_flat(g, name, torch.bfloat16, (d,), dev)
 
 
 def _weight_grad(t, name, g, d, dev):
@@ -943,8 +976,7 @@ def _weight_grad(t, name, g, d, dev):
         return None
     if t is None:
         return torch.empty((d,), dtype=torch.float32, device=dev)
-    _check_tensor(t, name, torch.float32, (d,), dev)
-    return t
+    return _check_flat(t, name, torch.float32, (d,), dev)
 
 
 def attn_rope_axes(Q, K, rotary: RotaryAxes, *, inverse: bool = False, Yq=None, Yk=None, stream=None):
@@ -953,13 +985,15 @@ def attn_rope_axes(Q, K, rotary: RotaryAxes, *, inverse: bool = False, Yq=None, 
     inverse=True turns back (the gradient map).  Views with contiguous rows
     are read and written in place; Yq may be Q and Yk may be K."""
     T, Hq, Hk, d, dev = _qk_dims(Q, K)
-    with _scope(dev, stream):
-        Yq, Yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
-        rc = load().attn_rope_axes(T, Hq, Hk, d, rotary.arg(T, d, dev), 1 if inverse else 0,
-                                   _qk_strides(q=Q, k=K, yq=Yq, yk=Yk), _ptr(Q), _ptr(K), _ptr(Yq), _ptr(Yk),
-                                   _stream(dev, stream))
-    _check(rc, "attn_rope_axes")
-    return Yq, Yk
+
+    def body(st):
+        yq, yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
+        _check(load().attn_rope_axes(T, Hq, Hk, d, rotary.arg(T, d, dev), 1 if inverse else 0,
+                                     _stride_arg(AttnQkStrides, _FWD_FIELDS, Q, K, yq, yk), _addr(Q), _addr(K),
+                                     _addr(yq), _addr(yk), st), "attn_rope_axes")
+        return yq, yk
+
+    return _launch(dev, stream, body)
 
 
 def attn_qk_norm_rope(Q, K, gq=None, gk=None, rotary: Optional[RotaryAxes] = None, *, eps: float = 1e-6, Yq=None,
@@ -970,13 +1004,15 @@ def attn_qk_norm_rope(Q, K, gq=None, gk=None, rotary: Optional[RotaryAxes] = Non
     T, Hq, Hk, d, dev = _qk_dims(Q, K)
     _check_weight(gq, "gq", d, dev, Q)
     _check_weight(gk, "gk", d, dev, K)
-    with _scope(dev, stream):
-        Yq, Yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
-        rc = load().attn_qk_norm_rope(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
-                                      _qk_strides(q=Q, k=K, yq=Yq, yk=Yk), _ptr(Q), _ptr(K), _ptr(gq), _ptr(gk),
-                                      _ptr(Yq), _ptr(Yk), _stream(dev, stream))
-    _check(rc, "attn_qk_norm_rope")
-    return Yq, Yk
+
+    def body(st):
+        yq, yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
+        _check(load().attn_qk_norm_rope(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
+                                        _stride_arg(AttnQkStrides, _FWD_FIELDS, Q, K, yq, yk), _addr(Q), _addr(K),
+                                        _addr(gq), _addr(gk), _addr(yq), _addr(yk), st), "attn_qk_norm_rope")
+        return yq, yk
+
+    return _launch(dev, stream, body)
 
 
 def attn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hkv, d) -> int:
@@ -996,19 +1032,23 @@ def attn_qk_norm_rope_bwd(Q, K, gq, gk, dYq, dYk, rotary: Optional[RotaryAxes] =
         _check_rows(dYk, "dYk", (T, Hk, d), dev)
     elif dYk is not None:
         raise ValueError("dYk was given without its input")
-    lib = load()
-    with _scope(dev, stream):
-        dQ, dK = _rows_like(dQ, "dQ", Q, dev), _rows_like(dK, "dK", K, dev)
-        dgq, dgk = (_weight_grad(t, name, g, d, dev) for t, name, g in ((dgq, "dgq", gq), (dgk, "dgk", gk)))
-        if workspace is None:
-            need = int(lib.attn_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d))
-            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
-        rc = lib.attn_qk_norm_rope_bwd(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
-                                       _qk_strides(q=Q, k=K, dyq=dYq, dyk=dYk, dq=dQ, dk=dK), _ptr(Q), _ptr(K),
-                                       _ptr(gq), _ptr(gk), _ptr(dYq), _ptr(dYk), _ptr(dQ), _ptr(dK), _ptr(dgq),
-                                       _ptr(dgk), *_ws(workspace), _stream(dev, stream))
-    _check(rc, "attn_qk_norm_rope_bwd")
-    return dQ, dK, dgq, dgk
+
+    def body(st):
+        lib = load()
+        dq, dk = _rows_like(dQ, "dQ", Q, dev), _rows_like(dK, "dK", K, dev)
+        wq, wk = _weight_grad(dgq, "dgq", gq, d, dev), _weight_grad(dgk, "dgk", gk, d, dev)
+        ws = workspace
+        if ws is None:
+            need = lib.attn_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d)
+            ws = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+        _check(lib.attn_qk_norm_rope_bwd(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
+                                         _stride_arg(AttnQkStrides, _BWD_FIELDS, Q, K, dYq, dYk, dq, dk), _addr(Q),
+                                         _addr(K), _addr(gq), _addr(gk), _addr(dYq), _addr(dYk), _addr(dq), _addr(dk),
+                                         _addr(wq), _addr(wk), ws.data_ptr(), ws.numel() * ws.element_size(), st),
+               "attn_qk_norm_rope_bwd")
+        return dq, dk, wq, wk
+
+    return _launch(dev, stream, body)
 
 
 # ---------------------------------------------------------------------------
@@ -1024,9 +1064,9 @@ class QuantCache:
         if not isinstance(pool, torch.Tensor) or pool.dim() != 3:
             raise ValueError("pool must be a [pages, Hkv, block] tensor")
         self.pool, self.d_h, self.d_v = pool, int(d_h), int(d_v)
-        self.pages, self.Hkv, block = (int(x) for x in pool.shape)
+        self.pages, self.Hkv, block = pool.shape
         self.device = pool.device
-        _check_tensor(pool, "pool", torch.uint8, tuple(pool.shape), pool.device)
+        _check_flat(pool, "pool", torch.uint8, pool.shape, pool.device)
         # Bytes of one page of one head: codes and a 32-bit word per 64 elements.
         want = ATTN_CACHE_PAGE_TOKENS * (self.d_h + self.d_v) * 9 // 16
         if block != want:
@@ -1049,25 +1089,21 @@ def attn_cache_page_bytes(Hkv, d_h, d_v) -> int:
     return int(load().attn_cache_page_bytes(int(Hkv), int(d_h), int(d_v)))
 
 
-def _cache_strides(K, V):
-    if K.is_contiguous() and V.is_contiguous():
-        return None
-    return _strides_arg(True, k=K, v=V)
-
-
 def attn_cache_append(cache: QuantCache, K, V, slots, *, stream=None) -> None:
     """Write new tokens K [tokens, Hkv, d_h], V [tokens, Hkv, d_v] (bf16) into
     the cache, rounded to 4 bits: token i into slots[i] = page * 32 + place
     (int64, device; negative: skipped).  The slots of a call are distinct."""
     dev = cache.device
-    T = int(K.shape[0]) if K.dim() == 3 else -1
+    T = K.shape[0]
     _check_rows(K, "K", (T, cache.Hkv, cache.d_h), dev)
     _check_rows(V, "V", (T, cache.Hkv, cache.d_v), dev)
-    _check_tensor(slots, "slots", torch.int64, (T,), dev)
-    with _scope(dev, stream):
-        rc = load().attn_cache_append(cache.arg(), T, _cache_strides(K, V), _ptr(slots), _ptr(K), _ptr(V),
-                                      _stream(dev, stream))
-    _check(rc, "attn_cache_append")
+    _check_flat(slots, "slots", torch.int64, (T,), dev)
+
+    def body(st):
+        _check(load().attn_cache_append(cache.arg(), T, _stride_arg(AttnStrides, _KV_FIELDS, K, V), slots.data_ptr(),
+                                        K.data_ptr(), V.data_ptr(), st), "attn_cache_append")
+
+    _launch(dev, stream, body)
 
 
 def attn_cache_read(cache: QuantCache, slots, *, K=None, V=None, stream=None):
@@ -1075,16 +1111,18 @@ def attn_cache_read(cache: QuantCache, slots, *, K=None, V=None, stream=None):
     rounded to bf16: returns (K [tokens, Hkv, d_h], V [tokens, Hkv, d_v]);
     negative slots give zeros."""
     dev = cache.device
-    T = int(slots.shape[0]) if slots.dim() == 1 else -1
-    _check_tensor(slots, "slots", torch.int64, (T,), dev)
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    _check_flat(slots, "slots", torch.int64, (T,), dev)
     ks, vs = (T, cache.Hkv, cache.d_h), (T, cache.Hkv, cache.d_v)
-    with _scope(dev, stream):
-        K = torch.empty(ks, dtype=torch.bfloat16, device=dev) if K is None else _check_rows(K, "K", ks, dev)
-        V = torch.empty(vs, dtype=torch.bfloat16, device=dev) if V is None else _check_rows(V, "V", vs, dev)
-        rc = load().attn_cache_read(cache.arg(), T, _cache_strides(K, V), _ptr(slots), _ptr(K), _ptr(V),
-                                    _stream(dev, stream))
-    _check(rc, "attn_cache_read")
-    return K, V
+
+    def body(st):
+        k = torch.empty(ks, dtype=torch.bfloat16, device=dev) if K is None else _check_rows(K, "K", ks, dev)
+        v = torch.empty(vs, dtype=torch.bfloat16, device=dev) if V is None else _check_rows(V, "V", vs, dev)
+        _check(load().attn_cache_read(cache.arg(), T, _stride_arg(AttnStrides, _KV_FIELDS, k, v), slots.data_ptr(),
+                                      k.data_ptr(), v.data_ptr(), st), "attn_cache_read")
+        return k, v
+
+    return _launch(dev, stream, body)
 
 
 def attn_fwd_decode_cache_workspace_bytes(cache: QuantCache, B, Hq, n_q, max_pages) -> int:
@@ -1100,28 +1138,29 @@ def attn_fwd_decode_cache(Q, cache: QuantCache, page_table, lengths, *, scale: O
     Returns (O [B, Hq, n_q, d_v] bf16, LSE [B, Hq, n_q] fp32)."""
     if Q.dim() != 4 or page_table.dim() != 2:
         raise ValueError("Q must be 4-D [B, Hq, n_q, d_h] and page_table 2-D [B, max_pages]")
-    B, Hq, n_q, d_h = (int(x) for x in Q.shape)
+    B, Hq, n_q, d_h = Q.shape
     dev = cache.device
-    max_pages = int(page_table.shape[1])
-    _check_tensor(Q, "Q", torch.bfloat16, (B, Hq, n_q, cache.d_h), dev)
-    _check_tensor(page_table, "page_table", torch.int32, (B, max_pages), dev)
-    _check_tensor(lengths, "lengths", torch.int32, (B,), dev)
+    max_pages = page_table.shape[1]
+    _check_flat(Q, "Q", torch.bfloat16, (B, Hq, n_q, cache.d_h), dev)
+    _check_flat(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    _check_flat(lengths, "lengths", torch.int32, (B,), dev)
     scale = 1.0 / math.sqrt(d_h) if scale is None else float(scale)
-    lib = load()
-    with _scope(dev, stream):
-        if O is None:
-            O = torch.empty((B, Hq, n_q, cache.d_v), dtype=torch.bfloat16, device=dev)
+    os, ls = (B, Hq, n_q, cache.d_v), (B, Hq, n_q)
+
+    def body(st):
+        lib = load()
+        o = torch.empty(os, dtype=torch.bfloat16, device=dev) if O is None else _check_flat(O, "O", torch.bfloat16, os, dev)
+        lse = torch.empty(ls, dtype=torch.float32, device=dev) if LSE is None else _check_flat(LSE, "LSE", torch.float32,
+                                                                                             ls, dev)
+        ws, size = workspace, 0
+        if ws is None:
+            size = lib.attn_fwd_decode_cache_workspace_bytes(cache.arg(), B, Hq, n_q, max_pages)
+            ws = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
         else:
-            _check_tensor(O, "O", torch.bfloat16, (B, Hq, n_q, cache.d_v), dev)
-        if LSE is None:
-            LSE = torch.empty((B, Hq, n_q), dtype=torch.float32, device=dev)
-        else:
-            _check_tensor(LSE, "LSE", torch.float32, (B, Hq, n_q), dev)
-        if workspace is None:
-            need = int(lib.attn_fwd_decode_cache_workspace_bytes(cache.arg(), B, Hq, n_q, max_pages))
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-        ws_ptr, ws_bytes = (_ws(workspace) if workspace is not None else (None, ctypes.c_size_t(0)))
-        rc = lib.attn_fwd_decode_cache(cache.arg(), B, Hq, n_q, max_pages, scale, _ptr(Q), _ptr(page_table),
-                                       _ptr(lengths), _ptr(O), _ptr(LSE), ws_ptr, ws_bytes, _stream(dev, stream))
-    _check(rc, "attn_fwd_decode_cache")
-    return O, LSE
+            size = ws.numel() * ws.element_size()
+        _check(lib.attn_fwd_decode_cache(cache.arg(), B, Hq, n_q, max_pages, scale, Q.data_ptr(),
+                                         page_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                         _addr(ws), size, st), "attn_fwd_decode_cache")
+        return o, lse
+
+    return _launch(dev, stream, body)

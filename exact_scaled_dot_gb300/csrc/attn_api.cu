@@ -942,32 +942,27 @@ int cache_io(const attn_cache* c, int64_t tokens, const attn_strides* strides, c
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// How attn_fwd_decode_cache divides the work: CTAs of 8 query rows (16 when a
-// KV head has more), each over a range of pages of one sequence.
+// How attn_fwd_decode_cache divides the work: row tiles of 8 query rows (16
+// when a KV head has more), and as many ranges of the pages as CTAs of all
+// tiles are resident at once (fewer when there are few pages).
 struct DecodeCachePlan {
-  int tile_rows, chunks, split_pages, splits;
-  size_t opart_bytes, bytes;
+  int tile_rows, chunks, ranges;
+  size_t opart_bytes, lpart_bytes, bytes;
 };
-
-// CTAs that a launch over full-length sequences aims at: four on each SM.
-constexpr int64_t kDecodeCacheCtas = 4 * 152;
-constexpr int kMinSplitPages = 8;
 
 DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int max_pages) {
   DecodeCachePlan d;
   const int64_t R = static_cast<int64_t>(Hq / c->Hkv) * n_q;
   d.tile_rows = R > 8 ? 16 : 8;
   d.chunks = static_cast<int>((R + d.tile_rows - 1) / d.tile_rows);
-  const int64_t tiles = static_cast<int64_t>(B) * c->Hkv * d.chunks;
-  const int64_t want = std::max<int64_t>(1, (kDecodeCacheCtas + tiles - 1) / tiles);
-  int64_t pages = (max_pages + want - 1) / want;
-  pages = std::max<int64_t>(pages, kMinSplitPages);
-  pages = (pages + 3) / 4 * 4;     // a page for every warp of the CTA
-  d.split_pages = static_cast<int>(pages);
-  d.splits = static_cast<int>((max_pages + pages - 1) / pages);
-  const size_t rows = static_cast<size_t>(B) * Hq * n_q;
-  d.opart_bytes = d.splits > 1 ? round256(d.splits * rows * c->d_v * sizeof(float)) : 0;
-  d.bytes = d.splits > 1 ? d.opart_bytes + round256(d.splits * rows * sizeof(float)) : 0;
+  const int64_t tiles = static_cast<int64_t>(c->Hkv) * d.chunks;
+  const int64_t resident = 152 * (d.tile_rows == 8 ? kDecodeCacheResident8 : kDecodeCacheResident16);
+  const int64_t most = (static_cast<int64_t>(B) * max_pages + kMinRangePages - 1) / kMinRangePages;
+  d.ranges = static_cast<int>(std::max<int64_t>(1, std::min(resident / tiles, most)));
+  const size_t rows = static_cast<size_t>(tiles) * d.ranges * 2 * d.tile_rows;
+  d.opart_bytes = round256(rows * c->d_v * sizeof(float));
+  d.lpart_bytes = round256(rows * sizeof(float));
+  d.bytes = d.ranges > 1 ? d.opart_bytes + d.lpart_bytes + round256((static_cast<size_t>(B) + 2) * sizeof(int32_t)) : 0;
   return d;
 }
 
@@ -975,7 +970,8 @@ int check_decode_cache(const attn_cache* c, int B, int Hq, int n_q, int max_page
   const int rc = check_cache(c);
   if (rc) return rc;
   if (B <= 0 || Hq <= 0 || n_q <= 0 || max_pages <= 0 || Hq % c->Hkv != 0) return ATTN_ERR_SHAPE;
-  if (max_pages > (1 << 26) - 1) return ATTN_ERR_SHAPE;                          // key numbers are int32
+  if (max_pages > (1 << 26) - 1) return ATTN_ERR_SHAPE;                          // key and page counts are int32
+  if (static_cast<int64_t>(B) * max_pages > int64_t{1} << 30) return ATTN_ERR_SHAPE;
   if (static_cast<int64_t>(B) * Hq > (int64_t{1} << 31) / 16 - 1) return ATTN_ERR_SHAPE;
   if (n_q > 16) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
@@ -1892,11 +1888,12 @@ int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
   p.O = O;
   p.LSE = LSE;
   p.Opart = plan.bytes > 0 ? static_cast<float*>(workspace) : nullptr;
-  p.Lpart = plan.bytes > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.opart_bytes) : nullptr;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.Lpart = plan.bytes > 0 ? reinterpret_cast<float*>(ws + plan.opart_bytes) : nullptr;
+  p.first_page = plan.bytes > 0 ? reinterpret_cast<int32_t*>(ws + plan.opart_bytes + plan.lpart_bytes) : nullptr;
   p.tile_rows = plan.tile_rows;
   p.chunks = plan.chunks;
-  p.split_pages = plan.split_pages;
-  p.splits = plan.splits;
+  p.ranges = plan.ranges;
   p.status = status;
   const cudaError_t e = launch_decode_cache(cache->d_h, cache->d_v, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -7,7 +7,7 @@
 //   K words [32][d_h / 64]  V words [32][d_v / 64]   (32 bits each)
 // Byte i of a row of codes holds element 2i in its low half and 2i + 1 in
 // its high half.  The word of a group of 64 elements holds its scale s (bf16)
-// in the upper 16 bits and its zero point z (0..15) in the lowest byte; an
+// in the upper 16 bits and its zero point z (0..15) in the lower 16; an
 // element stands for s (code - z).  A block is contiguous and a multiple of
 // 16 bytes, so one bulk copy brings it into shared memory.
 #pragma once

@@ -553,13 +553,13 @@ int attn_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, int3
  *   K words [32][d_h / 64], V words [32][d_v / 64]  (32 bits each).
  * Byte i of a row of codes has element 2i in its low and 2i + 1 in its high
  * half.  The word of a group of 64 elements has its scale s (bf16) in the
- * upper 16 bits and its zero point z in the lowest byte (0..15); an element
+ * upper 16 bits and its zero point z (0..15) in the lower 16; an element
  * stands for s (code - z).  attn_cache_append writes, for a group with
  * lo = min(0, min x) and hi = max(0, max x):
  *   s = bf16((hi - lo) / 15), z = min(15, rint(-lo / s)),
  *   code = clamp(rint(x / s) + z, 0, 15)        (s = 0: codes and z are 0)
  * in fp32, so that an element is off by at most about s / 2 (s where z's
- * rounding and that of the range's end meet).  Inputs are finite, |x| < 2^126.
+ * rounding and that of the range's end meet).  Inputs are finite, |x| < 2^96.
  * The pool's contents need no initialisation: only the tokens that a call
  * names are read. */
 typedef struct {

@@ -167,5 +167,10 @@ def attend(q, K, V, length, scale):
             # whose largest possible value is 2^14 times the largest scale's power of two.
             step = np.abs(v).max() / 7.0 if n else 0.0
             Oerr[r, i] = ((F16 + 2 * rel) * A) @ np.abs(v) + n * 2.0 ** -25 * 15 * 2 * step / 64 / max(p.sum(), 1.0)
+            # The codes and the zero points are summed apart, in fp32: sums of up to
+            # 15 s per weight over n / 16 + 8 steps, each of which rounds or cuts off at
+            # most 2^-23 of the sum.  15 s is the group's range, at most 2 max |v| + s.
+            span = np.repeat(np.abs(v.reshape(n, -1, GROUP)).max(-1), GROUP, axis=-1) * 2.2
+            Oerr[r, i] += 2 * (n / 16 + 8) * 2.0 ** -23 * (A @ span)
             Lerr[r, i] = rel.max() + 2.0 ** -20 * (1 + abs(L[r, i]) * 0.25)
     return O, L, Oerr, Lerr

@@ -147,8 +147,8 @@ def test_cache_attention_refuses(lib):
     assert call(pages=1000, n=need - 1) == bnd.ATTN_ERR_WORKSPACE
     assert call(pages=1000, ws=ctypes.c_void_p(512 + 16)) == bnd.ATTN_ERR_WORKSPACE
     assert lib.attn_fwd_decode_cache_workspace_bytes(_cache(), 2, 8, 17, 1000) == 0
-    # one range: no workspace
-    assert lib.attn_fwd_decode_cache_workspace_bytes(_cache(), 2, 8, 1, 4) == 0
+    # four pages in all are one CTA's: no workspace
+    assert lib.attn_fwd_decode_cache_workspace_bytes(_cache(), 1, 8, 1, 4) == 0
 
 
 def test_page_bytes(lib):

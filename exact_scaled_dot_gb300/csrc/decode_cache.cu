@@ -244,7 +244,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     }
   }
 
-  uint32_t used = 0;         // copies that this warp has issued: stage used % kStages, phase used / kStages
+  // The stage of this warp's next page, and the parity that its barrier's
+  // phase will have (the stages are used in turn, across sequences).
+  uint32_t st = 0, parity = 0;
+  auto after = [](uint32_t s) { return s + 1 == kStages ? 0u : s + 1; };
   for (; b < p.B && *abort_flag != 2; ++b) {
     int len;
     const int npages = pages_of(p, b, len);
@@ -265,11 +268,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     int ids = 0;            // page numbers of a batch of 32 of this warp's pages, one per lane
     uint32_t bad = 0u;      // bit s: stage s stands for a page outside the pool
     int issued = 0;
-    auto issue = [&]() {
+    auto issue = [&](uint32_t s) {           // the next page, into stage s
       if ((issued & 31) == 0)
         ids = issued + static_cast<int>(lane) < n ? table[(issued + static_cast<int>(lane)) * kWarps] : 0;
       const int id = __shfl_sync(0xffffffffu, ids, issued & 31);
-      const uint32_t s = (used + issued) % kStages;
       const bool in_pool = id >= 0 && id < p.pages;
       bad = in_pool ? bad & ~(1u << s) : bad | (1u << s);
       if (lane == 0) {
@@ -284,7 +286,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
       }
       ++issued;
     };
-    while (issued < kStages && issued < n) issue();
+    for (uint32_t s = st; issued < kStages && issued < n; s = after(s)) issue(s);
 
     // ---- Q fragments: column g of row group nt is query row r0 + 8 nt + g ----
     // k-step 4 gk + 2 w + e holds the dims 64 gk + 16 t + 8 w + {2e, 2e+4} in
@@ -361,14 +363,12 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     const int key_g = g ^ ((g >> 1) & 1);
     const int key_t0 = (2 * t) ^ (t & 1), key_t1 = (2 * t + 1) ^ (t & 1);
 
-    bool ok = true;
-    for (int it = 0; it < n && ok; ++it) {
-      const uint32_t st = (used + it) % kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * st, ((used + it) / kStages) & 1u, abort_flag, p.wait_limit_ns));
-      if (!ok) break;
+    int done = 0;
+    while (done < n) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, parity, abort_flag, p.wait_limit_ns))) break;
       {
         const uint8_t* blk = ring_ptr + st * C::kBlock;
-        const int key0 = (first + static_cast<int>(warp) + it * kWarps) * kPageTokens;
+        const int key0 = (first + static_cast<int>(warp) + done * kWarps) * kPageTokens;
         // ---- S^T of the page's two 16-key blocks ----
         float s[2][NT][4];
 #pragma unroll
@@ -532,14 +532,19 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         }
       }
       __syncwarp();            // every lane has read the stage
-      if (issued < n) issue();
+      if (issued < n) issue(st);
+      st = after(st);
+      parity ^= st == 0 ? 1u : 0u;
+      ++done;
     }
-    used += issued;
     if (*abort_flag) {
       // Every copy already in flight must land before the CTA can exit.
       int no_abort = 0;
-      for (uint32_t u = used - (issued < kStages ? issued : kStages); u != used; ++u)
-        mbar_wait(bars + 8 * (u % kStages), (u / kStages) & 1u, &no_abort, p.wait_limit_ns);
+      for (; done < issued; ++done) {
+        mbar_wait(bars + 8 * st, parity, &no_abort, p.wait_limit_ns);
+        st = after(st);
+        parity ^= st == 0 ? 1u : 0u;
+      }
     }
     if (next0 >= end) cudaTriggerProgrammaticLaunchCompletion();   // the merge kernel may start (it waits for this grid)
     __syncthreads();
@@ -627,38 +632,34 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
   if (threadIdx.x == 0 && *abort_flag == 1) record_status(p.status, ATTN_ERR_TIMEOUT);
 }
 
-// Merge of the parts of a sequence that several ranges share, one block per
-// query row: LSE = M + ln sum_s exp(LSE_s - M), O = sum_s exp(LSE_s - LSE) O_s.
-// Launched while the main kernel drains; the warps take every kWarps-th part.
-template <int DV>
+// Merge of the parts of a sequence that several ranges share: LSE = M + ln
+// sum_s exp(LSE_s - M), O = sum_s exp(LSE_s - LSE) O_s.  ROWS query rows per
+// block, each shared by kWarps / ROWS warps, which take every so many parts.
+// Launched while the main kernel drains.  Rows of a sequence without pages
+// get O = 0, LSE = -inf here.
+template <int DV, int ROWS>
 __global__ void __launch_bounds__(kThreads) decode_cache_merge_kernel(const __grid_constant__ DecCacheParams p) {
-  constexpr int kPer = DV / 32;
-  __shared__ float acc_s[kWarps][DV + 4];
-  __shared__ float sum_s[kWarps];
+  constexpr int kPer = DV / 32, kShare = kWarps / ROWS;
   const int R = p.group * p.n_q;
-  const int64_t r = blockIdx.x;              // (b, KV head, row)
   const uint32_t lane = lane_id(), warp = warp_id();
-  const int bh = static_cast<int>(blockIdx.x) / R;
-  const int row = static_cast<int>(blockIdx.x) - bh * R;
+  const int r = static_cast<int>(blockIdx.x * ROWS + warp / kShare);    // (b, KV head, row)
+  const int who = static_cast<int>(warp) % kShare;
+  if (r >= p.B * p.Hkv * R) return;          // (ROWS = 1: never)
+  const int bh = r / R, row = r - bh * R;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int chunk = row / p.tile_rows;
+  // The row in part 0 of its tile; a part has tile_rows of them.
+  const int64_t base_row =
+      static_cast<int64_t>(h * p.chunks + chunk) * p.ranges * 2 * p.tile_rows + row - chunk * p.tile_rows;
   cudaGridDependencySynchronize();
   if (status_blocks(p.status)) return;
   const int per = p.first_page[0], seq0 = p.first_page[1 + b], npages = p.first_page[2 + b] - seq0;
-  if (npages == 0) {
-    for (int k = static_cast<int>(threadIdx.x); k < DV; k += kThreads)
-      static_cast<__nv_bfloat16*>(p.O)[r * DV + k] = __float2bfloat16_rn(0.f);
-    if (threadIdx.x == 0) p.LSE[r] = -INFINITY;
-    return;
-  }
   const int i0 = seq0 / per, i1 = (seq0 + npages - 1) / per;
-  if (i0 == i1) return;                      // written by the main kernel
-  const int chunk = row / p.tile_rows;
-  const int64_t tile = static_cast<int64_t>(h) * p.chunks + chunk;
-  auto part_row = [&](int i) {
-    return ((tile * p.ranges + i) * 2 + (seq0 > i * per ? 1 : 0)) * p.tile_rows + row - chunk * p.tile_rows;
-  };
+  if (npages > 0 && i0 == i1) return;        // written by the main kernel
+  auto part_row = [&](int i) { return base_row + (2 * i + (seq0 > i * per ? 1 : 0)) * p.tile_rows; };
+  const int n = npages > 0 ? i1 - i0 + 1 : 0;
   float M = -INFINITY;
-  for (int i = i0 + static_cast<int>(lane); i <= i1; i += 32) M = fmaxf(M, p.Lpart[part_row(i)]);
+  for (int i = static_cast<int>(lane); i < n; i += 32) M = fmaxf(M, p.Lpart[part_row(i0 + i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   const float base = M == -INFINITY ? 0.f : M;
@@ -666,8 +667,8 @@ __global__ void __launch_bounds__(kThreads) decode_cache_merge_kernel(const __gr
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
 #pragma unroll 8
-  for (int i = i0 + static_cast<int>(warp); i <= i1; i += kWarps) {
-    const int64_t pr = part_row(i);
+  for (int i = who; i < n; i += kShare) {
+    const int64_t pr = part_row(i0 + i);
     const float w = fast_exp2((p.Lpart[pr] - base) * kLog2e);
     sum += w;
     const float2* src = reinterpret_cast<const float2*>(p.Opart + pr * DV + lane * kPer);
@@ -678,20 +679,32 @@ __global__ void __launch_bounds__(kThreads) decode_cache_merge_kernel(const __gr
       acc[k + 1] = fmaf(w, v.y, acc[k + 1]);
     }
   }
+  if constexpr (kShare > 1) {
+    __shared__ float acc_s[kShare][DV], sum_s[kShare];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) acc_s[warp][lane * kPer + k] = acc[k];
-  if (lane == 0) sum_s[warp] = sum;
-  __syncthreads();
-  sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
-  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
-  const int k = static_cast<int>(threadIdx.x) * 2;
-  if (k < DV) {
-    const float o0 = acc_s[0][k] + acc_s[1][k] + acc_s[2][k] + acc_s[3][k];
-    const float o1 = acc_s[0][k + 1] + acc_s[1][k + 1] + acc_s[2][k + 1] + acc_s[3][k + 1];
-    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.O) + r * DV + k) = pack_bf16x2(o0 * inv, o1 * inv);
+    for (int k = 0; k < kPer; ++k) acc_s[who][k * 32 + lane] = acc[k];
+    if (lane == 0) sum_s[who] = sum;
+    __syncthreads();
+    if (who > 0) return;
+#pragma unroll
+    for (int w = 1; w < kShare; ++w) {
+      sum += sum_s[w];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] += acc_s[w][k * 32 + lane];
+    }
   }
-  if (threadIdx.x == 0) p.LSE[r] = sum == 0.f ? -INFINITY : M + fast_log2(sum) * kLn2;
+  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.O) + static_cast<int64_t>(r) * DV + lane * kPer);
+#pragma unroll
+  for (int k = 0; k < kPer; k += 2) dst[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
+  if (lane == 0) p.LSE[r] = sum == 0.f ? -INFINITY : M + fast_log2(sum) * kLn2;
 }
+
+// Up to this many query rows, the merge gives each a block of its own: four
+// times the loads in flight for the many parts of few long sequences.
+// Measured: 256 rows of 8 long sequences, 4 us against 5; 3072 rows of 48
+// ragged ones, 6 us against 4 with a warp per row.
+constexpr int kMergeBlockRows = 8 * 152;
 
 template <int DH, int DV, int NT>
 cudaError_t launch_t(const DecCacheParams& p, cudaStream_t stream) {
@@ -706,12 +719,17 @@ cudaError_t launch_t(const DecCacheParams& p, cudaStream_t stream) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.group * p.n_q));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_cache_merge_kernel<DV>, p);
+  const int rows = p.B * p.Hkv * p.group * p.n_q;
+  if (rows <= kMergeBlockRows) {
+    cfg.gridDim = dim3(static_cast<unsigned>(rows));
+    return cudaLaunchKernelEx(&cfg, decode_cache_merge_kernel<DV, 1>, p);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
+  return cudaLaunchKernelEx(&cfg, decode_cache_merge_kernel<DV, kWarps>, p);
 }
 
 template <int DH, int DV>

@@ -87,6 +87,9 @@ int check_scale(float scale) {
   return (std::isfinite(scale) && scale > 0.f) ? ATTN_OK : ATTN_ERR_SCALE;
 }
 
+// eps of a norm: a normal number, so that eps and 1/sqrt(eps) are.
+int check_eps(float eps) { return std::isnormal(eps) && eps > 0.f ? ATTN_OK : ATTN_ERR_SCALE; }
+
 int check_ptrs(std::initializer_list<const void*> ptrs) {
   for (const void* p : ptrs)
     if (!p) return ATTN_ERR_NULL;
@@ -1745,7 +1748,7 @@ int attn_qk_norm_rope(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t 
                       const void* gq, const void* gk, void* Yq, void* Yk, void* stream) {
   int rc = check_qk_dims(tokens, heads_q, heads_k, d);
   if (rc) return rc;
-  rc = check_scale(eps);
+  rc = check_eps(eps);
   if (rc) return rc;
   rc = check_axes(rotary, d);
   if (rc) return rc;
@@ -1780,7 +1783,7 @@ int attn_qk_norm_rope(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t 
 
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d) {
   if (check_qk_dims(tokens, heads_q, heads_k, d) != ATTN_OK) return 0;
-  return round256(static_cast<size_t>(2) * qk_bwd_blocks(tokens, heads_q, heads_k, d) * d * sizeof(float));
+  return round256(static_cast<size_t>(qk_bwd_blocks(tokens, heads_q, heads_k)) * d * sizeof(float));
 }
 
 int attn_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, float eps,
@@ -1789,7 +1792,7 @@ int attn_qk_norm_rope_bwd(int64_t tokens, int32_t heads_q, int32_t heads_k, int3
                           float* dgq, float* dgk, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_qk_dims(tokens, heads_q, heads_k, d);
   if (rc) return rc;
-  rc = check_scale(eps);
+  rc = check_eps(eps);
   if (rc) return rc;
   rc = check_axes(rotary, d);
   if (rc) return rc;

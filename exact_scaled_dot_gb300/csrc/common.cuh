@@ -326,7 +326,9 @@ struct QkParams {
   int32_t inverse;             // rotation alone: by -a
   int32_t axes;                // position axes (0: no rotation)
   const int32_t* pos;          // [axes][tokens]
-  float* partial;              // backward: [2][blocks][d] shares of the weight gradients
+  int32_t part_heads;          // heads of a token that one block takes, and how many
+  int32_t parts_q;             // such parts the query heads make (set by the launchers)
+  float* partial;              // backward: [parts][blocks][d] shares of the weight gradients
   float w_hi[64], w_lo[64];    // frequency of each block (0 past the sections), as in RotaryAngles
   uint8_t axis[64];            // axis of each block
 };
@@ -404,10 +406,10 @@ cudaError_t launch_rope_prep(const RopePrepParams& p, cudaStream_t stream);
 cudaError_t launch_rope(int64_t tokens, int d, int heads_a, int heads_b, const int32_t* pos, const float* w_hi,
                         const float* w_lo, int inverse, const void* xa, void* ya, const void* xb, void* yb, cudaStream_t stream);
 // norm: RMS norm before the rotation; else the rotation alone.
-cudaError_t launch_qk_fwd(const QkParams& p, bool norm, cudaStream_t stream);
-// Blocks of the backward, the number of partial weight gradients per tensor.
-int qk_bwd_blocks(int64_t tokens, int heads_q, int heads_k, int d);
-cudaError_t launch_qk_bwd(const QkParams& p, float* dgq, float* dgk, cudaStream_t stream);
+cudaError_t launch_qk_fwd(QkParams p, bool norm, cudaStream_t stream);
+// Blocks of the backward: partial weight gradients.
+int qk_bwd_blocks(int64_t tokens, int heads_q, int heads_k);
+cudaError_t launch_qk_bwd(QkParams p, float* dgq, float* dgk, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_decode_cache(int dh, int dv, const DecCacheParams& p, cudaStream_t stream);

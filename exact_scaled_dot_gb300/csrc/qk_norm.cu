@@ -13,12 +13,12 @@
 // since d r / d x_i = -r^3 x_i / d.
 //
 // All three kernels move each row once: 4 bytes per element forward (bf16 in
-// and out), 6 backward (x and dy in, dx out), and are bound by DRAM.  A row's
-// chunk of 8 elements (one 16-byte access, four blocks) belongs to one lane;
-// 16 lanes (8 up to width 64) hold a row and sum over it with shuffles.  A
-// lane keeps its chunk for a group of heads of one token, so the token's four
-// angles are formed once per group, and every row of the group is requested
-// before the first is worked on.
+// and out), 6 backward (x and dy in, dx out), and are bound by DRAM.  Eight
+// lanes hold a row, each one or two chunks of 8 elements (16-byte accesses;
+// up to width 64, up to 128), and sum over it with three shuffles.  Lanes
+// walk over the heads of a token, so that the token's angles (and with them
+// the products of cosines, sines and weights) are formed once for up to
+// kMostHeads rows, and request several rows before they work on the first.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -30,21 +30,27 @@
 namespace esd {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kFwdHeads = 8;    // heads per work item, forward
-constexpr int kBwdHeads = 4;    // backward: two rows per head in flight
+constexpr int kThreads = 128;
+constexpr int kLanes = 8;                      // lanes of a row
+constexpr int kSlots = kThreads / kLanes;      // tokens that a block works on at once
+// Heads of one token that a slot takes, at most.  More share the angles,
+// fewer balance the blocks: forward 32.5, 30.3, 30.8 us with 8, 16, 32 heads
+// (8192 tokens, 32 + 8 heads of 128), backward 160, 163 us with 8, 16.
+constexpr int kFwdHeads = 16;
+constexpr int kBwdHeads = 8;
+constexpr int kStages = 4;                     // steps in the ring (a power of two)
 
-// The lanes that hold one row.
-template <int LANES>
-__device__ __forceinline__ uint32_t row_mask(uint32_t lane) {
-  return (LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u)) << (lane & ~(LANES - 1u));
+__device__ __forceinline__ float row_sum(float v, uint32_t mask) {
+  v += __shfl_xor_sync(mask, v, 1);
+  v += __shfl_xor_sync(mask, v, 2);
+  return v + __shfl_xor_sync(mask, v, 4);
 }
 
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v, uint32_t mask) {
-#pragma unroll
-  for (int off = LANES / 2; off > 0; off >>= 1) v += __shfl_xor_sync(mask, v, off);
-  return v;
+// 1 / sqrt(x) of a normal positive x (x >= eps), to a few 1e-7.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
@@ -56,53 +62,65 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// A lane's four blocks: frequencies and axes, fixed for the whole kernel.
-struct LaneBlocks {
-  float wh[4], wl[4];
-  int axis[4];
-};
-__device__ __forceinline__ LaneBlocks lane_blocks(const QkParams& p, int c) {
-  LaneBlocks b;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    b.wh[q] = p.w_hi[4 * c + q];
-    b.wl[q] = p.w_lo[4 * c + q];
-    b.axis[q] = p.axis[4 * c + q];
-  }
-  return b;
+// 16 bytes from global to shared memory, in the thread's current group.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {      // all but the last N groups are there
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
-// (cos, sin) of the four blocks at token `tok`: t0 of blocks 0, 1 and t1 of
-// blocks 2, 3.  Same angles as the single-axis rotation.
-__device__ __forceinline__ void block_angles(const QkParams& p, const LaneBlocks& b, int64_t tok, float4& t0,
-                                             float4& t1) {
-  if (p.axes == 0) {
+// Which heads of which tensor a block works on: blockIdx.y counts the parts
+// of the query heads, then those of the key heads.
+struct Part {
+  int which, h0, n;
+};
+__device__ __forceinline__ Part part_of(const QkParams& p) {
+  const int y = static_cast<int>(blockIdx.y);
+  const int which = y >= p.parts_q ? 1 : 0;
+  const int h0 = (which ? y - p.parts_q : y) * p.part_heads;
+  return Part{which, h0, min(p.part_heads, p.heads[which] - h0)};
+}
+
+// The frequencies (w_hi, w_lo) and the axis of every block, in shared memory:
+// read once per token by lanes that differ in the block.
+struct BlockTable {
+  float4 e[64];
+};
+__device__ __forceinline__ void fill_table(const QkParams& p, BlockTable& t) {
+  if (threadIdx.x < 64)
+    t.e[threadIdx.x] = make_float4(p.w_hi[threadIdx.x], p.w_lo[threadIdx.x], __int_as_float(p.axis[threadIdx.x]), 0.f);
+  __syncthreads();
+}
+
+// Cosines and sines of the four blocks of chunk c at the token's positions
+// (the same angles as the single-axis rotation); t0: blocks 0, 1, t1: 2, 3.
+__device__ __forceinline__ void chunk_angles(const BlockTable& tab, int axes, const int32_t (&pos)[kMaxAxes], int c,
+                                             float4& t0, float4& t1) {
+  if (axes == 0) {
     t0 = t1 = make_float4(1.f, 0.f, 1.f, 0.f);
     return;
   }
-  int32_t pos[kMaxAxes];
-#pragma unroll
-  for (int a = 0; a < kMaxAxes; ++a) pos[a] = a < p.axes ? p.pos[a * p.tokens + tok] : 0;
-  float c[4], s[4];
+  float cs[4], sn[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int32_t at = b.axis[q] == 0 ? pos[0] : (b.axis[q] == 1 ? pos[1] : pos[2]);
-    rope_cos_sin(reduced_angle(at, b.wh[q], b.wl[q]), c[q], s[q]);
+    const float4 e = tab.e[4 * c + q];
+    const int axis = __float_as_int(e.z);
+    const int32_t at = axis == 0 ? pos[0] : (axis == 1 ? pos[1] : pos[2]);
+    rope_cos_sin(reduced_angle(at, e.x, e.y), cs[q], sn[q]);
   }
-  t0 = make_float4(c[0], s[0], c[1], s[1]);
-  t1 = make_float4(c[2], s[2], c[3], s[3]);
+  t0 = make_float4(cs[0], sn[0], cs[1], sn[1]);
+  t1 = make_float4(cs[2], sn[2], cs[3], sn[3]);
 }
 
-// Eight fp32 elements turned (s negated by the caller to turn back).
-__device__ __forceinline__ void turn8(float (&x)[8], float4 t0, float4 t1) {
-  float y0, y1;
-  rot_block(x[0], x[1], t0.x, t0.y, y0, y1), x[0] = y0, x[1] = y1;
-  rot_block(x[2], x[3], t0.z, t0.w, y0, y1), x[2] = y0, x[3] = y1;
-  rot_block(x[4], x[5], t1.x, t1.y, y0, y1), x[4] = y0, x[5] = y1;
-  rot_block(x[6], x[7], t1.z, t1.w, y0, y1), x[6] = y0, x[7] = y1;
+__device__ __forceinline__ void token_positions(const QkParams& p, int64_t tok, int32_t (&pos)[kMaxAxes]) {
+#pragma unroll
+  for (int a = 0; a < kMaxAxes; ++a) pos[a] = a < p.axes ? p.pos[a * p.tokens + tok] : 0;
 }
 
-// Weights of a lane's chunk (ones without a weight vector).
+// Weights of chunk c (ones without a weight vector).
 __device__ __forceinline__ void load_weights(const void* g, int c, float (&w)[8]) {
   if (g) {
     unpack8(static_cast<const uint4*>(g)[c], w);
@@ -112,156 +130,264 @@ __device__ __forceinline__ void load_weights(const void* g, int c, float (&w)[8]
   }
 }
 
-// Forward.  Work item: a group of up to kFwdHeads heads of one token; the
-// items of the queries come first, then those of the keys.
-template <int LANES, bool NORM>
+// Forward.  CH chunks per lane: chunk i of lane c is c + 8 i.
+template <int CH, bool NORM>
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant__ QkParams p) {
+  constexpr int kRows = CH == 1 ? 4 : 2;       // rows of a step
+  __shared__ BlockTable tab;
+  __shared__ uint4 ring[kStages][kRows * CH][kThreads];
+  fill_table(p, tab);
   const uint32_t lane = lane_id();
-  const int c = static_cast<int>(lane & (LANES - 1));
-  const uint32_t mask = row_mask<LANES>(lane);
-  const bool on = c < p.d / 8;
-  const LaneBlocks blk = lane_blocks(p, on ? c : 0);
+  const uint32_t mask = 0xffu << (lane & 24u);
+  const int c = static_cast<int>(lane & 7);
+  const Part part = part_of(p);
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  const int groups_q = (p.heads[0] + kFwdHeads - 1) / kFwdHeads;
-  const int groups_k = (p.heads[1] + kFwdHeads - 1) / kFwdHeads;
-  const int64_t items_q = p.tokens * groups_q;
-  const int64_t items = items_q + p.tokens * groups_k;
-  const int64_t slots = static_cast<int64_t>(gridDim.x) * (kThreads / LANES);
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES; u0 < items;
-       u0 += slots) {
-    const int which = u0 >= items_q ? 1 : 0;
-    const int64_t u = which ? u0 - items_q : u0;
-    const int groups = which ? groups_k : groups_q;
-    const int64_t tok = u / groups;
-    const int h0 = static_cast<int>(u - tok * groups) * kFwdHeads;
-    const int n = min(kFwdHeads, p.heads[which] - h0);
-    const uint4* x = static_cast<const uint4*>(p.x[which]) + (tok * p.sx[which].row + h0 * p.sx[which].head) / 8 + c;
-    const int64_t xh = p.sx[which].head / 8;
-    uint4 v[kFwdHeads];
+  const int64_t tok = static_cast<int64_t>(blockIdx.x) * kSlots + threadIdx.x / kLanes;
+  if (tok >= p.tokens) return;
+  const int64_t xh = p.sx[part.which].head / 8, yh = p.sy[part.which].head / 8;
+  const uint4* x = static_cast<const uint4*>(p.x[part.which]) + tok * (p.sx[part.which].row / 8) + part.h0 * xh + c;
+  uint4* y = static_cast<uint4*>(p.y[part.which]) + tok * (p.sy[part.which].row / 8) + part.h0 * yh + c;
+  bool on[CH];
 #pragma unroll
-    for (int j = 0; j < kFwdHeads; ++j) v[j] = on && j < n ? x[j * xh] : make_uint4(0u, 0u, 0u, 0u);
-    float4 t0, t1;
-    block_angles(p, blk, tok, t0, t1);
-    if (p.inverse) rope_transpose(t0, t1);
-    uint4* y = static_cast<uint4*>(p.y[which]) + (tok * p.sy[which].row + h0 * p.sy[which].head) / 8 + c;
-    const int64_t yh = p.sy[which].head / 8;
-    float w[8];
-    if constexpr (NORM) load_weights(p.g[which], on ? c : 0, w);
+  for (int i = 0; i < CH; ++i) on[i] = c + 8 * i < p.d / 8;
+  auto request = [&](int it) {       // the rows of step `it`
+    const int h = it * kRows;
 #pragma unroll
-    for (int j = 0; j < kFwdHeads; ++j) {
-      if (j >= n) break;
-      uint4 out;
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (on[i] && h + j < part.n)
+          copy16(smem_u32(&ring[it & (kStages - 1)][j * CH + i][threadIdx.x]), x + (h + j) * xh + 8 * i);
+    copy_commit();
+  };
+#pragma unroll
+  for (int it = 0; it < kStages - 1; ++it) request(it);
+  int32_t pos[kMaxAxes];
+  token_positions(p, tok, pos);
+  // cs: the cosines and sines; with a norm, each block's map (x0, x1) ->
+  // (x0 a - x1 b, x0 c + x1 d) with the weights in it.
+  float4 cs[CH][2], map[CH][4];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int ci = on[i] ? c + 8 * i : 0;
+    chunk_angles(tab, p.axes, pos, ci, cs[i][0], cs[i][1]);
+    if (p.inverse) rope_transpose(cs[i][0], cs[i][1]);
+    if constexpr (NORM) {
+      float w[8];
+      load_weights(p.g[part.which], ci, w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 t = cs[i][q / 2];
+        const float co = q & 1 ? t.z : t.x, si = q & 1 ? t.w : t.y;
+        map[i][q] = make_float4(w[2 * q] * co, w[2 * q + 1] * si, w[2 * q] * si, w[2 * q + 1] * co);
+      }
+    }
+  }
+  for (int it = 0; it * kRows < part.n; ++it) {
+    copy_wait<kStages - 2>();
+    uint4 v[kRows][CH];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        v[j][i] = ring[it & (kStages - 1)][j * CH + i][threadIdx.x];
+        if (!on[i]) v[j][i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    request(it + kStages - 1);
+    const int h = it * kRows;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
       if constexpr (NORM) {
-        float e[8];
-        unpack8(v[j], e);
-        float sq = 0.f;
+        float e[CH][8], sq = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sq = fmaf(e[k], e[k], sq);
-        const float r = rsqrtf(row_sum<LANES>(sq, mask) * inv_d + p.eps);
+        for (int i = 0; i < CH; ++i) {
+          unpack8(v[j][i], e[i]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] *= r * w[k];
-        turn8(e, t0, t1);
-        out = pack8(e);
+          for (int k = 0; k < 8; ++k) sq = fmaf(e[i][k], e[i][k], sq);
+        }
+        const float r = inv_sqrt(fmaf(row_sum(sq, mask), inv_d, p.eps));
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float x0 = e[i][2 * q], x1 = e[i][2 * q + 1];
+            e[i][2 * q] = r * fmaf(x0, map[i][q].x, -(x1 * map[i][q].y));
+            e[i][2 * q + 1] = r * fmaf(x0, map[i][q].z, x1 * map[i][q].w);
+          }
+          if (on[i] && h + j < part.n) y[(h + j) * yh + 8 * i] = pack8(e[i]);
+        }
       } else {
-        out = rot_bf16x8(v[j], t0, t1);
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          if (on[i] && h + j < part.n) y[(h + j) * yh + 8 * i] = rot_bf16x8(v[j][i], cs[i][0], cs[i][1]);
       }
-      if (on) y[j * yh] = out;
     }
   }
+  copy_wait<0>();        // (only empty groups are left)
 }
 
-// Backward.  Work item: a group of up to kBwdHeads heads of one token.  The
-// lanes add e o n for their chunk over all their rows; a block then adds its
-// rows' shares in a fixed order into partial[which][block][d], and
-// qk_dg_kernel adds the blocks', again in a fixed order: no atomics, the
-// same bits on every run.
-template <int LANES>
+// Steps of the backward's lanes: kRows heads of one token after another, then the next
+// token.  A cursor names a step; the ring's runs kStages - 1 steps ahead.
+template <int ROWS>
+struct Cursor {
+  int64_t tok;
+  int h;
+  __device__ __forceinline__ void next(int n, int64_t step) {
+    h += ROWS;
+    if (h >= n) {
+      h = 0;
+      tok += step;
+    }
+  }
+};
+
+// Backward.  The lanes add e o n for their chunks over all their rows; a
+// block then adds its slots' shares in a fixed order into
+// partial[blockIdx.y][blockIdx.x][d], and qk_dg_kernel adds the blocks', again
+// in a fixed order: no atomics, the same bits on every run.
+template <int CH>
 __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant__ QkParams p) {
-  constexpr int kRows = kThreads / LANES;
-  __shared__ float red[kRows][LANES * 8 + 4];
+  constexpr int kRows = CH == 1 ? 2 : 1;       // rows of a step
+  __shared__ BlockTable tab;
+  // The ring (x, then dy), and at the end the slots' shares of dg.
+  __shared__ union {
+    uint4 ring[kStages][2][kRows * CH][kThreads];
+    float red[kSlots][CH * 64 + 4];
+  } sh;
+  fill_table(p, tab);
   const uint32_t lane = lane_id();
-  const int c = static_cast<int>(lane & (LANES - 1));
-  const uint32_t mask = row_mask<LANES>(lane);
-  const bool on = c < p.d / 8;
-  const LaneBlocks blk = lane_blocks(p, on ? c : 0);
+  const uint32_t mask = 0xffu << (lane & 24u);
+  const int c = static_cast<int>(lane & 7);
+  const Part part = part_of(p);
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  const int slot = static_cast<int>(threadIdx.x) / LANES;
-  for (int which = 0; which < 2; ++which) {
-    if (p.heads[which] == 0) break;
-    const int groups = (p.heads[which] + kBwdHeads - 1) / kBwdHeads;
-    const int64_t items = p.tokens * groups;
-    float w[8], dg[8];
-    load_weights(p.g[which], on ? c : 0, w);
+  const int64_t xr = p.sx[part.which].row / 8, xh = p.sx[part.which].head / 8;
+  const int64_t dyr = p.sdy[part.which].row / 8, dyh = p.sdy[part.which].head / 8;
+  const int64_t dxr = p.sy[part.which].row / 8, dxh = p.sy[part.which].head / 8;
+  const uint4* x = static_cast<const uint4*>(p.x[part.which]) + part.h0 * xh + c;
+  const uint4* dy = static_cast<const uint4*>(p.dy[part.which]) + part.h0 * dyh + c;
+  uint4* dx = static_cast<uint4*>(p.y[part.which]) + part.h0 * dxh + c;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kSlots;
+  Cursor<kRows> at{static_cast<int64_t>(blockIdx.x) * kSlots + threadIdx.x / kLanes, 0}, ahead = at;
+  bool on[CH];
+  float w[CH][8], dg[CH][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dg[k] = 0.f;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRows + slot; u < items;
-         u += static_cast<int64_t>(gridDim.x) * kRows) {
-      const int64_t tok = u / groups;
-      const int h0 = static_cast<int>(u - tok * groups) * kBwdHeads;
-      const int n = min(kBwdHeads, p.heads[which] - h0);
-      const uint4* x = static_cast<const uint4*>(p.x[which]) + (tok * p.sx[which].row + h0 * p.sx[which].head) / 8 + c;
-      const uint4* dy =
-          static_cast<const uint4*>(p.dy[which]) + (tok * p.sdy[which].row + h0 * p.sdy[which].head) / 8 + c;
-      uint4 v[kBwdHeads], dv[kBwdHeads];
+  for (int i = 0; i < CH; ++i) {
+    on[i] = c + 8 * i < p.d / 8;
+    load_weights(p.g[part.which], on[i] ? c + 8 * i : 0, w[i]);
 #pragma unroll
-      for (int j = 0; j < kBwdHeads; ++j) {
-        const bool ld = on && j < n;
-        v[j] = ld ? x[j * (p.sx[which].head / 8)] : make_uint4(0u, 0u, 0u, 0u);
-        dv[j] = ld ? dy[j * (p.sdy[which].head / 8)] : make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < 8; ++k) dg[i][k] = 0.f;
+  }
+  auto request = [&](int stage) {
+    if (ahead.tok < p.tokens) {
+      const uint4* rx = x + ahead.tok * xr + ahead.h * xh;
+      const uint4* rd = dy + ahead.tok * dyr + ahead.h * dyh;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          if (on[i] && ahead.h + j < part.n) {
+            copy16(smem_u32(&sh.ring[stage][0][j * CH + i][threadIdx.x]), rx + j * xh + 8 * i);
+            copy16(smem_u32(&sh.ring[stage][1][j * CH + i][threadIdx.x]), rd + j * dyh + 8 * i);
+          }
+    }
+    copy_commit();
+    ahead.next(part.n, step);
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) request(s);
+  float4 cs[CH][2];
+  int32_t pos[kMaxAxes];
+  if (at.tok < p.tokens) token_positions(p, at.tok, pos);
+  for (int it = 0; at.tok < p.tokens; ++it) {
+    if (at.h == 0) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        chunk_angles(tab, p.axes, pos, on[i] ? c + 8 * i : 0, cs[i][0], cs[i][1]);
+        rope_transpose(cs[i][0], cs[i][1]);
       }
-      float4 t0, t1;
-      block_angles(p, blk, tok, t0, t1);
-      rope_transpose(t0, t1);
-      uint4* dx = static_cast<uint4*>(p.y[which]) + (tok * p.sy[which].row + h0 * p.sy[which].head) / 8 + c;
+      if (at.tok + step < p.tokens) token_positions(p, at.tok + step, pos);     // the next token's, early
+    }
+    copy_wait<kStages - 2>();
+    const int stage = it & (kStages - 1);
+    uint4 v[kRows][CH], dv[kRows][CH];
 #pragma unroll
-      for (int j = 0; j < kBwdHeads; ++j) {
-        if (j >= n) break;
-        float e[8], xv[8];
-        unpack8(v[j], xv);
-        unpack8(dv[j], e);
-        turn8(e, t0, t1);
-        float sq = 0.f, tx = 0.f;
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const bool there = on[i] && at.h + j < part.n;
+        v[j][i] = sh.ring[stage][0][j * CH + i][threadIdx.x];
+        dv[j][i] = sh.ring[stage][1][j * CH + i][threadIdx.x];
+        if (!there) v[j][i] = dv[j][i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    request((it + kStages - 1) & (kStages - 1));
+    uint4* row = dx + at.tok * dxr + at.h * dxh;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      float e[CH][8], xv[CH][8], pr[CH][8], sq = 0.f, tx = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        unpack8(v[j][i], xv[i]);
+        unpack8(dv[j][i], e[i]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 t = cs[i][q / 2];
+          float y0, y1;
+          rot_block(e[i][2 * q], e[i][2 * q + 1], q & 1 ? t.z : t.x, q & 1 ? t.w : t.y, y0, y1);
+          e[i][2 * q] = y0;
+          e[i][2 * q + 1] = y1;
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          sq = fmaf(xv[k], xv[k], sq);
-          tx = fmaf(e[k] * w[k], xv[k], tx);
+          sq = fmaf(xv[i][k], xv[i][k], sq);
+          pr[i][k] = e[i][k] * xv[i][k];
+          tx = fmaf(w[i][k], pr[i][k], tx);            // t o x = g o e o x
         }
-        const float r = rsqrtf(row_sum<LANES>(sq, mask) * inv_d + p.eps);
-        // mean(t o n) = r mean(t o x), and n = r x.
-        const float m = row_sum<LANES>(tx, mask) * inv_d * r;
+      }
+      const float r = inv_sqrt(fmaf(row_sum(sq, mask), inv_d, p.eps));
+      const float m = row_sum(tx, mask) * inv_d * r * r * r;      // dx = r t - m x
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float nk = xv[k] * r;
-          dg[k] = fmaf(e[k], nk, dg[k]);
-          e[k] = r * fmaf(-nk, m, e[k] * w[k]);
+          dg[i][k] = fmaf(r, pr[i][k], dg[i][k]);
+          e[i][k] = fmaf(r * w[i][k], e[i][k], -(m * xv[i][k]));
         }
-        if (on) dx[j * (p.sy[which].head / 8)] = pack8(e);
+        if (on[i] && at.h + j < part.n) row[j * dxh + 8 * i] = pack8(e[i]);
       }
     }
-    // The block's share of dg, row by row.
-    __syncthreads();
+    at.next(part.n, step);
+  }
+  copy_wait<0>();        // (only empty groups are left)
+  __syncthreads();
+  // The block's share of dg, slot by slot.
 #pragma unroll
-    for (int k = 0; k < 8; ++k) red[slot][c * 8 + k] = dg[k];
-    __syncthreads();
-    for (int k = threadIdx.x; k < p.d; k += kThreads) {
-      float s = 0.f;
-      for (int i = 0; i < kRows; ++i) s += red[i][k];
-      p.partial[(static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * p.d + k] = s;
-    }
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sh.red[threadIdx.x / kLanes][(c + 8 * i) * 8 + k] = dg[i][k];
+  __syncthreads();
+  for (int k = threadIdx.x; k < p.d; k += kThreads) {
+    float s = 0.f;
+    for (int i = 0; i < kSlots; ++i) s += sh.red[i][k];
+    p.partial[(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * p.d + k] = s;
   }
 }
 
-// dg[which][k] = the sum over `blocks` partials; one block per 32 columns of
-// one weight vector.
-__global__ void __launch_bounds__(1024) qk_dg_kernel(const float* partial, int blocks, int d, float* dgq, float* dgk) {
+// dgq and dgk: the sums over their blocks' partials (the first blocks_q,
+// then the rest); one block per 32 columns of one weight vector.
+__global__ void __launch_bounds__(1024) qk_dg_kernel(const float* partial, int blocks_q, int blocks_k, int d, float* dgq,
+                                                     float* dgk) {
   __shared__ float red[32][33];
   const int col = static_cast<int>(blockIdx.x) * 32 + (threadIdx.x & 31);
   const int row = threadIdx.x >> 5;
   float* dst = blockIdx.y ? dgk : dgq;
-  const float* src = partial + static_cast<int64_t>(blockIdx.y) * blocks * d;
+  const float* src = partial + (blockIdx.y ? static_cast<int64_t>(blocks_q) * d : 0);
+  const int blocks = blockIdx.y ? blocks_k : blocks_q;
+  cudaGridDependencySynchronize();
   float s = 0.f;
-  if (dst && col < d)
+  if (dst && col < d) {
+#pragma unroll 4
     for (int b = row; b < blocks; b += 32) s += src[static_cast<int64_t>(b) * d + col];
+  }
   red[row][threadIdx.x & 31] = s;
   __syncthreads();
   s = red[threadIdx.x & 31][row];     // column `row` of the tile, partial row = lane
@@ -271,37 +397,69 @@ __global__ void __launch_bounds__(1024) qk_dg_kernel(const float* partial, int b
   if (dst && (threadIdx.x & 31) == 0 && out < d) dst[out] = s;
 }
 
-template <int LANES>
-cudaError_t launch_fwd_t(const QkParams& p, bool norm, cudaStream_t stream) {
-  const int64_t items = p.tokens * ((p.heads[0] + kFwdHeads - 1) / kFwdHeads + (p.heads[1] + kFwdHeads - 1) / kFwdHeads);
-  int64_t blocks = (items * LANES + kThreads - 1) / kThreads;
-  if (blocks > 152 * 32) blocks = 152 * 32;
-  if (norm) qk_fwd_kernel<LANES, true><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
-  else qk_fwd_kernel<LANES, false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+int parts_of(int heads, int part_heads) { return (heads + part_heads - 1) / part_heads; }
+
+// Heads that a slot takes: `most`, fewer while the blocks would leave SMs
+// idle (a decode step's few tokens).
+int choose_part_heads(int64_t tokens, int heads_q, int heads_k, int most) {
+  int n = most;
+  const int64_t rows = (tokens + kSlots - 1) / kSlots;
+  while (n > 1 && rows * (parts_of(heads_q, n) + parts_of(heads_k, n)) < 2 * 152) n /= 2;
+  return n;
+}
+
+// The backward's blocks along the tokens: four of all parts on each SM, which
+// is what its registers allow, so that each works to the end with its ring
+// filled and has one share of dg.
+int bwd_blocks_x(int64_t tokens, int parts) {
+  const int64_t rows = (tokens + kSlots - 1) / kSlots, most = std::max(1, 152 * 4 / parts);
+  return static_cast<int>(std::min(rows, most));
 }
 
 }  // namespace
 
-int qk_bwd_blocks(int64_t tokens, int heads_q, int heads_k, int d) {
-  const int rows = kThreads / (d <= 64 ? 8 : 16);
-  const int64_t most = tokens * ((std::max(heads_q, heads_k) + kBwdHeads - 1) / kBwdHeads);
-  const int64_t blocks = (most + rows - 1) / rows;
-  return static_cast<int>(blocks < 152 * 4 ? blocks : 152 * 4);
+int qk_bwd_blocks(int64_t tokens, int heads_q, int heads_k) {
+  const int n = choose_part_heads(tokens, heads_q, heads_k, kBwdHeads);
+  const int parts = parts_of(heads_q, n) + parts_of(heads_k, n);
+  return parts * bwd_blocks_x(tokens, parts);
 }
 
-cudaError_t launch_qk_fwd(const QkParams& p, bool norm, cudaStream_t stream) {
-  return p.d <= 64 ? launch_fwd_t<8>(p, norm, stream) : launch_fwd_t<16>(p, norm, stream);
+cudaError_t launch_qk_fwd(QkParams p, bool norm, cudaStream_t stream) {
+  p.part_heads = choose_part_heads(p.tokens, p.heads[0], p.heads[1], kFwdHeads);
+  p.parts_q = parts_of(p.heads[0], p.part_heads);
+  const dim3 grid(static_cast<unsigned>((p.tokens + kSlots - 1) / kSlots),
+                  static_cast<unsigned>(p.parts_q + parts_of(p.heads[1], p.part_heads)));
+  if (p.d <= 64) {
+    if (norm) qk_fwd_kernel<1, true><<<grid, kThreads, 0, stream>>>(p);
+    else qk_fwd_kernel<1, false><<<grid, kThreads, 0, stream>>>(p);
+  } else {
+    if (norm) qk_fwd_kernel<2, true><<<grid, kThreads, 0, stream>>>(p);
+    else qk_fwd_kernel<2, false><<<grid, kThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
 }
 
-cudaError_t launch_qk_bwd(const QkParams& p, float* dgq, float* dgk, cudaStream_t stream) {
-  const int blocks = qk_bwd_blocks(p.tokens, p.heads[0], p.heads[1], p.d);
-  if (p.d <= 64) qk_bwd_kernel<8><<<blocks, kThreads, 0, stream>>>(p);
-  else qk_bwd_kernel<16><<<blocks, kThreads, 0, stream>>>(p);
+cudaError_t launch_qk_bwd(QkParams p, float* dgq, float* dgk, cudaStream_t stream) {
+  p.part_heads = choose_part_heads(p.tokens, p.heads[0], p.heads[1], kBwdHeads);
+  p.parts_q = parts_of(p.heads[0], p.part_heads);
+  const int parts = p.parts_q + parts_of(p.heads[1], p.part_heads);
+  const dim3 grid(static_cast<unsigned>(bwd_blocks_x(p.tokens, parts)), static_cast<unsigned>(parts));
+  if (p.d <= 64) qk_bwd_kernel<1><<<grid, kThreads, 0, stream>>>(p);
+  else qk_bwd_kernel<2><<<grid, kThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dgq && !dgk)) return e;
-  qk_dg_kernel<<<dim3((p.d + 31) / 32, 2), 1024, 0, stream>>>(p.partial, blocks, p.d, dgq, dgk);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.d + 31) / 32), 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_dg_kernel, static_cast<const float*>(p.partial),
+                            static_cast<int>(grid.x) * p.parts_q, static_cast<int>(grid.x) * (parts - p.parts_q), p.d,
+                            dgq, dgk);
 }
 
 }  // namespace esd

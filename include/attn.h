@@ -523,7 +523,7 @@ int attn_rope_axes(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d, 
 /* RMS norm of every query and key row over its width, then the rotation, in
  * one pass: n = x / sqrt(mean(x^2) + eps), y = R(n o g).  gq, gk: bf16 [d]
  * weights shared by the heads, or NULL (ones).  rotary NULL: no rotation.
- * eps finite and > 0 (ATTN_ERR_SCALE).  Sums and products in fp32, one
+ * eps finite, > 0 and not subnormal (ATTN_ERR_SCALE).  Sums and products in fp32, one
  * rounding to bf16; x^2 must stay in fp32's range (|x| < 2^60).  heads_k = 0
  * and K = Yk = NULL: queries only.  Y may be X with the same strides.  Uses
  * strides q, k, yq, yk. */
@@ -531,7 +531,8 @@ int attn_qk_norm_rope(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t 
                       const attn_rotary_axes* rotary, const attn_qk_strides* strides, const void* Q, const void* K,
                       const void* gq, const void* gk, void* Yq, void* Yk, void* stream);
 
-/* Bytes of workspace of attn_qk_norm_rope_bwd (at most 0.6 MB); 0 for invalid sizes. */
+/* Bytes of workspace of attn_qk_norm_rope_bwd (at most 0.4 MB for up to 4096 heads); 0 for
+ * invalid sizes. */
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d);
 
 /* Gradients of attn_qk_norm_rope: dQ, dK (bf16, like Q and K) and the weight

@@ -40,10 +40,11 @@ constexpr int kFwdHeads = 16;
 constexpr int kBwdHeads = 8;
 constexpr int kStages = 4;                     // steps in the ring (a power of two)
 
-__device__ __forceinline__ float row_sum(float v, uint32_t mask) {
-  v += __shfl_xor_sync(mask, v, 1);
-  v += __shfl_xor_sync(mask, v, 2);
-  return v + __shfl_xor_sync(mask, v, 4);
+// Over the eight lanes of a row; called by whole warps.
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  return v + __shfl_xor_sync(0xffffffffu, v, 4);
 }
 
 // 1 / sqrt(x) of a normal positive x (x >= eps), to a few 1e-7.
@@ -138,12 +139,13 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
   __shared__ uint4 ring[kStages][kRows * CH][kThreads];
   fill_table(p, tab);
   const uint32_t lane = lane_id();
-  const uint32_t mask = 0xffu << (lane & 24u);
   const int c = static_cast<int>(lane & 7);
   const Part part = part_of(p);
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  const int64_t tok = static_cast<int64_t>(blockIdx.x) * kSlots + threadIdx.x / kLanes;
-  if (tok >= p.tokens) return;
+  // Slots past the last token go along with the last one and write nothing.
+  const int64_t slot_tok = static_cast<int64_t>(blockIdx.x) * kSlots + threadIdx.x / kLanes;
+  const bool there = slot_tok < p.tokens;
+  const int64_t tok = there ? slot_tok : p.tokens - 1;
   const int64_t xh = p.sx[part.which].head / 8, yh = p.sy[part.which].head / 8;
   const uint4* x = static_cast<const uint4*>(p.x[part.which]) + tok * (p.sx[part.which].row / 8) + part.h0 * xh + c;
   uint4* y = static_cast<uint4*>(p.y[part.which]) + tok * (p.sy[part.which].row / 8) + part.h0 * yh + c;
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 8; ++k) sq = fmaf(e[i][k], e[i][k], sq);
         }
-        const float r = inv_sqrt(fmaf(row_sum(sq, mask), inv_d, p.eps));
+        const float r = inv_sqrt(fmaf(row_sum(sq), inv_d, p.eps));
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
 #pragma unroll
@@ -214,12 +216,12 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
             e[i][2 * q] = r * fmaf(x0, map[i][q].x, -(x1 * map[i][q].y));
             e[i][2 * q + 1] = r * fmaf(x0, map[i][q].z, x1 * map[i][q].w);
           }
-          if (on[i] && h + j < part.n) y[(h + j) * yh + 8 * i] = pack8(e[i]);
+          if (there && on[i] && h + j < part.n) y[(h + j) * yh + 8 * i] = pack8(e[i]);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < CH; ++i)
-          if (on[i] && h + j < part.n) y[(h + j) * yh + 8 * i] = rot_bf16x8(v[j][i], cs[i][0], cs[i][1]);
+          if (there && on[i] && h + j < part.n) y[(h + j) * yh + 8 * i] = rot_bf16x8(v[j][i], cs[i][0], cs[i][1]);
       }
     }
   }
@@ -256,7 +258,6 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
   } sh;
   fill_table(p, tab);
   const uint32_t lane = lane_id();
-  const uint32_t mask = 0xffu << (lane & 24u);
   const int c = static_cast<int>(lane & 7);
   const Part part = part_of(p);
   const float inv_d = 1.0f / static_cast<float>(p.d);
@@ -267,7 +268,9 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
   const uint4* dy = static_cast<const uint4*>(p.dy[part.which]) + part.h0 * dyh + c;
   uint4* dx = static_cast<uint4*>(p.y[part.which]) + part.h0 * dxh + c;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kSlots;
+  // The warps go through the steps together: the block's first slot decides.
   Cursor<kRows> at{static_cast<int64_t>(blockIdx.x) * kSlots + threadIdx.x / kLanes, 0}, ahead = at;
+  const int slot = static_cast<int>(threadIdx.x) / kLanes;
   bool on[CH];
   float w[CH][8], dg[CH][8];
 #pragma unroll
@@ -296,10 +299,13 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) request(s);
   float4 cs[CH][2];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) cs[i][0] = cs[i][1] = make_float4(1.f, 0.f, 1.f, 0.f);    // (slots without a token)
   int32_t pos[kMaxAxes];
   if (at.tok < p.tokens) token_positions(p, at.tok, pos);
-  for (int it = 0; at.tok < p.tokens; ++it) {
-    if (at.h == 0) {
+  for (int it = 0; at.tok - slot < p.tokens; ++it) {
+    const bool there = at.tok < p.tokens;
+    if (at.h == 0 && there) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         chunk_angles(tab, p.axes, pos, on[i] ? c + 8 * i : 0, cs[i][0], cs[i][1]);
@@ -314,10 +320,10 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
     for (int j = 0; j < kRows; ++j)
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const bool there = on[i] && at.h + j < part.n;
+        const bool read = there && on[i] && at.h + j < part.n;
         v[j][i] = sh.ring[stage][0][j * CH + i][threadIdx.x];
         dv[j][i] = sh.ring[stage][1][j * CH + i][threadIdx.x];
-        if (!there) v[j][i] = dv[j][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (!read) v[j][i] = dv[j][i] = make_uint4(0u, 0u, 0u, 0u);
       }
     request((it + kStages - 1) & (kStages - 1));
     uint4* row = dx + at.tok * dxr + at.h * dxh;
@@ -343,8 +349,8 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
           tx = fmaf(w[i][k], pr[i][k], tx);            // t o x = g o e o x
         }
       }
-      const float r = inv_sqrt(fmaf(row_sum(sq, mask), inv_d, p.eps));
-      const float m = row_sum(tx, mask) * inv_d * r * r * r;      // dx = r t - m x
+      const float r = inv_sqrt(fmaf(row_sum(sq), inv_d, p.eps));
+      const float m = row_sum(tx) * inv_d * r * r * r;      // dx = r t - m x
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
 #pragma unroll
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
           dg[i][k] = fmaf(r, pr[i][k], dg[i][k]);
           e[i][k] = fmaf(r * w[i][k], e[i][k], -(m * xv[i][k]));
         }
-        if (on[i] && at.h + j < part.n) row[j * dxh + 8 * i] = pack8(e[i]);
+        if (there && on[i] && at.h + j < part.n) row[j * dxh + 8 * i] = pack8(e[i]);
       }
     }
     at.next(part.n, step);

@@ -37,21 +37,28 @@ constexpr int kTokens = 4;
 constexpr float kToGrid = 6144.0f;          // 1.5 2^12: sums near it are multiples of 2^-11
 constexpr float kToInteger = 12582912.0f;   // 1.5 2^23: sums near it are integers
 
-// Larger of two bf16 pairs, element by element.
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// Pairs of bf16, element by element.
+__device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t a) { return *reinterpret_cast<const __nv_bfloat162*>(&a); }
+__device__ __forceinline__ uint32_t as_bits(__nv_bfloat162 a) { return *reinterpret_cast<const uint32_t*>(&a); }
+__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b) { return as_bits(__hmax2(as_pair(a), as_pair(b))); }
+__device__ __forceinline__ uint32_t min_pairs(uint32_t a, uint32_t b) { return as_bits(__hmin2(as_pair(a), as_pair(b))); }
+
+// 1/x of a normal x whose reciprocal is normal, within 2^-22 of it.
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // The lane's eight elements quantised with its group's (eight lanes') range.
-__device__ __forceinline__ void quantize8(uint4 v, uint32_t mask, uint32_t& codes, uint32_t& word) {
+// Called by whole warps.
+__device__ __forceinline__ void quantize8(uint4 v, uint32_t& codes, uint32_t& word) {
   // max(0, x) and max(0, -x) over the lane as one pair, then over the group.
-  const uint32_t kNeg = 0x80008000u;
-  const uint32_t up = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
-  const uint32_t dn = max_bf16x2(max_bf16x2(v.x ^ kNeg, v.y ^ kNeg), max_bf16x2(v.z ^ kNeg, v.w ^ kNeg));
-  uint32_t m = max_bf16x2(max_bf16x2(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632)), 0u);
+  const uint32_t up = max_pairs(max_pairs(v.x, v.y), max_pairs(v.z, v.w));
+  const uint32_t dn = min_pairs(min_pairs(v.x, v.y), min_pairs(v.z, v.w)) ^ 0x80008000u;
+  uint32_t m = max_pairs(max_pairs(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632)), 0u);
 #pragma unroll
-  for (int off = 4; off > 0; off >>= 1) m = max_bf16x2(m, __shfl_xor_sync(mask, m, off));
+  for (int off = 4; off > 0; off >>= 1) m = max_pairs(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float hi = bf16_lo(m), neg_lo = bf16_hi(m);
   const uint32_t sb = pack_bf16x2(__fdiv_rn(hi + neg_lo, 15.0f), 0.f) << 16;
   const float s = __uint_as_float(sb);
@@ -70,7 +77,7 @@ __device__ __forceinline__ void quantize8(uint4 v, uint32_t mask, uint32_t& code
     }
     return;
   }
-  const float inv = __frcp_rn(s);
+  const float inv = reciprocal(s);
   // rint(a / s) + kToInteger: the second sum is exact before its one rounding.
   auto rounded = [inv](float a) { return fmaf(a, inv, kToGrid) + (kToInteger - kToGrid); };
   const float z = rounded(neg_lo) - kToInteger;
@@ -90,72 +97,79 @@ template <bool APPEND, int DH, int DV>
 __global__ void __launch_bounds__(kThreads) cache_io_kernel(const __grid_constant__ CacheIoParams p) {
   constexpr int kPer = (DH + DV) / 8;
   const int u = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x);
-  if (u >= p.Hkv * kPer) return;
+  const bool on = u < p.Hkv * kPer;
   // This thread's head, tensor (K or V) and chunk, and where they are in a
-  // token's row and, at place 0, in a page.
-  const int h = u / kPer;
-  const bool val = u - h * kPer >= DH / 8;
-  const int c = u - h * kPer - (val ? DH / 8 : 0);
-  const int64_t page_stride = static_cast<int64_t>(p.Hkv) * page_head_bytes(DH, DV);
-  uint8_t* const head0 = p.pool + static_cast<int64_t>(h) * page_head_bytes(DH, DV);
-  uint8_t* const codes0 = head0 + (val ? off_v_codes(DH) : off_k_codes()) + 4 * c;
-  uint8_t* const words0 = head0 + (val ? off_v_words(DH, DV) : off_k_words(DH, DV)) + 4 * (c >> 3);
+  // token's row and, at place 0, in a page (a page is below 2^32 bytes).
+  const int h = on ? u / kPer : 0;
+  const int k = on ? u - h * kPer : 0;
+  const bool val = k >= DH / 8;
+  const int c = k - (val ? DH / 8 : 0);
+  const uint32_t page_stride = static_cast<uint32_t>(p.Hkv) * page_head_bytes(DH, DV);
+  uint8_t* const codes0 = p.pool + static_cast<int64_t>(h) * page_head_bytes(DH, DV) +
+                          (val ? off_v_codes(DH) : off_k_codes()) + 4 * c;
+  const int to_words = (val ? off_v_words(DH, DV) - off_v_codes(DH) : off_k_words(DH, DV)) + 4 * (c >> 3) - 4 * c;
   const int code_row = (val ? DV : DH) / 2, word_row = (val ? DV : DH) / 16;
   const TensorStrides& st = val ? p.sv : p.sk;
-  uint4* const rows = static_cast<uint4*>(const_cast<void*>(val ? p.V : p.K)) + h * (st.head / 8) + c;
-  const int64_t row = st.row / 8;
-  // The eight lanes of a group: their units are consecutive and start at a
-  // multiple of 8, as their threads do.
-  const uint32_t mask = 0xffu << ((threadIdx.y * blockDim.x + threadIdx.x) & 24u);
-  const int tokens = static_cast<int>(p.tokens), step = static_cast<int>(gridDim.x * blockDim.y);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; t0 < tokens; t0 += kTokens * step) {
+  // Tokens of the thread: t, t + step, ...  The warps go through the loop
+  // together (quantize8's sums over lanes), tokens past the end left out.
+  const uint32_t tokens = static_cast<uint32_t>(p.tokens), step = gridDim.x * blockDim.y;
+  uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t row_step = st.row / 8 * step;
+  uint4* row = static_cast<uint4*>(const_cast<void*>(val ? p.V : p.K)) + h * (st.head / 8) + c + t * (st.row / 8);
+  for (uint32_t t_block = blockIdx.x * blockDim.y; t_block < tokens; t_block += kTokens * step) {
+    bool here[kTokens];
     int64_t slot[kTokens];
     uint4 v[kTokens];
+    uint4* at_row[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-      const int64_t t = t0 + i * static_cast<int64_t>(step);
-      slot[i] = t < tokens ? p.slots[t] : -1;
-      if (APPEND && t < tokens) v[i] = rows[t * row];
+      here[i] = on && t < tokens;
+      at_row[i] = row;
+      slot[i] = here[i] ? p.slots[t] : -1;
+      if (APPEND) v[i] = here[i] ? *row : make_uint4(0u, 0u, 0u, 0u);
+      t += step;
+      row += row_step;
     }
     // Codes and words of the slots; a slot without a token (negative: padding;
     // past the pool: recorded in the status word) has none.
     uint32_t codes[kTokens], word[kTokens];
-    int64_t at[kTokens];     // bytes to the slot's page
+    uint8_t* at[kTokens];    // the slot's codes
     int off[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-      const bool in_pool = slot[i] < p.pages * kPageTokens;
-      if (!in_pool && u == 0) record_status(p.status, ATTN_ERR_PAGE);
-      if (!in_pool) slot[i] = -1;
-      at[i] = (slot[i] >> 5) * page_stride;
+      if (slot[i] >= p.pages * kPageTokens) {
+        if (u == 0) record_status(p.status, ATTN_ERR_PAGE);
+        slot[i] = -1;
+      }
       off[i] = static_cast<int>(slot[i]) & (kPageTokens - 1);
+      at[i] = codes0 + static_cast<uint64_t>(static_cast<uint32_t>(slot[i] >> 5)) * page_stride + off[i] * code_row;
       if (!APPEND) {
         codes[i] = word[i] = 0u;
         if (slot[i] >= 0) {
-          codes[i] = *reinterpret_cast<const uint32_t*>(codes0 + at[i] + off[i] * code_row);
-          word[i] = *reinterpret_cast<const uint32_t*>(words0 + at[i] + off[i] * word_row);
+          codes[i] = *reinterpret_cast<const uint32_t*>(at[i]);
+          word[i] = *reinterpret_cast<const uint32_t*>(at[i] + to_words + off[i] * (word_row - code_row));
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-      const int64_t t = t0 + i * static_cast<int64_t>(step);
+      if (t_block + i * step >= tokens) break;       // (none of the block's)
       if (APPEND) {
-        if (slot[i] < 0) continue;                 // (the same for the group's lanes)
-        quantize8(v[i], mask, codes[i], word[i]);
-        *reinterpret_cast<uint32_t*>(codes0 + at[i] + off[i] * code_row) = codes[i];
-        if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(words0 + at[i] + off[i] * word_row) = word[i];
-      } else {
-        if (t >= tokens) break;
-        const float s = bf16_hi(word[i]);
-        // 8388608 + code less 8388608 + z, times s: exact up to the rounding to bf16.
-        const float z = __uint_as_float(0x4B000000u | (word[i] & 0xFFu));
-        float x[8];
+        quantize8(v[i], codes[i], word[i]);
+        if (slot[i] >= 0) {
+          *reinterpret_cast<uint32_t*>(at[i]) = codes[i];
+          if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(at[i] + to_words + off[i] * (word_row - code_row)) = word[i];
+        }
+      } else if (here[i]) {
+        // As bf16: 128 + code less 128 + z, exact, times s, rounded once.
+        const __nv_bfloat162 z = as_pair(0x43004300u | __byte_perm(word[i], 0u, 0x4040));
+        const __nv_bfloat162 s = as_pair(__byte_perm(word[i], 0u, 0x3232));
+        uint32_t x[4];       // elements (k, k + 4)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          x[k] = s * (__uint_as_float(0x4B000000u | ((codes[i] >> (4 * k)) & 15u)) - z);
-        rows[t * row] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                   pack_bf16x2(x[6], x[7]));
+        for (int q = 0; q < 4; ++q)
+          x[q] = as_bits(__hmul2(s, __hsub2(as_pair(((codes[i] >> (4 * q)) & 0x000F000Fu) | 0x43004300u), z)));
+        *at_row[i] = make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                                __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
       }
     }
   }
@@ -164,8 +178,17 @@ static_assert(kPageTokens == 32, "slot >> 5 is the page");
 
 template <bool APPEND, int DH, int DV>
 cudaError_t launch_io_t(const CacheIoParams& p, cudaStream_t stream) {
-  const int units = p.Hkv * ((DH + DV) / 8);        // a multiple of 16
-  const dim3 block(static_cast<unsigned>(std::min(units, kThreads)), static_cast<unsigned>(std::max(1, kThreads / units)));
+  // Blocks of whole warps: several tokens of all units where that fits, else
+  // the units rounded up.  Units are a multiple of 8, so the eight lanes of a
+  // group are the same token's.
+  const int units = p.Hkv * ((DH + DV) / 8);
+  int x = std::min(units, kThreads), y = kThreads / x;
+  while (x * y % 32 != 0 && y > 0) --y;
+  if (y == 0) {
+    x = (x + 31) / 32 * 32;
+    y = std::max(1, kThreads / x);
+  }
+  const dim3 block(static_cast<unsigned>(x), static_cast<unsigned>(y));
   // kTokens tokens a thread once there are enough to fill the GPU.
   const int64_t rows = (p.tokens + block.y - 1) / block.y, want = std::max<int64_t>((rows + kTokens - 1) / kTokens, 152 * 4);
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(std::min(rows, want), 152 * 64)),

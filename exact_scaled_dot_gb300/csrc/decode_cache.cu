@@ -341,11 +341,11 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     // O^T before the zero points, [group][dim pair i][(dim, row), (dim, row + 1),
     // 16 (dim + 1, row), 16 (dim + 1, row + 1)], and what they take off.
     float o[NT][GV][4][4], oz[NT][GV][2];
-    float m_ref[NT][2], l_sum[NT][2];
+    float m_ref[NT][2], l_sum[NT][2], shift[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) m_ref[nt][k] = kNoKey, l_sum[nt][k] = 0.f;
+      for (int k = 0; k < 2; ++k) m_ref[nt][k] = kNoKey, shift[nt][k] = -kNoKey, l_sum[nt][k] = 0.f;
 #pragma unroll
       for (int gv = 0; gv < GV; ++gv)
 #pragma unroll
@@ -357,6 +357,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     }
     int e_ref = -100;                // the weights carry 2^(6 - e_ref)
     float s_lim = exp2_int(-100);    // 2^e_ref: above every scale so far
+    float most = 114.f;              // 14 - e_ref
     // Which key of a 16-key block fragment row m (and m + 8) stands for: rows
     // 4q + 2 and 4q + 3 are swapped, so that the four lanes t of one V load
     // read keys of both parities (rows of 64 bytes: both halves of the banks).
@@ -441,14 +442,16 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
             }
         }
         // ---- running maximum (lazy) and the weights' scale ----
+        // The weights' exponents are s f + shift, shift = 6 - e_ref - (the
+        // reference maximum); none may reach 14 - e_ref.
         bool need = false;
         float mx[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            mx[nt][k] = fmaxf(fmaxf(s[0][nt][k], s[0][nt][2 + k]), fmaxf(s[1][nt][k], s[1][nt][2 + k])) * f[nt][k];
-            need |= mx[nt][k] > m_ref[nt][k] + 8.0f;
+            mx[nt][k] = fmaxf(fmaxf(s[0][nt][k], s[0][nt][2 + k]), fmaxf(s[1][nt][k], s[1][nt][2 + k]));
+            need |= fmaf(mx[nt][k], f[nt][k], shift[nt][k]) > most;
           }
         float smax = 0.f;
 #pragma unroll
@@ -462,8 +465,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
           e = e > 126 ? 126 : (e < e_ref ? e_ref : e);
           const int de = e_ref - e < -126 ? -126 : e_ref - e;
           const float back = exp2_int(de);
+          const float e_step = static_cast<float>(e_ref - e);
           e_ref = e;
           s_lim = exp2_int(e);
+          most = static_cast<float>(14 - e);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -472,12 +477,14 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-              float alpha = 1.f;
-              if (m > m_ref[nt][k] + 8.0f) {
-                alpha = fast_exp2(m_ref[nt][k] - m);
+              m *= f[nt][k];
+              shift[nt][k] += e_step;
+              float alpha = back;
+              if (m + shift[nt][k] > most) {
+                alpha *= fast_exp2(m_ref[nt][k] - m);
                 m_ref[nt][k] = m;
+                shift[nt][k] = static_cast<float>(6 - e) - m;
               }
-              alpha *= back;
               l_sum[nt][k] *= alpha;
 #pragma unroll
               for (int gv = 0; gv < GV; ++gv) {
@@ -491,19 +498,18 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
             }
         }
         // ---- weights and O^T += V^T P^T ----
-        const float shift = static_cast<float>(6 - e_ref);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           uint32_t bw[NT][GV][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float n0 = shift - m_ref[nt][0], n1 = shift - m_ref[nt][1];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const float p0 = fast_exp2(fmaf(s[kb][nt][2 * hf], f[nt][0], n0));
-              const float p1 = fast_exp2(fmaf(s[kb][nt][2 * hf + 1], f[nt][1], n1));
-              l_sum[nt][0] += p0;
-              l_sum[nt][1] += p1;
+              float p0, p1;
+              ffma2(p0, p1, s[kb][nt][2 * hf], s[kb][nt][2 * hf + 1], f[nt][0], f[nt][1], shift[nt][0], shift[nt][1]);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              fadd2(l_sum[nt][0], l_sum[nt][1], p0, p1);
 #pragma unroll
               for (int gv = 0; gv < GV; ++gv) {
                 const float sc = __uint_as_float(vw[kb][hf][gv]);

@@ -182,6 +182,8 @@ CASES = {
     "one_key": ([1], 1, 1, 1, 64, 64),
     "page_ends": ([31, 32, 33, 63, 64, 65], 8, 2, 1, 128, 128),
     "no_key": ([0, 5, 0, 40], 4, 2, 1, 128, 64),
+    "no_key_at_all": ([0, 0, 0], 4, 2, 1, 64, 64),
+    "one_page_of_many_sequences": ([5, 31, 32, 1, 0, 17, 30, 2, 9, 12, 3, 0, 0, 28, 6, 7, 8] * 4, 4, 2, 1, 64, 64),
     "rows_before_the_first_token": ([1, 2, 3, 300], 6, 2, 4, 64, 64),
     "group_5_of_3_queries": ([17, 450, 129], 10, 2, 3, 128, 128),
     "nine_rows": ([500, 31], 9, 1, 1, 128, 128),

@@ -14,10 +14,16 @@
 // the ties back where they are and moves nothing else across one; adding and
 // subtracting 1.5 2^23 then rounds to the integer, ties to even.
 //
-// Both directions are bound by DRAM (2 bytes per element on one side and
-// 0.5625 on the other).  A lane owns 8 elements: one 16-byte access of the
-// bf16 row and one 32-bit word of codes; 8 lanes are a group.  A thread keeps
-// its place in the token's rows (head, tensor, chunk) and walks over tokens.
+// Both directions move 2 bytes per element on one side and 0.5625 on the
+// other.  A lane owns 8 elements of K's row and 8 of V's: one 16-byte access of
+// the bf16 row and one 32-bit word of codes each; 8 lanes are a group.  A
+// thread keeps its place in the token's rows (head, chunk) and walks over
+// tokens, so that what the two share (slot, page, offsets) is worked out once.
+//
+// Measured (GB300, 16384 tokens, 8 heads, widths 128): writing and reading
+// back 36 us, 71 % of the measured copy rate.  What bounds the write is the
+// integer pipe (68 % of its cycles busy: range, rounding and packing of each
+// element, some 15 instructions), not DRAM.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -32,9 +38,9 @@ namespace {
 
 constexpr int kThreads = 256;
 // Tokens that a thread has in flight once there are enough to fill the GPU
-// (16384 tokens, 8 heads, widths 128, writing and reading: 44, 39 and 46 us
-// with 2, 4 and 8); with fewer, one token a thread.
-constexpr int kMostTokens = 4;
+// (16384 tokens, 8 heads, widths 128, writing and reading back: 39.7, 36.0,
+// 36.6 and 36.9 us with 1, 2, 3 and 4); with fewer, one token a thread.
+constexpr int kMostTokens = 2;
 
 constexpr float kToGrid = 6144.0f;          // 1.5 2^12: sums near it are multiples of 2^-11
 constexpr float kToInteger = 12582912.0f;   // 1.5 2^23: sums near it are integers
@@ -93,49 +99,57 @@ __device__ __forceinline__ void quantize8(uint4 v, uint32_t& codes, uint32_t& wo
   word |= __float_as_uint(z + 8388608.0f) & 0xFFu;
 }
 
-// Blocks of (units, tokens) threads: unit u of a token counts the 8-element
-// chunks of K and V of head 0, head 1, ...; blockIdx.y continues the units.
+// Eight elements as bf16: 128 + code less 128 + z, exact, times s, rounded once.
+__device__ __forceinline__ uint4 dequantize8(uint32_t codes, uint32_t word) {
+  const __nv_bfloat162 z = as_pair(0x43004300u | __byte_perm(word, 0u, 0x4040));
+  const __nv_bfloat162 s = as_pair(__byte_perm(word, 0u, 0x3232));
+  uint32_t x[4];       // elements (k, k + 4)
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    x[k] = as_bits(__hmul2(s, __hsub2(as_pair(((codes >> (4 * k)) & 0x000F000Fu) | 0x43004300u), z)));
+  return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                    __byte_perm(x[2], x[3], 0x7632));
+}
+
+// Blocks of (units, tokens) threads: a unit is an 8-element chunk of one head,
+// of K's row and (where V's is as wide) of V's; blockIdx.y continues the units.
 template <bool APPEND, int DH, int DV, int kTokens>
 __global__ void __launch_bounds__(kThreads) cache_io_kernel(const __grid_constant__ CacheIoParams p) {
-  constexpr int kPer = (DH + DV) / 8;
+  constexpr int kPer = DH / 8;
+  static_assert(DV <= DH, "V's chunks are among K's");
   const int u = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x);
   const bool on = u < p.Hkv * kPer;
-  // This thread's head, tensor (K or V) and chunk, and where they are in a
-  // token's row and, at place 0, in a page (a page is below 2^32 bytes).
   const int h = on ? u / kPer : 0;
-  const int k = on ? u - h * kPer : 0;
-  const bool val = k >= DH / 8;
-  const int c = k - (val ? DH / 8 : 0);
+  const int c = on ? u - h * kPer : 0;
+  const bool on_v = on && c < DV / 8;
+  // Where the chunk is in a token's rows and, at place 0, in a page (a page is
+  // below 2^32 bytes).
   const uint32_t page_stride = static_cast<uint32_t>(p.Hkv) * page_head_bytes(DH, DV);
-  uint8_t* const codes0 = p.pool + static_cast<int64_t>(h) * page_head_bytes(DH, DV) +
-                          (val ? off_v_codes(DH) : off_k_codes()) + 4 * c;
-  const int to_words = (val ? off_v_words(DH, DV) - off_v_codes(DH) : off_k_words(DH, DV)) + 4 * (c >> 3) - 4 * c;
-  const int code_row = (val ? DV : DH) / 2, word_row = (val ? DV : DH) / 16;
-  const TensorStrides& st = val ? p.sv : p.sk;
+  uint8_t* const head0 = p.pool + static_cast<int64_t>(h) * page_head_bytes(DH, DV) + 4 * c;
+  const int word_of_chunk = 4 * (c >> 3) - 4 * c;
   // Tokens of the thread: t, t + step, ...  The warps go through the loop
   // together (quantize8's sums over lanes), tokens past the end left out.
   const uint32_t tokens = static_cast<uint32_t>(p.tokens), step = gridDim.x * blockDim.y;
   uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t row_step = st.row / 8 * step;
-  uint4* row = static_cast<uint4*>(const_cast<void*>(val ? p.V : p.K)) + h * (st.head / 8) + c + t * (st.row / 8);
+  const int64_t step_k = p.sk.row / 8 * step, step_v = p.sv.row / 8 * step;
+  uint4* row_k = static_cast<uint4*>(const_cast<void*>(p.K)) + h * (p.sk.head / 8) + c + t * (p.sk.row / 8);
+  uint4* row_v = static_cast<uint4*>(const_cast<void*>(p.V)) + h * (p.sv.head / 8) + c + t * (p.sv.row / 8);
   for (uint32_t t_block = blockIdx.x * blockDim.y; t_block < tokens; t_block += kTokens * step) {
-    bool here[kTokens];
     int64_t slot[kTokens];
-    uint4 v[kTokens];
-    uint4* at_row[kTokens];
+    uint4 v[kTokens][2];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-      here[i] = on && t < tokens;
-      at_row[i] = row;
-      slot[i] = here[i] ? p.slots[t] : -1;
-      if (APPEND) v[i] = here[i] ? *row : make_uint4(0u, 0u, 0u, 0u);
-      t += step;
-      row += row_step;
+      const bool here = on && t + i * step < tokens;
+      slot[i] = here ? p.slots[t + i * step] : -1;
+      if (APPEND) {
+        v[i][0] = here ? row_k[i * step_k] : make_uint4(0u, 0u, 0u, 0u);
+        v[i][1] = here && on_v ? row_v[i * step_v] : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
-    // Codes and words of the slots; a slot without a token (negative: padding;
-    // past the pool: recorded in the status word) has none.
-    uint32_t codes[kTokens], word[kTokens];
-    uint8_t* at[kTokens];    // the slot's codes
+    // Codes and words of the slots, K's and V's; a slot without a token
+    // (negative: padding; past the pool: recorded in the status word) has none.
+    uint32_t codes[kTokens][2], word[kTokens][2];
+    uint8_t* at[kTokens];    // the slot's page
     int off[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
@@ -144,35 +158,44 @@ __global__ void __launch_bounds__(kThreads) cache_io_kernel(const __grid_constan
         slot[i] = -1;
       }
       off[i] = static_cast<int>(slot[i]) & (kPageTokens - 1);
-      at[i] = codes0 + static_cast<uint64_t>(static_cast<uint32_t>(slot[i] >> 5)) * page_stride + off[i] * code_row;
+      at[i] = head0 + static_cast<uint64_t>(static_cast<uint32_t>(slot[i] >> 5)) * page_stride;
       if (!APPEND) {
-        codes[i] = word[i] = 0u;
+        codes[i][0] = word[i][0] = codes[i][1] = word[i][1] = 0u;
         if (slot[i] >= 0) {
-          codes[i] = *reinterpret_cast<const uint32_t*>(at[i]);
-          word[i] = *reinterpret_cast<const uint32_t*>(at[i] + to_words + off[i] * (word_row - code_row));
+          codes[i][0] = *reinterpret_cast<const uint32_t*>(at[i] + off_k_codes() + off[i] * (DH / 2));
+          word[i][0] = *reinterpret_cast<const uint32_t*>(at[i] + off_k_words(DH, DV) + word_of_chunk + off[i] * (DH / 16));
+          if (on_v) {
+            codes[i][1] = *reinterpret_cast<const uint32_t*>(at[i] + off_v_codes(DH) + off[i] * (DV / 2));
+            word[i][1] =
+                *reinterpret_cast<const uint32_t*>(at[i] + off_v_words(DH, DV) + word_of_chunk + off[i] * (DV / 16));
+          }
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
       if (APPEND) {
-        quantize8(v[i], codes[i], word[i]);
+        quantize8(v[i][0], codes[i][0], word[i][0]);
+        quantize8(v[i][1], codes[i][1], word[i][1]);
         if (slot[i] >= 0) {
-          *reinterpret_cast<uint32_t*>(at[i]) = codes[i];
-          if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(at[i] + to_words + off[i] * (word_row - code_row)) = word[i];
+          const bool first = (c & 7) == 0;
+          *reinterpret_cast<uint32_t*>(at[i] + off_k_codes() + off[i] * (DH / 2)) = codes[i][0];
+          if (first)
+            *reinterpret_cast<uint32_t*>(at[i] + off_k_words(DH, DV) + word_of_chunk + off[i] * (DH / 16)) = word[i][0];
+          if (on_v) {
+            *reinterpret_cast<uint32_t*>(at[i] + off_v_codes(DH) + off[i] * (DV / 2)) = codes[i][1];
+            if (first)
+              *reinterpret_cast<uint32_t*>(at[i] + off_v_words(DH, DV) + word_of_chunk + off[i] * (DV / 16)) = word[i][1];
+          }
         }
-      } else if (here[i]) {
-        // As bf16: 128 + code less 128 + z, exact, times s, rounded once.
-        const __nv_bfloat162 z = as_pair(0x43004300u | __byte_perm(word[i], 0u, 0x4040));
-        const __nv_bfloat162 s = as_pair(__byte_perm(word[i], 0u, 0x3232));
-        uint32_t x[4];       // elements (k, k + 4)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          x[q] = as_bits(__hmul2(s, __hsub2(as_pair(((codes[i] >> (4 * q)) & 0x000F000Fu) | 0x43004300u), z)));
-        *at_row[i] = make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
-                                __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+      } else if (on && t + i * step < tokens) {
+        row_k[i * step_k] = dequantize8(codes[i][0], word[i][0]);
+        if (on_v) row_v[i * step_v] = dequantize8(codes[i][1], word[i][1]);
       }
     }
+    t += kTokens * step;
+    row_k += kTokens * step_k;
+    row_v += kTokens * step_v;
   }
 }
 static_assert(kPageTokens == 32, "slot >> 5 is the page");
@@ -184,7 +207,7 @@ cudaError_t launch_io_t(const CacheIoParams& p, cudaStream_t stream) {
   // Blocks of whole warps: several tokens of all units where that fits, else
   // the units rounded up.  Units are a multiple of 8, so the eight lanes of a
   // group are the same token's.
-  const int units = p.Hkv * ((DH + DV) / 8);
+  const int units = p.Hkv * (DH / 8);
   int x = std::min(units, kThreads), y = kThreads / x;
   while (x * y % 32 != 0 && y > 0) --y;
   if (y == 0) {

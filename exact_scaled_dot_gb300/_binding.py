@@ -850,6 +850,13 @@ def attn_rope_qk(Q, K, positions, *, base: float = 10000.0, inverse: bool = Fals
 # ---------------------------------------------------------------------------
 # Query/key norm and rotation over several position axes (token-major rows)
 # ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=64)
+def _axes_bytes(base, sections, restart):
+    """attn_rotary_axes without its positions."""
+    return bytes(AttnRotaryAxes(base, len(sections), (ctypes.c_int32 * ATTN_MAX_AXES)(*sections), 1 if restart else 0,
+                                None))
+
+
 class RotaryAxes:
     """Rotary position embedding over one to three position axes
     (attn_rotary_axes): positions is an int32 device tensor [axes, tokens]
@@ -873,24 +880,23 @@ class RotaryAxes:
         if not 1 <= n <= ATTN_MAX_AXES:
             raise ValueError(f"sections must name 1 to {ATTN_MAX_AXES} axes")
         _check_flat(pos, "positions", torch.int32, (tokens,) if n == 1 and pos.dim() == 1 else (n, tokens), device)
-        r = AttnRotaryAxes(self.base, n, (ctypes.c_int32 * ATTN_MAX_AXES)(*sections), 1 if self.restart else 0,
-                           pos.data_ptr())
+        r = AttnRotaryAxes.from_buffer_copy(_axes_bytes(self.base, sections, self.restart))
+        r.pos = pos.data_ptr()
         return ctypes.byref(r)
 
 
-def _launch(dev, stream, body):
-    """body(stream handle) with its allocations and launches on the caller's
-    stream (so that the allocator ties the outputs and workspaces made here to
-    the work that uses them) and on the tensors' device, which need not be the
-    current one.  The common case, neither differing from the current ones,
-    enters no context: these calls may take less time on the GPU than that."""
-    if stream is None:
-        if dev.index == torch._C._cuda_getDevice():
-            return body(torch._C._cuda_getCurrentRawStream(dev.index))
-        with torch.cuda.device(dev):
-            return body(torch._C._cuda_getCurrentRawStream(dev.index))
-    with torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
+def _elsewhere(dev, stream):
+    """The context that a call has to enter to allocate and launch on the
+    caller's stream (so that the allocator ties the outputs and workspaces made
+    here to the work that uses them) and on the tensors' device, which need not
+    be the current one; None when both are the current ones.  A call enters it
+    and starts over: these calls may take less time on the GPU than contexts
+    and closures do here."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream must be of the tensors' device {dev}, got {stream.device}")
+        return torch.cuda.stream(stream)
+    return None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -985,15 +991,15 @@ def attn_rope_axes(Q, K, rotary: RotaryAxes, *, inverse: bool = False, Yq=None, 
     inverse=True turns back (the gradient map).  Views with contiguous rows
     are read and written in place; Yq may be Q and Yk may be K."""
     T, Hq, Hk, d, dev = _qk_dims(Q, K)
-
-    def body(st):
-        yq, yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
-        _check(load().attn_rope_axes(T, Hq, Hk, d, rotary.arg(T, d, dev), 1 if inverse else 0,
-                                     _stride_arg(AttnQkStrides, _FWD_FIELDS, Q, K, yq, yk), _addr(Q), _addr(K),
-                                     _addr(yq), _addr(yk), st), "attn_rope_axes")
-        return yq, yk
-
-    return _launch(dev, stream, body)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_rope_axes(Q, K, rotary, inverse=inverse, Yq=Yq, Yk=Yk)
+    Yq, Yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
+    _check(load().attn_rope_axes(T, Hq, Hk, d, rotary.arg(T, d, dev), 1 if inverse else 0,
+                                 _stride_arg(AttnQkStrides, _FWD_FIELDS, Q, K, Yq, Yk), _addr(Q), _addr(K), _addr(Yq),
+                                 _addr(Yk), torch._C._cuda_getCurrentRawStream(dev.index)), "attn_rope_axes")
+    return Yq, Yk
 
 
 def attn_qk_norm_rope(Q, K, gq=None, gk=None, rotary: Optional[RotaryAxes] = None, *, eps: float = 1e-6, Yq=None,
@@ -1002,19 +1008,21 @@ def attn_qk_norm_rope(Q, K, gq=None, gk=None, rotary: Optional[RotaryAxes] = Non
     K [tokens, Hkv, d] (or None), times the bf16 weights gq, gk [d] (None:
     ones), then the rotation (None: none), in one pass; returns (Yq, Yk)."""
     T, Hq, Hk, d, dev = _qk_dims(Q, K)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_qk_norm_rope(Q, K, gq, gk, rotary, eps=eps, Yq=Yq, Yk=Yk)
     _check_weight(gq, "gq", d, dev, Q)
     _check_weight(gk, "gk", d, dev, K)
-
-    def body(st):
-        yq, yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
-        _check(load().attn_qk_norm_rope(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
-                                        _stride_arg(AttnQkStrides, _FWD_FIELDS, Q, K, yq, yk), _addr(Q), _addr(K),
-                                        _addr(gq), _addr(gk), _addr(yq), _addr(yk), st), "attn_qk_norm_rope")
-        return yq, yk
-
-    return _launch(dev, stream, body)
+    Yq, Yk = _rows_like(Yq, "Yq", Q, dev), _rows_like(Yk, "Yk", K, dev)
+    _check(load().attn_qk_norm_rope(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
+                                    _stride_arg(AttnQkStrides, _FWD_FIELDS, Q, K, Yq, Yk), _addr(Q), _addr(K),
+                                    _addr(gq), _addr(gk), _addr(Yq), _addr(Yk),
+                                    torch._C._cuda_getCurrentRawStream(dev.index)), "attn_qk_norm_rope")
+    return Yq, Yk
 
 
+@functools.lru_cache(maxsize=256)
 def attn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hkv, d) -> int:
     return int(load().attn_qk_norm_rope_bwd_workspace_bytes(int(tokens), int(Hq), int(Hkv), int(d)))
 
@@ -1025,6 +1033,11 @@ def attn_qk_norm_rope_bwd(Q, K, gq, gk, dYq, dYk, rotary: Optional[RotaryAxes] =
     and eps: returns (dQ, dK) in bf16 and (dgq, dgk) in fp32 [d] (None for a
     weight that is None)."""
     T, Hq, Hk, d, dev = _qk_dims(Q, K)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_qk_norm_rope_bwd(Q, K, gq, gk, dYq, dYk, rotary, eps=eps, dQ=dQ, dK=dK, dgq=dgq, dgk=dgk,
+                                         workspace=workspace)
     _check_weight(gq, "gq", d, dev, Q)
     _check_weight(gk, "gk", d, dev, K)
     _check_rows(dYq, "dYq", (T, Hq, d), dev)
@@ -1032,23 +1045,18 @@ def attn_qk_norm_rope_bwd(Q, K, gq, gk, dYq, dYk, rotary: Optional[RotaryAxes] =
         _check_rows(dYk, "dYk", (T, Hk, d), dev)
     elif dYk is not None:
         raise ValueError("dYk was given without its input")
-
-    def body(st):
-        lib = load()
-        dq, dk = _rows_like(dQ, "dQ", Q, dev), _rows_like(dK, "dK", K, dev)
-        wq, wk = _weight_grad(dgq, "dgq", gq, d, dev), _weight_grad(dgk, "dgk", gk, d, dev)
-        ws = workspace
-        if ws is None:
-            need = lib.attn_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d)
-            ws = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
-        _check(lib.attn_qk_norm_rope_bwd(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
-                                         _stride_arg(AttnQkStrides, _BWD_FIELDS, Q, K, dYq, dYk, dq, dk), _addr(Q),
-                                         _addr(K), _addr(gq), _addr(gk), _addr(dYq), _addr(dYk), _addr(dq), _addr(dk),
-                                         _addr(wq), _addr(wk), ws.data_ptr(), ws.numel() * ws.element_size(), st),
-               "attn_qk_norm_rope_bwd")
-        return dq, dk, wq, wk
-
-    return _launch(dev, stream, body)
+    dQ, dK = _rows_like(dQ, "dQ", Q, dev), _rows_like(dK, "dK", K, dev)
+    dgq, dgk = _weight_grad(dgq, "dgq", gq, d, dev), _weight_grad(dgk, "dgk", gk, d, dev)
+    if workspace is None:
+        need = attn_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d)
+        workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+    _check(load().attn_qk_norm_rope_bwd(T, Hq, Hk, d, eps, None if rotary is None else rotary.arg(T, d, dev),
+                                        _stride_arg(AttnQkStrides, _BWD_FIELDS, Q, K, dYq, dYk, dQ, dK), _addr(Q),
+                                        _addr(K), _addr(gq), _addr(gk), _addr(dYq), _addr(dYk), _addr(dQ), _addr(dK),
+                                        _addr(dgq), _addr(dgk), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(),
+                                        torch._C._cuda_getCurrentRawStream(dev.index)), "attn_qk_norm_rope_bwd")
+    return dQ, dK, dgq, dgk
 
 
 # ---------------------------------------------------------------------------
@@ -1098,12 +1106,13 @@ def attn_cache_append(cache: QuantCache, K, V, slots, *, stream=None) -> None:
     _check_rows(K, "K", (T, cache.Hkv, cache.d_h), dev)
     _check_rows(V, "V", (T, cache.Hkv, cache.d_v), dev)
     _check_flat(slots, "slots", torch.int64, (T,), dev)
-
-    def body(st):
-        _check(load().attn_cache_append(cache.arg(), T, _stride_arg(AttnStrides, _KV_FIELDS, K, V), slots.data_ptr(),
-                                        K.data_ptr(), V.data_ptr(), st), "attn_cache_append")
-
-    _launch(dev, stream, body)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_cache_append(cache, K, V, slots)
+    _check(load().attn_cache_append(cache.arg(), T, _stride_arg(AttnStrides, _KV_FIELDS, K, V), slots.data_ptr(),
+                                    K.data_ptr(), V.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index)),
+           "attn_cache_append")
 
 
 def attn_cache_read(cache: QuantCache, slots, *, K=None, V=None, stream=None):
@@ -1113,20 +1122,27 @@ def attn_cache_read(cache: QuantCache, slots, *, K=None, V=None, stream=None):
     dev = cache.device
     T = slots.shape[0] if slots.dim() == 1 else -1
     _check_flat(slots, "slots", torch.int64, (T,), dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_cache_read(cache, slots, K=K, V=V)
     ks, vs = (T, cache.Hkv, cache.d_h), (T, cache.Hkv, cache.d_v)
+    K = torch.empty(ks, dtype=torch.bfloat16, device=dev) if K is None else _check_rows(K, "K", ks, dev)
+    V = torch.empty(vs, dtype=torch.bfloat16, device=dev) if V is None else _check_rows(V, "V", vs, dev)
+    _check(load().attn_cache_read(cache.arg(), T, _stride_arg(AttnStrides, _KV_FIELDS, K, V), slots.data_ptr(),
+                                  K.data_ptr(), V.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index)),
+           "attn_cache_read")
+    return K, V
 
-    def body(st):
-        k = torch.empty(ks, dtype=torch.bfloat16, device=dev) if K is None else _check_rows(K, "K", ks, dev)
-        v = torch.empty(vs, dtype=torch.bfloat16, device=dev) if V is None else _check_rows(V, "V", vs, dev)
-        _check(load().attn_cache_read(cache.arg(), T, _stride_arg(AttnStrides, _KV_FIELDS, k, v), slots.data_ptr(),
-                                      k.data_ptr(), v.data_ptr(), st), "attn_cache_read")
-        return k, v
 
-    return _launch(dev, stream, body)
+@functools.lru_cache(maxsize=256)
+def _decode_cache_bytes(Hkv, d_h, d_v, pages, B, Hq, n_q, max_pages) -> int:
+    cache = AttnCache(Hkv, d_h, d_v, pages, None)
+    return int(load().attn_fwd_decode_cache_workspace_bytes(ctypes.byref(cache), B, Hq, n_q, max_pages))
 
 
 def attn_fwd_decode_cache_workspace_bytes(cache: QuantCache, B, Hq, n_q, max_pages) -> int:
-    return int(load().attn_fwd_decode_cache_workspace_bytes(cache.arg(), int(B), int(Hq), int(n_q), int(max_pages)))
+    return _decode_cache_bytes(cache.Hkv, cache.d_h, cache.d_v, cache.pages, int(B), int(Hq), int(n_q), int(max_pages))
 
 
 def attn_fwd_decode_cache(Q, cache: QuantCache, page_table, lengths, *, scale: Optional[float] = None, O=None,
@@ -1144,23 +1160,21 @@ def attn_fwd_decode_cache(Q, cache: QuantCache, page_table, lengths, *, scale: O
     _check_flat(Q, "Q", torch.bfloat16, (B, Hq, n_q, cache.d_h), dev)
     _check_flat(page_table, "page_table", torch.int32, (B, max_pages), dev)
     _check_flat(lengths, "lengths", torch.int32, (B,), dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_fwd_decode_cache(Q, cache, page_table, lengths, scale=scale, O=O, LSE=LSE, workspace=workspace)
     scale = 1.0 / math.sqrt(d_h) if scale is None else float(scale)
     os, ls = (B, Hq, n_q, cache.d_v), (B, Hq, n_q)
-
-    def body(st):
-        lib = load()
-        o = torch.empty(os, dtype=torch.bfloat16, device=dev) if O is None else _check_flat(O, "O", torch.bfloat16, os, dev)
-        lse = torch.empty(ls, dtype=torch.float32, device=dev) if LSE is None else _check_flat(LSE, "LSE", torch.float32,
-                                                                                             ls, dev)
-        ws, size = workspace, 0
-        if ws is None:
-            size = lib.attn_fwd_decode_cache_workspace_bytes(cache.arg(), B, Hq, n_q, max_pages)
-            ws = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
-        else:
-            size = ws.numel() * ws.element_size()
-        _check(lib.attn_fwd_decode_cache(cache.arg(), B, Hq, n_q, max_pages, scale, Q.data_ptr(),
-                                         page_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                         _addr(ws), size, st), "attn_fwd_decode_cache")
-        return o, lse
-
-    return _launch(dev, stream, body)
+    O = torch.empty(os, dtype=torch.bfloat16, device=dev) if O is None else _check_flat(O, "O", torch.bfloat16, os, dev)
+    LSE = (torch.empty(ls, dtype=torch.float32, device=dev) if LSE is None
+           else _check_flat(LSE, "LSE", torch.float32, ls, dev))
+    if workspace is None:
+        size = _decode_cache_bytes(cache.Hkv, cache.d_h, cache.d_v, cache.pages, B, Hq, n_q, max_pages)
+        workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _check(load().attn_fwd_decode_cache(cache.arg(), B, Hq, n_q, max_pages, scale, Q.data_ptr(), page_table.data_ptr(),
+                                        lengths.data_ptr(), O.data_ptr(), LSE.data_ptr(), _addr(workspace), size,
+                                        torch._C._cuda_getCurrentRawStream(dev.index)), "attn_fwd_decode_cache")
+    return O, LSE

@@ -350,13 +350,13 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
         }
       }
       const float r = inv_sqrt(fmaf(row_sum(sq), inv_d, p.eps));
-      const float m = row_sum(tx) * inv_d * r * r * r;      // dx = r t - m x
+      const float m = row_sum(tx) * inv_d * r * r;          // dx = r (t - m x); r^3 may pass fp32's range
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           dg[i][k] = fmaf(r, pr[i][k], dg[i][k]);
-          e[i][k] = fmaf(r * w[i][k], e[i][k], -(m * xv[i][k]));
+          e[i][k] = r * fmaf(w[i][k], e[i][k], -(m * xv[i][k]));
         }
         if (there && on[i] && at.h + j < part.n) row[j * dxh + 8 * i] = pack8(e[i]);
       }

@@ -169,6 +169,20 @@ def test_small_large_and_zero_rows():
     _check_backward(K, gk, dYk, dK, dgk, a, EPS, "keys")
 
 
+def test_rows_whose_cubed_norm_passes_fp32():
+    """r = 2^62: r^3 is beyond fp32, dx (some 2^68) is not."""
+    import exact_scaled_dot_gb300 as esd
+    eps = 2.0 ** -125
+    Q, K, gq, gk, dYq, dYk, a, rot = _inputs("odd_heads", seed=3)
+    Q = (Q.sign().double() * 2.0 ** -62).to(torch.bfloat16)
+    dYq = (dYq.double() * 64).to(torch.bfloat16)
+    dYq[3] = Q[3] * 2.0 ** 68
+    dQ, dK, dgq, dgk = esd.attn_qk_norm_rope_bwd(Q, K, gq, gk, dYq, dYk, rot, eps=eps)
+    torch.cuda.synchronize()
+    _check_backward(Q, gq, dYq, dQ, dgq, a, eps, "queries")
+    _check_backward(K, gk, dYk, dK, dgk, a, eps, "keys")
+
+
 def test_in_place_and_views_write_nothing_else():
     import exact_scaled_dot_gb300 as esd
     T, Hq, Hk, d = 75, 6, 2, 128

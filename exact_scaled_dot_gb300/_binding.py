@@ -295,6 +295,14 @@ def _check_tensor(t: torch.Tensor, name: str, dtype, shape: Tuple[int, ...], dev
         raise ValueError(f"{name} must be contiguous")
 
 
+def _not_expanded(row: int, head: int) -> Tuple[int, int]:
+    # To the library {0, 0} means contiguous: it would read past a row that
+    # stands for all.  (It refuses one zero by itself.)
+    if row == 0 and head == 0:
+        raise ValueError("a tensor that is one row expanded over rows and heads is not supported (copy it)")
+    return row, head
+
+
 def _padded_strides(t: torch.Tensor, name: str) -> Tuple[int, int]:
     """(row, head) element strides of a [B, H, n, d] view; its batch stride
     must be H times its head stride (size-1 dimensions are free)."""
@@ -305,14 +313,14 @@ def _padded_strides(t: torch.Tensor, name: str) -> Tuple[int, int]:
     if B > 1 and sB != H * head:
         raise ValueError(f"{name}: the batch stride must be H times the head stride (use the packed entry points "
                          f"for sequence-major tensors)")
-    return row, head
+    return _not_expanded(row, head)
 
 
 def _packed_strides(t: torch.Tensor) -> Tuple[int, int]:
     """(row = token, head) element strides of a [T, H, d] view."""
     T, H, d = t.shape
     row, head, _ = t.stride()
-    return (row if T > 1 else H * d), (head if H > 1 else d)
+    return _not_expanded(row if T > 1 else H * d, head if H > 1 else d)
 
 
 def _strides_arg(packed: bool, **tensors):
@@ -853,6 +861,8 @@ def attn_rope_qk(Q, K, positions, *, base: float = 10000.0, inverse: bool = Fals
 @functools.lru_cache(maxsize=64)
 def _axes_bytes(base, sections, restart):
     """attn_rotary_axes without its positions."""
+    if not all(0 < s < 2 ** 31 for s in sections):
+        raise ValueError(f"sections must be positive numbers of blocks, got {sections}")
     return bytes(AttnRotaryAxes(base, len(sections), (ctypes.c_int32 * ATTN_MAX_AXES)(*sections), 1 if restart else 0,
                                 None))
 

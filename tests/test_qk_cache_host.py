@@ -172,6 +172,22 @@ def test_binding_refuses():
         esd.attn_qk_norm_rope(cpu.float(), None)
     with pytest.raises(ValueError):
         esd.QuantCache(torch.zeros((4, 2, 100), dtype=torch.uint8), 64, 64)
+    # a count of blocks that would wrap in the library's 32 bits
+    with pytest.raises(ValueError):
+        esd._binding._axes_bytes(10000.0, (2 ** 32 + 8,), False)
+
+
+def test_one_row_expanded_is_refused():
+    """Strides {0, 0} mean contiguous to the library: a row that stands for all of them must not reach it."""
+    one = torch.zeros((64,), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        esd._binding._stride_arg(esd._binding.AttnQkStrides, ("q",), one.expand(4, 2, 64))
+    with pytest.raises(ValueError):
+        esd._binding._strides_arg(True, q=one.expand(4, 2, 64))
+    with pytest.raises(ValueError):
+        esd._binding._strides_arg(False, q=one.expand(3, 4, 2, 64))
+    # one zero alone is the library's to refuse; size-1 dimensions are free
+    assert esd._binding._packed_strides(one.expand(1, 1, 64)) == (64, 64)
 
 
 def test_reference_gradient_against_differences():

@@ -320,9 +320,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
           v[gk][w] = r < R ? q[gk * 8 + 2 * t + w] : make_uint4(0u, 0u, 0u, 0u);
           m = bf16_absmax_fold(m, v[gk][w]);
         }
-      float mx = bf16_absmax_value(m);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      uint32_t mb = __float_as_uint(bf16_absmax_value(m));     // (as bits, so that a NaN is the largest)
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+      const float mx = __uint_as_float(mb);
       // 2^14 <= mx 2^e < 2^15 (0 and non-finite rows: e = 0).
       int e = 0;
       if (mx > 0.f && mx < INFINITY) e = 14 - ilogbf(mx);
@@ -340,7 +341,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
           qf[nt][4 * gk + 2 * w + 1][1] = __byte_perm(u.y, u.w, 0x7632);
         }
       // The factors and limits of the rows this lane has in the accumulators.
-      const float fac = p.scale_log2 * exp2_int(-e) * 512.0f;
+      // Never 0, which a masked -inf must not meet; NaN for a row of Q with an
+      // infinity or a NaN, whose fp16 operands hide it.
+      float fac = fmaxf(p.scale_log2 * exp2_int(-e) * 512.0f, 0x1p-126f);
+      if (!(mx < INFINITY)) fac = __uint_as_float(0x7FC00000u);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         f[nt][k] = __shfl_sync(0xffffffffu, fac, (2 * t + k) * 4);
@@ -719,8 +723,8 @@ __global__ void __launch_bounds__(kThreads) decode_cache_merge_kernel(const __gr
 
 // Up to this many query rows, the merge gives each a block of its own: four
 // times the loads in flight for the many parts of few long sequences.
-// Measured: 256 rows of 8 long sequences, 4 us against 5; 3072 rows of 48
-// ragged ones, 6 us against 4 with a warp per row.
+// Measured: 8 long sequences of 32 rows, 4 us against 5; 48 ragged ones of 64
+// rows, 6 us against 4 with a warp per row.
 constexpr int kMergeBlockRows = 8 * 152;
 
 template <int DH, int DV, int NT>

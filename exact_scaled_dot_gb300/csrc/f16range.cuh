@@ -67,11 +67,12 @@ __device__ __forceinline__ float bf16_absmax_value(uint32_t m) {
 }
 
 // Record a device-side condition in the status word.  A wait that timed out
-// takes precedence over a range report, since it makes later kernels skip
-// their work; a range report only fills an empty word.
+// takes precedence over a range or page report, since it makes later kernels
+// skip their work; such a report only fills an empty word.
 __device__ __forceinline__ void record_status(unsigned int* status, unsigned int code) {
   const unsigned int old = atomicCAS(status, 0u, code);
-  if (code == static_cast<unsigned int>(ATTN_ERR_TIMEOUT) && old == static_cast<unsigned int>(ATTN_ERR_RANGE))
+  if (code == static_cast<unsigned int>(ATTN_ERR_TIMEOUT) &&
+      (old == static_cast<unsigned int>(ATTN_ERR_RANGE) || old == static_cast<unsigned int>(ATTN_ERR_PAGE)))
     atomicCAS(status, old, code);
 }
 

@@ -254,6 +254,47 @@ def test_query_scales(e):
     _attend_and_check(Q, cache, table, lens, vals, scale=2.0 ** -e / 8)
 
 
+def test_tiny_scale_beside_masked_keys():
+    """Scores that all vanish (the scale times the queries' own is below fp32's range): equal weights."""
+    rng = np.random.default_rng(34)
+    cache, table, lens, vals = _filled(rng, [200, 35], 2, 128, 64)
+    Q = (_bf16(rng, 2, 4, 3, 128).double() * 2.0 ** -115).to(torch.bfloat16)
+    _attend_and_check(Q, cache, table, lens, vals, scale=2.0 ** -40)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_a_query_row_that_is_not_finite_gives_nan_alone(value):
+    import exact_scaled_dot_gb300 as esd
+    rng = np.random.default_rng(35)
+    cache, table, lens, _ = _filled(rng, [3000, 35], 2, 128, 128)
+    Q = _bf16(rng, 2, 4, 2, 128).cuda()
+    O, LSE = esd.attn_fwd_decode_cache(Q, cache, table, lens)
+    Q[0, 1, 0, 77] = Q[1, 2, 1, 0] = value
+    O2, LSE2 = esd.attn_fwd_decode_cache(Q, cache, table, lens)
+    torch.cuda.synchronize()
+    assert esd.attn_get_status() == 0
+    row = torch.zeros((2, 4, 2), dtype=torch.bool, device="cuda")
+    row[0, 1, 0] = row[1, 2, 1] = True
+    assert O2[row].isnan().all() and LSE2[row].isnan().all()
+    assert torch.equal(O2[~row], O[~row]) and torch.equal(LSE2[~row], LSE[~row])
+
+
+def test_a_timeout_replaces_a_page_report():
+    """Only a timeout stops later calls, so it must not be lost behind an earlier report."""
+    import exact_scaled_dot_gb300 as esd
+    cache = esd.QuantCache.empty(1, 1, 64, 64)
+    cache.pool.zero_()
+    try:
+        esd.attn_cache_read(cache, torch.tensor([32], device="cuda"))
+        torch.cuda.synchronize()
+        assert esd.attn_get_status() == esd.ATTN_ERR_PAGE
+        esd.attn_selftest_wait_timeout(50_000_000)
+        torch.cuda.synchronize()
+        assert esd.attn_get_status() == esd.ATTN_ERR_TIMEOUT
+    finally:
+        esd.attn_clear_status()
+
+
 def test_shared_pages_and_a_wider_table():
     """Sequences that share their first pages (a forked prompt), in a table wider than any of them."""
     rng = np.random.default_rng(26)

@@ -1161,6 +1161,8 @@ def attn_fwd_decode_cache(Q, cache: QuantCache, page_table, lengths, *, scale: O
     page_table int32 [B, max_pages] and lengths int32 [B] on the device (the
     n_q new tokens counted).  Row i of sequence b sees the keys
     j <= lengths[b] - n_q + i; a row that sees none gets O = 0, LSE = -inf.
+    A narrow page table (max_pages of the longest sequence, not of the longest
+    possible) lets short sequences run without a workspace and a second launch.
     Returns (O [B, Hq, n_q, d_v] bf16, LSE [B, Hq, n_q] fp32)."""
     if Q.dim() != 4 or page_table.dim() != 2:
         raise ValueError("Q must be 4-D [B, Hq, n_q, d_h] and page_table 2-D [B, max_pages]")

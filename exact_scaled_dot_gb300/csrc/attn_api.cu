@@ -946,10 +946,24 @@ int cache_io(const attn_cache* c, int64_t tokens, const attn_strides* strides, c
 }
 
 // How attn_fwd_decode_cache divides the work: row tiles of 8 query rows (16
-// when a KV head has more), and as many ranges of the pages as CTAs of all
-// tiles are resident at once (fewer when there are few pages).
+// when a KV head has more), and of each either
+//   a CTA per sequence, when the page table is narrow: up to 24 pages, or up
+//   to as many as there are such CTAs, 64 at most (the length of a sequence
+//   that all others may have to wait for), or
+//   as many equal ranges of all pages as CTAs are resident at once (fewer when
+//   there are few pages), and a merge of the sequences that ranges share.
+// Few CTAs of the first kind have eight warps.  Measured, ranges against whole
+// sequences (one KV head of 8 query rows unless given, widths 128):
+//   1 sequence of 8, 24, 32 pages: 7.5, 7.7, 7.9 us against 5.1, 7.5, 8.4
+//   64 of 32, 64: 11.2, 15.5 against 8.7, 13.0
+//   64 of 16, 64, 8 KV heads: 18.9, 41.4 against 12.9, 36.9
+// and one launch less for the host (20 us a call against 14).  Eight warps
+// against four: 1 sequence of 24 pages 7.5 us against 8.6, but 608 CTAs of 16
+// pages 22 us against 13.
+constexpr int kFewPages = 24, kManyPages = 64;
 struct DecodeCachePlan {
   int tile_rows, chunks, ranges;
+  bool whole_seqs, wide;
   size_t opart_bytes, lpart_bytes, bytes;
 };
 
@@ -962,10 +976,14 @@ DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
   const int64_t resident = 152 * (d.tile_rows == 8 ? kDecodeCacheResident8 : kDecodeCacheResident16);
   const int64_t most = (static_cast<int64_t>(B) * max_pages + kMinRangePages - 1) / kMinRangePages;
   d.ranges = static_cast<int>(std::max<int64_t>(1, std::min(resident / tiles, most)));
+  const int64_t ctas = tiles * B;
+  d.whole_seqs = d.ranges == 1 || max_pages <= std::min<int64_t>(std::max<int64_t>(ctas, kFewPages), kManyPages);
+  d.wide = d.whole_seqs && max_pages > kDecodeCacheWarps && ctas <= 152;
+  if (d.whole_seqs) d.ranges = B;
   const size_t rows = static_cast<size_t>(tiles) * d.ranges * 2 * d.tile_rows;
   d.opart_bytes = round256(rows * c->d_v * sizeof(float));
   d.lpart_bytes = round256(rows * sizeof(float));
-  d.bytes = d.ranges > 1 ? d.opart_bytes + d.lpart_bytes + round256((static_cast<size_t>(B) + 2) * sizeof(int32_t)) : 0;
+  d.bytes = !d.whole_seqs ? d.opart_bytes + d.lpart_bytes + round256((static_cast<size_t>(B) + 2) * sizeof(int32_t)) : 0;
   return d;
 }
 
@@ -1897,6 +1915,8 @@ int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
   p.tile_rows = plan.tile_rows;
   p.chunks = plan.chunks;
   p.ranges = plan.ranges;
+  p.whole_seqs = plan.whole_seqs;
+  p.wide = plan.wide;
   p.status = status;
   const cudaError_t e = launch_decode_cache(cache->d_h, cache->d_v, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -346,9 +346,11 @@ struct CacheIoParams {
   unsigned int* status;
 };
 
-// Attention over the 4-bit cache (decode_cache.cu): resident CTAs per SM of
-// the kernels for 8 and 16 query rows, and the fewest pages that a CTA takes
-// (one per warp).
+// Attention over the 4-bit cache (decode_cache.cu): warps of a CTA, resident
+// CTAs per SM of the kernels for 8 and 16 query rows, and the fewest pages
+// that a CTA takes (one per warp).  The wide kernel has a CTA per SM.
+constexpr int kDecodeCacheWarps = 4;
+constexpr int kDecodeCacheWideWarps = 8;
 constexpr int kDecodeCacheResident8 = 4;
 constexpr int kDecodeCacheResident16 = 3;
 constexpr int kMinRangePages = 4;
@@ -364,14 +366,16 @@ struct DecCacheParams {
   const void* Q;               // bf16 [B][Hq][n_q][d_h]
   void* O;                     // bf16 [B][Hq][n_q][d_v]
   float* LSE;                  // fp32 [B][Hq][n_q]
-  // Parts of sequences that several ranges share (ranges > 1), of row tile
+  // Parts of sequences that several ranges share (not whole_seqs), of row tile
   // tile and range i: 2 i (the sequence that the range begins in) and 2 i + 1.
   float* Opart;                // fp32 [Hkv chunks][ranges][2][tile_rows][d_v]
   float* Lpart;                // fp32 [Hkv chunks][ranges][2][tile_rows]
-  int32_t* first_page;         // pages of a range, then [B + 1] each sequence's first page (ranges > 1)
+  int32_t* first_page;         // pages of a range, then [B + 1] each sequence's first page (not whole_seqs)
   int32_t tile_rows;           // query rows of one CTA: 8 or 16
   int32_t chunks;              // row tiles per KV head
   int32_t ranges;              // CTAs of one row tile, over the pages of all sequences
+  int32_t whole_seqs;          // 1: each takes one whole sequence (ranges = B) and there is no merge
+  int32_t wide;                // 1: kDecodeCacheWideWarps warps each
   unsigned int* status;
 };
 

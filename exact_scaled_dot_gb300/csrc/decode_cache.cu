@@ -39,15 +39,16 @@
 // rescaled when e grows.  Weights down to 2^-20 of the largest keep 11 bits.
 // Sums, maxima and O are fp32.
 //
-// Work: for one (KV head, row tile), the pages of all sequences, one after
-// the other, are cut into equal ranges, one per CTA (the lengths are on the
-// device, so each CTA finds its range from them), and the CTAs of all tiles
-// are resident at once: no CTA waits for a place, and ragged lengths cost
-// nothing.  A CTA's 4 warps take every fourth page of a sequence, each with a
-// ring of pages of its own (one bulk copy per page) and its own softmax
-// state, and merge at the sequence's end.  A sequence that lies in one range
-// is written out directly; the others' parts are joined by the merge kernel
-// by their log-sum-exp, as in the decode forward.
+// Work: for one (KV head, row tile), short sequences get a CTA each.  Else the
+// pages of all sequences, one after the other, are cut into equal ranges, one
+// per CTA (the lengths are on the device, so each CTA finds its range from
+// them), and the CTAs of all tiles are resident at once: no CTA waits for a
+// place, and ragged lengths cost nothing.  A CTA's warps take every fourth
+// (eighth) page of a sequence, each with a ring of pages of its own (one bulk
+// copy per page) and its own softmax state, and merge at the sequence's end.
+// A sequence that lies in one range is written out directly; the others'
+// parts are joined by the merge kernel by their log-sum-exp, as in the decode
+// forward.  (attn_api.cu's plan has the rule and what both measured.)
 //
 // Measured (GB300, device time).  Eight sequences of 16-32 thousand keys, 32
 // query heads on 8, widths 128: 50 us, of which the merge 4; the cache's 248 MB
@@ -71,9 +72,7 @@ namespace esd {
 namespace {
 
 constexpr float kNoKey = -1e30f;    // the running maximum (exp2 domain) of a row that has seen no key
-constexpr int kWarps = 4;
 constexpr int kStages = 3;
-constexpr int kThreads = kWarps * 32;
 
 // d = A B + c (m16n8k16, fp16 operands, fp32 sums).
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -179,8 +178,9 @@ __device__ __forceinline__ int scan_pages(const DecCacheParams& p, int b0, uint3
   return n;
 }
 
-template <int DH, int DV, int NT>
+template <int DH, int DV, int NT, int WARPS>
 struct CacheCfg {
+  static constexpr int kWarps = WARPS, kThreads = 32 * WARPS;
   static constexpr int kRows = 8 * NT;
   static constexpr int kBlock = page_head_bytes(DH, DV);
   static constexpr int kRing = kWarps * kStages * kBlock;
@@ -189,17 +189,20 @@ struct CacheCfg {
   static constexpr int kOffBar = (kRing > kMerge ? kRing : kMerge);
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmemBytes = kOffAbort + 8;
-  // Resident CTAs per SM that the registers are held to (128 of a thread for
-  // 8 rows, 168 for 16).
-  static constexpr int kResident = NT == 1 ? kDecodeCacheResident8 : kDecodeCacheResident16;
+  // Resident CTAs per SM that the registers are held to (four warps: 128 of a
+  // thread for 8 rows, 168 for 16).
+  static constexpr int kResident =
+      WARPS == kDecodeCacheWideWarps ? 1 : (NT == 1 ? kDecodeCacheResident8 : kDecodeCacheResident16);
   static_assert(kBlock % 16 == 0 && kOffBar % 8 == 0, "bulk copies and barriers");
   static_assert(kResident * (kSmemBytes + 1024) <= 233472, "shared memory of the resident CTAs");
 };
 
-template <int DH, int DV, int NT>
-__global__ void __launch_bounds__(kThreads, CacheCfg<DH, DV, NT>::kResident)
+// WHOLE: every CTA takes one whole sequence.
+template <int DH, int DV, int NT, int WARPS, bool WHOLE>
+__global__ void __launch_bounds__(WARPS * 32, CacheCfg<DH, DV, NT, WARPS>::kResident)
 decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
-  using C = CacheCfg<DH, DV, NT>;
+  using C = CacheCfg<DH, DV, NT, WARPS>;
+  constexpr int kWarps = WARPS;
   constexpr int GK = DH / kQuantGroup, GV = DV / kQuantGroup;
   extern __shared__ __align__(128) uint8_t smem[];
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
@@ -215,7 +218,8 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
     fence_mbar_init();
   }
-  const Ranges rg = page_ranges(p, lane);
+  Ranges rg{0, 0};
+  if (!WHOLE) rg = page_ranges(p, lane);
   __syncthreads();
 
   // ---- work: range `range` of the pages, of tile (KV head h, row tile) ----
@@ -228,8 +232,11 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
   const int end = begin + rg.per < rg.total ? begin + rg.per : rg.total;
   // The sequence that `begin` lies in, and its first page's place.
   int b = 0, seq0 = 0;
-  if (begin >= rg.total) {
-    b = begin > 0 ? p.B : 0;     // nothing left for this CTA
+  if (WHOLE) {
+    b = range;
+    if (threadIdx.x == 0 && tile == 0 && p.lengths[b] > p.max_pages * kPageTokens) record_status(p.status, ATTN_ERR_PAGE);
+  } else if (begin >= rg.total) {
+    b = p.B;                     // nothing left for this CTA
   } else if (begin > 0) {
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       int incl;
@@ -245,7 +252,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     }
   }
   // The merge kernel's view of the same: per, then each sequence's first page.
-  if (blockIdx.x == 0 && warp == 0 && p.ranges > 1) {
+  if (blockIdx.x == 0 && warp == 0 && !WHOLE) {
     if (lane == 0) p.first_page[0] = rg.per;
     for (int b0 = 0, at = 0; b0 <= p.B; b0 += 32) {
       int incl;
@@ -259,18 +266,19 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
   // phase will have (the stages are used in turn, across sequences).
   uint32_t st = 0, parity = 0;
   auto after = [](uint32_t s) { return s + 1 == kStages ? 0u : s + 1; };
-  for (; b < p.B && *abort_flag != 2; ++b) {
+  const int b_end = WHOLE ? b + 1 : p.B;
+  for (; b < b_end && *abort_flag != 2; ++b) {
     int len;
     const int npages = pages_of(p, b, len);
     // This CTA's pages [first, last) of sequence b.  Sequences without pages
     // are the merge kernel's, where there is one.
     const int next0 = seq0 + npages;
-    if (p.ranges > 1) {
+    if (!WHOLE) {
       if (seq0 >= end) break;
       if (npages == 0) continue;
     }
     const int first = begin > seq0 ? begin - seq0 : 0;
-    const int last = end < next0 ? end - seq0 : npages;
+    const int last = !WHOLE && end < next0 ? end - seq0 : npages;
 
     // This warp's pages: first + warp, + kWarps, ...
     const int mine = (last - first - static_cast<int>(warp) + kWarps - 1) / kWarps;
@@ -567,7 +575,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         parity ^= st == 0 ? 1u : 0u;
       }
     }
-    if (next0 >= end) cudaTriggerProgrammaticLaunchCompletion();   // the merge kernel may start (it waits for this grid)
+    if (!WHOLE && next0 >= end) cudaTriggerProgrammaticLaunchCompletion();   // the merge kernel may start (it waits for this grid)
     __syncthreads();
 
     // ---- merge of the warps (over the ring) ----
@@ -655,12 +663,13 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
 
 // Merge of the parts of a sequence that several ranges share: LSE = M + ln
 // sum_s exp(LSE_s - M), O = sum_s exp(LSE_s - LSE) O_s.  ROWS query rows per
-// block, each shared by kWarps / ROWS warps, which take every so many parts.
+// block, each shared by kMergeWarps / ROWS warps, which take every so many parts.
 // Launched while the main kernel drains.  Rows of a sequence without pages
 // get O = 0, LSE = -inf here.
+constexpr int kMergeWarps = 4;
 template <int DV, int ROWS>
-__global__ void __launch_bounds__(kThreads) decode_cache_merge_kernel(const __grid_constant__ DecCacheParams p) {
-  constexpr int kPer = DV / 32, kShare = kWarps / ROWS;
+__global__ void __launch_bounds__(kMergeWarps * 32) decode_cache_merge_kernel(const __grid_constant__ DecCacheParams p) {
+  constexpr int kPer = DV / 32, kShare = kMergeWarps / ROWS;
   const int R = p.group * p.n_q;
   const uint32_t lane = lane_id(), warp = warp_id();
   const int r = static_cast<int>(blockIdx.x * ROWS + warp / kShare);    // (b, KV head, row)
@@ -727,20 +736,20 @@ __global__ void __launch_bounds__(kThreads) decode_cache_merge_kernel(const __gr
 // rows, 6 us against 4 with a warp per row.
 constexpr int kMergeBlockRows = 8 * 152;
 
-template <int DH, int DV, int NT>
+template <int DH, int DV, int NT, int WARPS, bool WHOLE>
 cudaError_t launch_t(const DecCacheParams& p, cudaStream_t stream) {
-  using C = CacheCfg<DH, DV, NT>;
-  auto kern = decode_cache_kernel<DH, DV, NT>;
+  using C = CacheCfg<DH, DV, NT, WARPS>;
+  auto kern = decode_cache_kernel<DH, DV, NT, WARPS, WHOLE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.Hkv * p.chunks * p.ranges), kThreads, C::kSmemBytes, stream>>>(p);
+  kern<<<static_cast<unsigned>(p.Hkv * p.chunks * p.ranges), C::kThreads, C::kSmemBytes, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.ranges == 1) return e;
+  if (e != cudaSuccess || WHOLE) return e;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
@@ -749,13 +758,21 @@ cudaError_t launch_t(const DecCacheParams& p, cudaStream_t stream) {
     cfg.gridDim = dim3(static_cast<unsigned>(rows));
     return cudaLaunchKernelEx(&cfg, decode_cache_merge_kernel<DV, 1>, p);
   }
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
-  return cudaLaunchKernelEx(&cfg, decode_cache_merge_kernel<DV, kWarps>, p);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  return cudaLaunchKernelEx(&cfg, decode_cache_merge_kernel<DV, kMergeWarps>, p);
 }
 
 template <int DH, int DV>
 cudaError_t launch_rows(const DecCacheParams& p, cudaStream_t stream) {
-  return p.tile_rows == 8 ? launch_t<DH, DV, 1>(p, stream) : launch_t<DH, DV, 2>(p, stream);
+  const bool one = p.tile_rows == 8;
+  if (!p.whole_seqs)
+    return one ? launch_t<DH, DV, 1, kDecodeCacheWarps, false>(p, stream)
+               : launch_t<DH, DV, 2, kDecodeCacheWarps, false>(p, stream);
+  if (p.wide)
+    return one ? launch_t<DH, DV, 1, kDecodeCacheWideWarps, true>(p, stream)
+               : launch_t<DH, DV, 2, kDecodeCacheWideWarps, true>(p, stream);
+  return one ? launch_t<DH, DV, 1, kDecodeCacheWarps, true>(p, stream)
+             : launch_t<DH, DV, 2, kDecodeCacheWarps, true>(p, stream);
 }
 
 }  // namespace

@@ -94,7 +94,8 @@ def test_scales_of_every_size_round_trip():
         assert np.array_equal(f64(got)[keep], ref.bf16(ref.values(c, s, z))[keep])
 
 
-def test_indices_past_the_pool_are_left_out_and_reported():
+@pytest.mark.parametrize("columns", [3, 80])
+def test_indices_past_the_pool_are_left_out_and_reported(columns):
     import exact_scaled_dot_gb300 as esd
     rng = np.random.default_rng(4)
     cache = esd.QuantCache(torch.zeros((3, 2, 32 * 128 * 9 // 16), dtype=torch.uint8, device="cuda"), 64, 64)
@@ -115,7 +116,8 @@ def test_indices_past_the_pool_are_left_out_and_reported():
     # a page number outside the pool: its keys are left out; a length above the table: cut
     esd.attn_cache_append(cache, _bf16(rng, 96, 2, 64).cuda(), _bf16(rng, 96, 2, 64).cuda(), torch.arange(96, device="cuda"))
     Q = _bf16(rng, 2, 4, 1, 64).cuda()
-    two = torch.tensor([[0, 3, 2], [0, -1, 2]], dtype=torch.int32, device="cuda")
+    two = torch.full((2, columns), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    two[:, :3] = torch.tensor([[0, 3, 2], [0, -1, 2]])
     O, LSE = esd.attn_fwd_decode_cache(Q, cache, two, torch.tensor([90, 10000], dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
     assert esd.attn_get_status() == esd.ATTN_ERR_PAGE
@@ -193,14 +195,19 @@ CASES = {
     "mha": ([333, 64], 8, 8, 2, 128, 128),
     "ragged_split": ([4000, 1, 700, 255, 256, 257], 8, 2, 1, 128, 128),
     "long": ([9001], 4, 1, 2, 128, 64),
+    "many_short": ([int(n) for n in np.random.default_rng(36).integers(0, 700, 41)], 16, 4, 1, 128, 128),
+    "many_short_16_rows": ([int(n) for n in np.random.default_rng(37).integers(0, 500, 44)], 8, 4, 5, 64, 64),
 }
 
 
+@pytest.mark.parametrize("spare_columns", [0, 70])
 @pytest.mark.parametrize("name", list(CASES))
-def test_attention_over_the_cache(name):
+def test_attention_over_the_cache(name, spare_columns):
+    """With the narrowest table, and with a wide one (which is cut into ranges of pages instead)."""
     lengths, Hq, Hkv, nq, dh, dv = CASES[name]
     rng = np.random.default_rng(len(name))
-    cache, table, lens, vals = _filled(rng, lengths, Hkv, dh, dv)
+    wide = max(1, max(-(-n // PAGE) for n in lengths)) + spare_columns
+    cache, table, lens, vals = _filled(rng, lengths, Hkv, dh, dv, wide=wide)
     _attend_and_check(_bf16(rng, len(lengths), Hq, nq, dh), cache, table, lens, vals)
 
 

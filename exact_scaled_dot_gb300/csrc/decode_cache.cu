@@ -268,6 +268,26 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
   auto after = [](uint32_t s) { return s + 1 == kStages ? 0u : s + 1; };
   const int b_end = WHOLE ? b + 1 : p.B;
   for (; b < b_end && *abort_flag != 2; ++b) {
+    // This lane's chunks of the query rows.
+    uint4 qv[NT][GK][2];
+    auto load_q = [&] {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + 8 * nt + g;
+        const uint4* q = reinterpret_cast<const uint4*>(p.Q) +
+                         ((static_cast<int64_t>(b) * p.Hkv + h) * R + (r < R ? r : 0)) * (DH / 8);
+#pragma unroll
+        for (int gk = 0; gk < GK; ++gk)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) qv[nt][gk][w] = r < R ? q[gk * 8 + 2 * t + w] : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    int ids = 0;            // page numbers of a batch of 32 of this warp's pages, one per lane
+    if (WHOLE) {            // what is known without the length, requested along with it
+      const int at = static_cast<int>(warp + lane * kWarps);
+      if (at < p.max_pages) ids = p.table[static_cast<int64_t>(b) * p.max_pages + at];
+      load_q();
+    }
     int len;
     const int npages = pages_of(p, b, len);
     // This CTA's pages [first, last) of sequence b.  Sequences without pages
@@ -284,11 +304,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     const int mine = (last - first - static_cast<int>(warp) + kWarps - 1) / kWarps;
     const int n = mine > 0 ? mine : 0;
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages + first + warp;
-    int ids = 0;            // page numbers of a batch of 32 of this warp's pages, one per lane
     uint32_t bad = 0u;      // bit s: stage s stands for a page outside the pool
     int issued = 0;
     auto issue = [&](uint32_t s) {           // the next page, into stage s
-      if ((issued & 31) == 0)
+      if ((issued & 31) == 0 && (!WHOLE || issued > 0))
         ids = issued + static_cast<int>(lane) < n ? table[(issued + static_cast<int>(lane)) * kWarps] : 0;
       const int id = __shfl_sync(0xffffffffu, ids, issued & 31);
       const bool in_pool = id >= 0 && id < p.pages;
@@ -311,23 +330,17 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     // k-step 4 gk + 2 w + e holds the dims 64 gk + 16 t + 8 w + {2e, 2e+4} in
     // its first and {2e+1, 2e+5} in its second register, the nibbles that one
     // mask takes from a word of codes.
+    if (!WHOLE) load_q();
     uint32_t qf[NT][4 * GK][2];
     float f[NT][2];        // scale log2(e) 2^(9 - e) of query rows 2t, 2t+1 of the group
     int lim[NT][2];        // keys below lim are visible to them
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + 8 * nt + g;
-      const uint4* q = reinterpret_cast<const uint4*>(p.Q) +
-                       ((static_cast<int64_t>(b) * p.Hkv + h) * R + (r < R ? r : 0)) * (DH / 8);
-      uint4 v[GK][2];
       uint32_t m = 0u;
 #pragma unroll
       for (int gk = 0; gk < GK; ++gk)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          v[gk][w] = r < R ? q[gk * 8 + 2 * t + w] : make_uint4(0u, 0u, 0u, 0u);
-          m = bf16_absmax_fold(m, v[gk][w]);
-        }
+        for (int w = 0; w < 2; ++w) m = bf16_absmax_fold(m, qv[nt][gk][w]);
       uint32_t mb = __float_as_uint(bf16_absmax_value(m));     // (as bits, so that a NaN is the largest)
       mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
       mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
@@ -342,7 +355,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           // x, y: dims 0..3, z, w: dims 4..7 of the 16-byte chunk.
-          const uint4 u = bf16x8_to_f16x8_scaled(v[gk][w], up);
+          const uint4 u = bf16x8_to_f16x8_scaled(qv[nt][gk][w], up);
           qf[nt][4 * gk + 2 * w][0] = __byte_perm(u.x, u.z, 0x5410);
           qf[nt][4 * gk + 2 * w][1] = __byte_perm(u.x, u.z, 0x7632);
           qf[nt][4 * gk + 2 * w + 1][0] = __byte_perm(u.y, u.w, 0x5410);

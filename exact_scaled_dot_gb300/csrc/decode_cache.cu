@@ -324,13 +324,13 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
       }
       ++issued;
     };
+    if (!WHOLE) load_q();
     for (uint32_t s = st; issued < kStages && issued < n; s = after(s)) issue(s);
 
     // ---- Q fragments: column g of row group nt is query row r0 + 8 nt + g ----
     // k-step 4 gk + 2 w + e holds the dims 64 gk + 16 t + 8 w + {2e, 2e+4} in
     // its first and {2e+1, 2e+5} in its second register, the nibbles that one
     // mask takes from a word of codes.
-    if (!WHOLE) load_q();
     uint32_t qf[NT][4 * GK][2];
     float f[NT][2];        // scale log2(e) 2^(9 - e) of query rows 2t, 2t+1 of the group
     int lim[NT][2];        // keys below lim are visible to them

@@ -95,6 +95,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// Four 8x8 matrices of 16-bit elements from shared memory, transposed: lanes
+// 8j..8j + 7 address the rows of matrix j; lane 4r + c gets its elements
+// (2c, r) and (2c + 1, r).
+__device__ __forceinline__ void load_transposed(uint32_t row, uint32_t (&x)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(row) : "memory");
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
@@ -110,7 +118,6 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
-__device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 
 // The fp16 operands c 2^-24 of bits 0-3, and 16 c 2^-24 of bits 4-7, of both
 // halves of x.
@@ -394,11 +401,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     int e_ref = -100;                // the weights carry 2^(6 - e_ref)
     float s_lim = exp2_int(-100);    // 2^e_ref: above every scale so far
     float most = 114.f;              // 14 - e_ref
-    // Which key of a 16-key block fragment row m (and m + 8) stands for: rows
-    // 4q + 2 and 4q + 3 are swapped, so that the four lanes t of one V load
-    // read keys of both parities (rows of 64 bytes: both halves of the banks).
-    const int key_g = g ^ ((g >> 1) & 1);
-    const int key_t0 = (2 * t) ^ (t & 1), key_t1 = (2 * t + 1) ^ (t & 1);
+    // The row of V's codes that this lane addresses in a transposed load: key
+    // (lane & 7), of the second eight from lane 16 on, 16 bytes on for odd
+    // groups of eight lanes.
+    const uint32_t v_addr = ring + off_v_codes(DH) + ((lane & 7) + (lane >> 4) * 8) * (DV / 2) + ((lane >> 3) & 1) * 16;
 
     int done = 0;
     while (done < n) {
@@ -410,7 +416,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         float s[2][NT][4];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-          const int ka = 16 * kb + key_g;
+          const int ka = 16 * kb + g;
           uint32_t pa[GK], pb[GK];
           lds_words<GK>(blk + off_k_words(DH, DV) + ka * (GK * 4), pa);
           lds_words<GK>(blk + off_k_words(DH, DV) + (ka + 8) * (GK * 4), pb);
@@ -457,14 +463,14 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
-            lds_words<GV>(blk + off_v_words(DH, DV) + (16 * kb + 8 * hf + key_g) * (GV * 4), vw[kb][hf]);
+            lds_words<GV>(blk + off_v_words(DH, DV) + (16 * kb + 8 * hf + g) * (GV * 4), vw[kb][hf]);
         const bool missing = (bad >> st) & 1u;     // (none of a missing page's keys is seen)
         if (missing || key0 + kPageTokens > len - p.n_q + 1) {
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const int key = missing ? len : key0 + 16 * kb + 8 * hf + key_g;
+              const int key = missing ? len : key0 + 16 * kb + 8 * hf + g;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -555,16 +561,13 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
               }
             }
           }
-          const uint8_t* vc = blk + off_v_codes(DH) + 16 * kb * (DV / 2) + g * 4;
 #pragma unroll
           for (int gv = 0; gv < GV; ++gv) {
-            const uint8_t* c = vc + gv * 32;
-            const uint32_t w0 = lds32(c + key_t0 * (DV / 2)), w1 = lds32(c + key_t1 * (DV / 2));
-            const uint32_t w2 = lds32(c + (key_t0 + 8) * (DV / 2)), w3 = lds32(c + (key_t1 + 8) * (DV / 2));
+            uint32_t x[4];         // keys 0-7: dims 4g.. of the group's first and second half; keys 8-15
+            load_transposed(v_addr + st * C::kBlock + 16 * kb * (DV / 2) + gv * 32, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t xa = __byte_perm(w0, w1, i < 2 ? 0x5410 : 0x7632);
-              uint32_t xb = __byte_perm(w2, w3, i < 2 ? 0x5410 : 0x7632);
+              uint32_t xa = x[i >> 1], xb = x[2 + (i >> 1)];
               if (i & 1) xa >>= 8, xb >>= 8;
               const uint32_t a0 = low_nibbles(xa), a1 = high_nibbles(xa), a2 = low_nibbles(xb), a3 = high_nibbles(xb);
 #pragma unroll
@@ -615,12 +618,12 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         }
 #pragma unroll
         for (int gv = 0; gv < GV; ++gv) {
-          float4* dst = reinterpret_cast<float4*>(oacc + row * C::kOStride + 64 * gv + 8 * g);
+          float4* dst = reinterpret_cast<float4*>(oacc + row * C::kOStride + 64 * gv + 4 * g);
           const float z = add_lanes(oz[nt][gv][k]);
           auto lo = [&](int i) { return (o[nt][gv][i][k] - z) * 262144.0f * two_e; };
           auto hi = [&](int i) { return fmaf(o[nt][gv][i][2 + k], 0.0625f, -z) * 262144.0f * two_e; };
           dst[0] = make_float4(lo(0), hi(0), lo(1), hi(1));
-          dst[1] = make_float4(lo(2), hi(2), lo(3), hi(3));
+          dst[8] = make_float4(lo(2), hi(2), lo(3), hi(3));
         }
       }
     __syncthreads();

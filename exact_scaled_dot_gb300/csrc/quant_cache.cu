@@ -68,35 +68,53 @@ __device__ __forceinline__ void quantize8(uint4 v, uint32_t& codes, uint32_t& wo
 #pragma unroll
   for (int off = 4; off > 0; off >>= 1) m = max_pairs(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float hi = bf16_lo(m), neg_lo = bf16_hi(m);
-  const uint32_t sb = pack_bf16x2(__fdiv_rn(hi + neg_lo, 15.0f), 0.f) << 16;
-  const float s = __uint_as_float(sb);
-  float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
-                bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+  // (hi - lo) / 15 by a product and one correction with the exact remainder,
+  // which rounds it correctly (Markstein's theorem) where nothing underflows.
+  const float range = hi + neg_lo, q0 = range * (1.0f / 15.0f);
+  uint32_t sb = pack_bf16x2(fmaf(fmaf(-15.0f, q0, range), 1.0f / 15.0f, q0), 0.f) << 16;
+  float s = __uint_as_float(sb);
   codes = 0u;
-  word = sb;
+  word = 0u;
   if (s < 0x1p-100f) {
     // 1/s may leave fp32's range: divide.  (s = 0: nothing to do.)
+    sb = pack_bf16x2(__fdiv_rn(range, 15.0f), 0.f) << 16;
+    s = __uint_as_float(sb);
     if (s > 0.f) {
+      const float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
+                          bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
       const float z = rintf(__fdiv_rn(neg_lo, s));
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         codes |= static_cast<uint32_t>(fminf(rintf(__fdiv_rn(x[k], s)) + z, 15.0f)) << (4 * k);
-      word |= static_cast<uint32_t>(z);
+      word = sb | static_cast<uint32_t>(z);
     }
     return;
   }
   const float inv = reciprocal(s);
   // rint(a / s) + kToInteger: the second sum is exact before its one rounding.
-  auto rounded = [inv](float a) { return fmaf(a, inv, kToGrid) + (kToInteger - kToGrid); };
-  const float z = rounded(neg_lo) - kToInteger;
+  constexpr float kStep = kToInteger - kToGrid;
+  const float z = fmaf(neg_lo, inv, kToGrid) + kStep - kToInteger;
   const float back = z - kToInteger;
+  // Codes past 15 come from elements above (15 - z) s, which rounded to bf16
+  // still is code 15: the elements are cut there, two at a time.
+  const float top = (15.0f - z) * s;
+  const uint32_t most = pack_bf16x2(top, top);
+  v = make_uint4(min_pairs(v.x, most), min_pairs(v.y, most), min_pairs(v.z, most), min_pairs(v.w, most));
+  // Pairs (k, k + 4), whose codes go to the same place of the two halves.
+  float lo[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+  float up4[4] = {bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = fminf(rounded(x[k]) + back, 15.0f);
+  for (int k = 0; k < 4; ++k) {
+    ffma2(lo[k], up4[k], lo[k], up4[k], inv, inv, kToGrid, kToGrid);
+    fadd2(lo[k], up4[k], kStep, kStep);
+    fadd2(lo[k], up4[k], back, back);
+  }
   // Four codes in base 16 are an exact fp32 integer.
-  const float lo4 = fmaf(fmaf(fmaf(x[3], 16.f, x[2]), 16.f, x[1]), 16.f, x[0]) + 8388608.0f;
-  const float hi4 = fmaf(fmaf(fmaf(x[7], 16.f, x[6]), 16.f, x[5]), 16.f, x[4]) + 8388608.0f;
-  codes = __byte_perm(__float_as_uint(lo4), __float_as_uint(hi4), 0x5410);
-  word |= __float_as_uint(z + 8388608.0f) & 0xFFu;
+#pragma unroll
+  for (int k = 2; k >= 0; --k) ffma2(lo[3], up4[3], lo[3], up4[3], 16.f, 16.f, lo[k], up4[k]);
+  fadd2(lo[3], up4[3], 8388608.0f, 8388608.0f);
+  codes = __byte_perm(__float_as_uint(lo[3]), __float_as_uint(up4[3]), 0x5410);
+  word = sb | (__float_as_uint(z + 8388608.0f) & 0xFFu);
 }
 
 // Eight elements as bf16: 128 + code less 128 + z, exact, times s, rounded once.

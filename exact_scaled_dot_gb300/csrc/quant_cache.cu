@@ -36,10 +36,12 @@
 namespace esd {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block (16384 tokens, 8 heads, widths 128, writing + reading
+// back: 18.7 + 16.1, 19.0 + 16.5, 22.3 + 17.2 us with 128, 256, 512).
+constexpr int kThreads = 128;
 // Tokens that a thread has in flight once there are enough to fill the GPU
-// (16384 tokens, 8 heads, widths 128, writing and reading back: 39.7, 36.0,
-// 36.6 and 36.9 us with 1, 2, 3 and 4); with fewer, one token a thread.
+// (the same with 256 threads: 20.4 + 19.0, 19.0 + 16.5, 19.3 + 17.2 and
+// 20.6 + 17.0 us with 1, 2, 3 and 4); with fewer, one token a thread.
 constexpr int kMostTokens = 2;
 
 constexpr float kToGrid = 6144.0f;          // 1.5 2^12: sums near it are multiples of 2^-11

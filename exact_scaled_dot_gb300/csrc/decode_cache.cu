@@ -50,16 +50,19 @@
 // parts are joined by the merge kernel by their log-sum-exp, as in the decode
 // forward.  (attn_api.cu's plan has the rule and what both measured.)
 //
-// Measured (GB300, device time).  Eight sequences of 16-32 thousand keys, 32
-// query heads on 8, widths 128: 50 us, of which the merge 4; the cache's 248 MB
-// take 37 us at the measured copy rate, and the kernel without its arithmetic
-// 43.  48 sequences of 4-12000 keys, 4 queries, 16 heads on 4, widths 128 and
-// 64: 47 us for 125 MB (19 us).  What bounds it is the issue of instructions:
-// a page costs a warp some 520 of them and 32 matrix products (48 with 16
-// query rows) that hold a scheduler for 8 cycles each, together the 800 (1000)
-// cycles measured.  More or fewer warps, a page of lookahead for the scores,
-// pages requested across sequences or a deeper ring changed nothing (each
-// within 2 %, tried and left out).
+// Measured (GB300, device time).  256 sequences of 2048 keys, 32 query heads on
+// 8, widths 128: 103 us for 604 MB, 5.9 TB/s.  Eight of 16-32 thousand keys:
+// 49 us, of which the merge 4; the 248 MB take 37 us at the measured copy rate,
+// and the kernel without its arithmetic 43.  48 sequences of 4-12000 keys, 4
+// queries, 16 heads on 4, widths 128 and 64: 43.6 us for 125 MB (19 us).  What
+// bounds it is the issue of instructions: a page costs a warp some 570 of them
+// (16 query rows: 600), 32 (48) of which are matrix products of 8 cycles.  The
+// schedulers issue in 0.6 of the cycles with the ALUs at 53 % (they take an
+// instruction every other cycle), the tensor pipe at 29 % (34); what warps wait
+// for is mostly one another's pipe (math throttle, dispatch, not selected).
+// More or fewer warps, a page of lookahead for the scores, pages or lengths
+// requested across sequences, a deeper ring and an earlier or later start of
+// the merge changed nothing or cost up to 2 % (tried and left out).
 #include <cstdint>
 #include <cuda_runtime.h>
 

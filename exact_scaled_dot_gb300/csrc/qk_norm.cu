@@ -13,7 +13,10 @@
 // since d r / d x_i = -r^3 x_i / d.
 //
 // All three kernels move each row once: 4 bytes per element forward (bf16 in
-// and out), 6 backward (x and dy in, dx out), and are bound by DRAM.  Eight
+// and out), 6 backward (x and dy in, dx out), and are bound by DRAM (of the
+// measured copy rate: norm and rotation of 8192 tokens of 32 + 8 heads of 128
+// in 28 us, 89 %; the backward of 32768 tokens in 159 us, 94 %; the rotation of
+// 65537 tokens of 16 + 16 heads in 158 us, 102 %).  Eight
 // lanes hold a row, each one or two chunks of 8 elements (16-byte accesses;
 // up to width 64, up to 128), and sum over it with three shuffles.  Lanes
 // walk over the heads of a token, so that the token's angles (and with them

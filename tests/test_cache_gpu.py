@@ -195,6 +195,7 @@ CASES = {
     "mha": ([333, 64], 8, 8, 2, 128, 128),
     "ragged_split": ([4000, 1, 700, 255, 256, 257], 8, 2, 1, 128, 128),
     "long": ([9001], 4, 1, 2, 128, 64),
+    "more_tiles_than_ctas": ([4200], 300, 1, 16, 64, 64),
     "many_short": ([int(n) for n in np.random.default_rng(36).integers(0, 700, 41)], 16, 4, 1, 128, 128),
     "many_short_16_rows": ([int(n) for n in np.random.default_rng(37).integers(0, 500, 44)], 8, 4, 5, 64, 64),
 }

@@ -188,7 +188,7 @@ __device__ __forceinline__ int scan_pages(const DecCacheParams& p, int b0, uint3
   return n;
 }
 
-template <int DH, int DV, int NT, int WARPS>
+template <int DH, int DV, int NT, int WARPS, bool WHOLE>
 struct CacheCfg {
   static constexpr int kWarps = WARPS, kThreads = 32 * WARPS;
   static constexpr int kRows = 8 * NT;
@@ -200,18 +200,22 @@ struct CacheCfg {
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmemBytes = kOffAbort + 8;
   // Resident CTAs per SM that the registers are held to (four warps: 128 of a
-  // thread for 8 rows, 168 for 16).
+  // thread for 8 rows, 168 for 16).  One more where key rows of 64 leave
+  // registers and many CTAs take turns: 256 sequences of 2048 keys, 32 heads on
+  // 8, 65.0 to 61.7 us, 16 rows on 4 heads 52.7 to 47.8; but not for ranges
+  // (16 rows 21.3 to 23.3 us: more of them, each shorter).
+  static constexpr int kMore = WHOLE && DH == 64 ? 1 : 0;
   static constexpr int kResident =
-      WARPS == kDecodeCacheWideWarps ? 1 : (NT == 1 ? kDecodeCacheResident8 : kDecodeCacheResident16);
+      WARPS == kDecodeCacheWideWarps ? 1 : (NT == 1 ? kDecodeCacheResident8 : kDecodeCacheResident16) + kMore;
   static_assert(kBlock % 16 == 0 && kOffBar % 8 == 0, "bulk copies and barriers");
   static_assert(kResident * (kSmemBytes + 1024) <= 233472, "shared memory of the resident CTAs");
 };
 
 // WHOLE: every CTA takes one whole sequence.
 template <int DH, int DV, int NT, int WARPS, bool WHOLE>
-__global__ void __launch_bounds__(WARPS * 32, CacheCfg<DH, DV, NT, WARPS>::kResident)
+__global__ void __launch_bounds__(WARPS * 32, CacheCfg<DH, DV, NT, WARPS, WHOLE>::kResident)
 decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
-  using C = CacheCfg<DH, DV, NT, WARPS>;
+  using C = CacheCfg<DH, DV, NT, WARPS, WHOLE>;
   constexpr int kWarps = WARPS;
   constexpr int GK = DH / kQuantGroup, GV = DV / kQuantGroup;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -757,7 +761,7 @@ constexpr int kMergeBlockRows = 8 * 152;
 
 template <int DH, int DV, int NT, int WARPS, bool WHOLE>
 cudaError_t launch_t(const DecCacheParams& p, cudaStream_t stream) {
-  using C = CacheCfg<DH, DV, NT, WARPS>;
+  using C = CacheCfg<DH, DV, NT, WARPS, WHOLE>;
   auto kern = decode_cache_kernel<DH, DV, NT, WARPS, WHOLE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;

@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
   constexpr int kRows = CH == 1 ? 4 : 2;       // rows of a step
   __shared__ BlockTable tab;
   __shared__ uint4 ring[kStages][kRows * CH][kThreads];
-  fill_table(p, tab);
   const uint32_t lane = lane_id();
   const int c = static_cast<int>(lane & 7);
   const Part part = part_of(p);
@@ -169,6 +168,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
   for (int it = 0; it < kStages - 1; ++it) request(it);
   int32_t pos[kMaxAxes];
   token_positions(p, tok, pos);
+  fill_table(p, tab);        // behind the first requests
   // cs: the cosines and sines; with a norm, each block's map (x0, x1) ->
   // (x0 a - x1 b, x0 c + x1 d) with the weights in it.
   float4 cs[CH][2], map[CH][4];
@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
     uint4 ring[kStages][2][kRows * CH][kThreads];
     float red[kSlots][CH * 64 + 4];
   } sh;
-  fill_table(p, tab);
   const uint32_t lane = lane_id();
   const int c = static_cast<int>(lane & 7);
   const Part part = part_of(p);
@@ -306,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
   for (int i = 0; i < CH; ++i) cs[i][0] = cs[i][1] = make_float4(1.f, 0.f, 1.f, 0.f);    // (slots without a token)
   int32_t pos[kMaxAxes];
   if (at.tok < p.tokens) token_positions(p, at.tok, pos);
+  fill_table(p, tab);        // behind the first requests
   for (int it = 0; at.tok - slot < p.tokens; ++it) {
     const bool there = at.tok < p.tokens;
     if (at.h == 0 && there) {

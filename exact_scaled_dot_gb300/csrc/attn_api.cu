@@ -878,23 +878,22 @@ int check_qk_ptrs(std::initializer_list<const void*> q, std::initializer_list<co
   return ATTN_OK;
 }
 
-// The frequency and axis of every block.
+// The frequency of every block and the axes' places.
 void fill_axes(QkParams* p, const attn_rotary_axes* r, int d) {
-  std::memset(p->w_hi, 0, sizeof(p->w_hi));
-  std::memset(p->w_lo, 0, sizeof(p->w_lo));
-  std::memset(p->axis, 0, sizeof(p->axis));
+  std::memset(p->w, 0, sizeof(p->w));
+  for (int a = 0; a < kMaxAxes; ++a) p->first[a] = 64;
   p->axes = r ? r->axes : 0;
   p->pos = r ? r->pos : nullptr;
   if (!r) return;
   int first = 0;
   for (int a = 0; a < r->axes; ++a) {
+    p->first[a] = first;
     for (int i = 0; i < r->sections[a]; ++i) {
       const int k = first + i;
       const double power = r->restart ? static_cast<double>(i) / r->sections[a] : 2.0 * k / d;
       const double w = std::pow(static_cast<double>(r->base), -power);
-      p->w_hi[k] = static_cast<float>(w);
-      p->w_lo[k] = static_cast<float>(w - static_cast<double>(p->w_hi[k]));
-      p->axis[k] = static_cast<uint8_t>(a);
+      p->w[k].x = static_cast<float>(w);
+      p->w[k].y = static_cast<float>(w - static_cast<double>(p->w[k].x));
     }
     first += r->sections[a];
   }

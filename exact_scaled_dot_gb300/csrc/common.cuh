@@ -329,8 +329,8 @@ struct QkParams {
   int32_t part_heads;          // heads of a token that one block takes, and how many
   int32_t parts_q;             // such parts the query heads make (set by the launchers)
   float* partial;              // backward: [parts][blocks][d] shares of the weight gradients
-  float w_hi[64], w_lo[64];    // frequency of each block (0 past the sections), as in RotaryAngles
-  uint8_t axis[64];            // axis of each block
+  float2 w[64];                // frequency of each block, hi and lo (0 past the sections), as in RotaryAngles
+  int32_t first[kMaxAxes];     // first block of each axis (64: none)
 };
 
 // Tokens written to or read from the 4-bit cache (quant_cache.cuh).

@@ -15,8 +15,8 @@
 // All three kernels move each row once: 4 bytes per element forward (bf16 in
 // and out), 6 backward (x and dy in, dx out), and are bound by DRAM (of the
 // measured copy rate: norm and rotation of 8192 tokens of 32 + 8 heads of 128
-// in 28 us, 89 %; the backward of 32768 tokens in 159 us, 94 %; the rotation of
-// 65537 tokens of 16 + 16 heads in 158 us, 102 %).  Eight
+// in 27 us, 92 %; the backward of 32768 tokens in 160 us, 94 %; the rotation of
+// 65537 tokens of 16 + 16 heads in 156 us, 103 %).  Eight
 // lanes hold a row, each one or two chunks of 8 elements (16-byte accesses;
 // up to width 64, up to 128), and sum over it with three shuffles.  Lanes
 // walk over the heads of a token, so that the token's angles (and with them
@@ -42,6 +42,7 @@ constexpr int kSlots = kThreads / kLanes;      // tokens that a block works on a
 constexpr int kFwdHeads = 16;
 constexpr int kBwdHeads = 8;
 constexpr int kStages = 4;                     // steps in the ring (a power of two)
+constexpr int kBwdResident = 4;                // backward blocks of an SM (128 registers a thread)
 
 // Over the eight lanes of a row; called by whole warps.
 __device__ __forceinline__ float row_sum(float v) {
@@ -88,32 +89,44 @@ __device__ __forceinline__ Part part_of(const QkParams& p) {
   return Part{which, h0, min(p.part_heads, p.heads[which] - h0)};
 }
 
-// The frequencies (w_hi, w_lo) and the axis of every block, in shared memory:
-// read once per token by lanes that differ in the block.
+// The frequencies (hi, lo) of every block, in shared memory: read once per token
+// by lanes that differ in the block.  (Lanes that differ read a kernel's
+// parameters one after the other: one read each, of the blocks there are.  Three
+// reads each, of 64 blocks, and ahead of the rows: 8 tokens 2.8 us instead of
+// 2.5, 1025 of 16 + 2 heads 4.3 instead of 3.5.)
 struct BlockTable {
-  float4 e[64];
+  float2 w[64];
 };
 __device__ __forceinline__ void fill_table(const QkParams& p, BlockTable& t) {
-  if (threadIdx.x < 64)
-    t.e[threadIdx.x] = make_float4(p.w_hi[threadIdx.x], p.w_lo[threadIdx.x], __int_as_float(p.axis[threadIdx.x]), 0.f);
+  const int k = static_cast<int>(threadIdx.x);
+  if (p.axes > 0 && k < p.d / 2) t.w[k] = p.w[k];
   __syncthreads();
+}
+
+// The axes of the four blocks of chunk c, a byte each: kept where angles are
+// formed in a loop.
+__device__ __forceinline__ uint32_t chunk_axes(const QkParams& p, int c) {
+  uint32_t axes = 0u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) axes |= ((4 * c + q >= p.first[1] ? 1u : 0u) + (4 * c + q >= p.first[2] ? 1u : 0u)) << (8 * q);
+  return axes;
 }
 
 // Cosines and sines of the four blocks of chunk c at the token's positions
 // (the same angles as the single-axis rotation); t0: blocks 0, 1, t1: 2, 3.
-__device__ __forceinline__ void chunk_angles(const BlockTable& tab, int axes, const int32_t (&pos)[kMaxAxes], int c,
+// position(q): the position that the chunk's block q turns by.
+template <class Position>
+__device__ __forceinline__ void chunk_angles(const QkParams& p, const BlockTable& tab, Position position, int c,
                                              float4& t0, float4& t1) {
-  if (axes == 0) {
+  if (p.axes == 0) {
     t0 = t1 = make_float4(1.f, 0.f, 1.f, 0.f);
     return;
   }
   float cs[4], sn[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const float4 e = tab.e[4 * c + q];
-    const int axis = __float_as_int(e.z);
-    const int32_t at = axis == 0 ? pos[0] : (axis == 1 ? pos[1] : pos[2]);
-    rope_cos_sin(reduced_angle(at, e.x, e.y), cs[q], sn[q]);
+    const float2 w = tab.w[4 * c + q];
+    rope_cos_sin(reduced_angle(position(q), w.x, w.y), cs[q], sn[q]);
   }
   t0 = make_float4(cs[0], sn[0], cs[1], sn[1]);
   t1 = make_float4(cs[2], sn[2], cs[3], sn[3]);
@@ -175,7 +188,10 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int ci = on[i] ? c + 8 * i : 0;
-    chunk_angles(tab, p.axes, pos, ci, cs[i][0], cs[i][1]);
+    chunk_angles(p, tab, [&](int q) {
+      const int k = 4 * ci + q;
+      return k < p.first[1] ? pos[0] : (k < p.first[2] ? pos[1] : pos[2]);
+    }, ci, cs[i][0], cs[i][1]);
     if (p.inverse) rope_transpose(cs[i][0], cs[i][1]);
     if constexpr (NORM) {
       float w[8];
@@ -251,7 +267,7 @@ struct Cursor {
 // partial[blockIdx.y][blockIdx.x][d], and qk_dg_kernel adds the blocks', again
 // in a fixed order: no atomics, the same bits on every run.
 template <int CH>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, kBwdResident) qk_bwd_kernel(const __grid_constant__ QkParams p) {
   constexpr int kRows = CH == 1 ? 2 : 1;       // rows of a step
   __shared__ BlockTable tab;
   // The ring (x, then dy), and at the end the slots' shares of dg.
@@ -275,9 +291,11 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
   const int slot = static_cast<int>(threadIdx.x) / kLanes;
   bool on[CH];
   float w[CH][8], dg[CH][8];
+  uint32_t axes[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     on[i] = c + 8 * i < p.d / 8;
+    axes[i] = chunk_axes(p, c + 8 * i);
     load_weights(p.g[part.which], on[i] ? c + 8 * i : 0, w[i]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) dg[i][k] = 0.f;
@@ -311,7 +329,10 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant_
     if (at.h == 0 && there) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        chunk_angles(tab, p.axes, pos, on[i] ? c + 8 * i : 0, cs[i][0], cs[i][1]);
+        chunk_angles(p, tab, [&](int q) {
+          const uint32_t axis = axes[i] >> (8 * q) & 0xFFu;
+          return axis == 0u ? pos[0] : (axis == 1u ? pos[1] : pos[2]);
+        }, on[i] ? c + 8 * i : 0, cs[i][0], cs[i][1]);
         rope_transpose(cs[i][0], cs[i][1]);
       }
       if (at.tok + step < p.tokens) token_positions(p, at.tok + step, pos);     // the next token's, early
@@ -417,11 +438,10 @@ int choose_part_heads(int64_t tokens, int heads_q, int heads_k, int most) {
   return n;
 }
 
-// The backward's blocks along the tokens: four of all parts on each SM, which
-// is what its registers allow, so that each works to the end with its ring
-// filled and has one share of dg.
+// The backward's blocks along the tokens: as many of all parts as are resident,
+// so that each works to the end with its ring filled and has one share of dg.
 int bwd_blocks_x(int64_t tokens, int parts) {
-  const int64_t rows = (tokens + kSlots - 1) / kSlots, most = std::max(1, 152 * 4 / parts);
+  const int64_t rows = (tokens + kSlots - 1) / kSlots, most = std::max(1, 152 * kBwdResident / parts);
   return static_cast<int>(std::min(rows, most));
 }
 

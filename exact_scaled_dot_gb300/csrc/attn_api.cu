@@ -946,20 +946,21 @@ int cache_io(const attn_cache* c, int64_t tokens, const attn_strides* strides, c
 
 // How attn_fwd_decode_cache divides the work: row tiles of 8 query rows (16
 // when a KV head has more), and of each either
-//   a CTA per sequence, when the page table is narrow: up to 24 pages, or up
+//   a CTA per sequence, when the page table is narrow: up to 32 pages, or up
 //   to as many as there are such CTAs, 64 at most (the length of a sequence
 //   that all others may have to wait for), or
 //   as many equal ranges of all pages as CTAs are resident at once (fewer when
 //   there are few pages), and a merge of the sequences that ranges share.
 // Few CTAs of the first kind have eight warps.  Measured, ranges against whole
 // sequences (one KV head of 8 query rows unless given, widths 128):
-//   1 sequence of 8, 24, 32 pages: 7.5, 7.7, 7.9 us against 5.1, 7.5, 8.4
-//   64 of 32, 64: 11.2, 15.5 against 8.7, 13.0
-//   64 of 16, 64, 8 KV heads: 18.9, 41.4 against 12.9, 36.9
+//   1 sequence of 8, 32, 48 pages: 7.0, 7.3, 7.4 us against 4.4, 7.2, 9.2
+//   64 of 32, 64: 10.3, 14.3 against 7.5, 11.4
+//   64 of 16, 64, 8 KV heads: 17.1, 37.6 against 11.2, 33.1
+//   256 of 64, 8 KV heads: 114 against 103
 // and one launch less for the host (20 us a call against 14).  Eight warps
-// against four: 1 sequence of 24 pages 7.5 us against 8.6, but 608 CTAs of 16
-// pages 22 us against 13.
-constexpr int kFewPages = 24, kManyPages = 64;
+// against four: 1 sequence of 32 pages 7.2 us against 9.3, but 512 CTAs of 16
+// pages 17.9 us against 11.2.
+constexpr int kFewPages = 32, kManyPages = 64;
 struct DecodeCachePlan {
   int tile_rows, chunks, ranges;
   bool whole_seqs, wide;

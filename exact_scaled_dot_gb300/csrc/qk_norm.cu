@@ -37,8 +37,8 @@ constexpr int kThreads = 128;
 constexpr int kLanes = 8;                      // lanes of a row
 constexpr int kSlots = kThreads / kLanes;      // tokens that a block works on at once
 // Heads of one token that a slot takes, at most.  More share the angles,
-// fewer balance the blocks: forward 32.5, 30.3, 30.8 us with 8, 16, 32 heads
-// (8192 tokens, 32 + 8 heads of 128), backward 160, 163 us with 8, 16.
+// fewer balance the blocks: forward 27.5, 26.9, 28.2 us with 8, 16, 32 heads
+// (8192 tokens, 32 + 8 heads of 128), backward 160, 164 us with 8, 16 (32768).
 constexpr int kFwdHeads = 16;
 constexpr int kBwdHeads = 8;
 constexpr int kStages = 4;                     // steps in the ring (a power of two)

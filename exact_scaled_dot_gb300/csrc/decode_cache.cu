@@ -58,7 +58,7 @@
 // bounds it is the issue of instructions: a page costs a warp some 570 of them
 // (16 query rows: 600), 32 (48) of which are matrix products of 8 cycles.  The
 // schedulers issue in 0.6 of the cycles with the ALUs at 53 % (they take an
-// instruction every other cycle), the tensor pipe at 29 % (34); what warps wait
+// instruction every other cycle), the tensor pipe at 29 % (35); what warps wait
 // for is mostly one another's pipe (math throttle, dispatch, not selected).
 // More or fewer warps, a page of lookahead for the scores, pages or lengths
 // requested across sequences, a deeper ring and an earlier or later start of

@@ -22,7 +22,7 @@
 //
 // Measured (GB300, 16384 tokens, 8 heads, widths 128): writing and reading
 // back 34 us, 76 % of the measured copy rate for their 172 MB.  What bounds both
-// is the issue of instructions (0.73 of the schedulers' cycles, the integer
+// is the issue of instructions (0.72 of the schedulers' cycles, the integer
 // pipe at 62 %: range, rounding and packing of each element), not DRAM.
 #include <algorithm>
 #include <cstdint>

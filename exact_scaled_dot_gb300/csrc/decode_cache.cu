@@ -37,7 +37,8 @@
 // only when a score exceeds it by 2^8), times 2^6 s_j 2^-e with 2^e above the
 // largest scale seen so far, so w <= 2^14 whatever the values' scale; O is
 // rescaled when e grows.  Weights down to 2^-20 of the largest keep 11 bits.
-// Sums, maxima and O are fp32.
+// Sums, maxima and O are fp32, and the sum of the P carries no scale of the
+// values: it cannot leave fp32's range, and the LSE does not depend on V.
 //
 // Work: for one (KV head, row tile), short sequences get a CTA each.  Else the
 // pages of all sequences, one after the other, are cut into equal ranges, one
@@ -74,7 +75,8 @@
 namespace esd {
 namespace {
 
-constexpr float kNoKey = -1e30f;    // the running maximum (exp2 domain) of a row that has seen no key
+constexpr float kNoKey = -1e30f;    // the reference (exp2 domain) of a row that has seen no key
+constexpr float kLazy = 8.f;        // a score may exceed its row's reference by this (exp2 domain)
 constexpr int kStages = 3;
 
 // d = A B + c (m16n8k16, fp16 operands, fp32 sums).
@@ -391,11 +393,11 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     // O^T before the zero points, [group][dim pair i][(dim, row), (dim, row + 1),
     // 16 (dim + 1, row), 16 (dim + 1, row + 1)], and what they take off.
     float o[NT][GV][4][4], oz[NT][GV][2];
-    float m_ref[NT][2], l_sum[NT][2], shift[NT][2];
+    float shift[NT][2], l_sum[NT][2];      // less the reference that P is relative to; the sum of P
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) m_ref[nt][k] = kNoKey, shift[nt][k] = -kNoKey, l_sum[nt][k] = 0.f;
+      for (int k = 0; k < 2; ++k) shift[nt][k] = -kNoKey, l_sum[nt][k] = 0.f;
 #pragma unroll
       for (int gv = 0; gv < GV; ++gv)
 #pragma unroll
@@ -407,7 +409,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     }
     int e_ref = -100;                // the weights carry 2^(6 - e_ref)
     float s_lim = exp2_int(-100);    // 2^e_ref: above every scale so far
-    float most = 114.f;              // 14 - e_ref
+    float w_up = exp2_int(106);      // 2^(6 - e_ref)
     // The row of V's codes that this lane addresses in a transposed load: key
     // (lane & 7), of the second eight from lane 16 on, 16 bytes on for odd
     // groups of eight lanes.
@@ -491,8 +493,6 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
             }
         }
         // ---- running maximum (lazy) and the weights' scale ----
-        // The weights' exponents are s f + shift, shift = 6 - e_ref - (the
-        // reference maximum); none may reach 14 - e_ref.
         bool need = false;
         float mx[NT][2];
 #pragma unroll
@@ -500,7 +500,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             mx[nt][k] = fmaxf(fmaxf(s[0][nt][k], s[0][nt][2 + k]), fmaxf(s[1][nt][k], s[1][nt][2 + k]));
-            need |= fmaf(mx[nt][k], f[nt][k], shift[nt][k]) > most;
+            need |= fmaf(mx[nt][k], f[nt][k], shift[nt][k]) > kLazy;
           }
         float smax = 0.f;
 #pragma unroll
@@ -512,12 +512,11 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
           const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
           int e = static_cast<int>(all >> 23) - 126;              // 2^e > the largest scale
           e = e > 126 ? 126 : (e < e_ref ? e_ref : e);
-          const int de = e_ref - e < -126 ? -126 : e_ref - e;
-          const float back = exp2_int(de);
-          const float e_step = static_cast<float>(e_ref - e);
+          // (Below 2^-126 nothing of O is left beside the new weights.)
+          const float back = exp2_int(e_ref - e < -126 ? -126 : e_ref - e);
           e_ref = e;
           s_lim = exp2_int(e);
-          most = static_cast<float>(14 - e);
+          w_up = exp2_int(6 - e);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -527,14 +526,13 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
               m *= f[nt][k];
-              shift[nt][k] += e_step;
-              float alpha = back;
-              if (m + shift[nt][k] > most) {
-                alpha *= fast_exp2(m_ref[nt][k] - m);
-                m_ref[nt][k] = m;
-                shift[nt][k] = static_cast<float>(6 - e) - m;
+              float alpha = 1.f;
+              if (m + shift[nt][k] > kLazy) {
+                alpha = fast_exp2(-shift[nt][k] - m);
+                shift[nt][k] = -m;
               }
               l_sum[nt][k] *= alpha;
+              alpha *= back;
 #pragma unroll
               for (int gv = 0; gv < GV; ++gv) {
                 oz[nt][gv][k] *= alpha;
@@ -559,6 +557,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
               p0 = fast_exp2(p0);
               p1 = fast_exp2(p1);
               fadd2(l_sum[nt][0], l_sum[nt][1], p0, p1);
+              fmul2(p0, p1, p0, p1, w_up, w_up);
 #pragma unroll
               for (int gv = 0; gv < GV; ++gv) {
                 const float sc = __uint_as_float(vw[kb][hf][gv]);
@@ -605,8 +604,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     float* oacc = reinterpret_cast<float*>(smem);                              // [warp][row][kOStride]
     float* mst = oacc + kWarps * C::kRows * C::kOStride;                       // [warp][row]
     float* lst = mst + kWarps * C::kRows;
-    // The sums carry 2^(6 - e_ref), o and oz another 2^-24 (the rows of the
-    // high nibbles 2^-20).
+    // o and oz carry 2^(6 - e_ref) 2^-24 (the rows of the high nibbles 2^-20).
     const float two_e = exp2_int(e_ref);
     auto add_lanes = [](float x) {             // over the 8 lanes of a query row
       x += __shfl_xor_sync(0xffffffffu, x, 4);
@@ -617,10 +615,10 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float l = add_lanes(l_sum[nt][k]) * 0.015625f * two_e;
+        const float l = add_lanes(l_sum[nt][k]);
         const int row = static_cast<int>(warp) * C::kRows + 8 * nt + 2 * t + k;
         if (g == 0) {
-          mst[row] = m_ref[nt][k];
+          mst[row] = -shift[nt][k];
           lst[row] = l;
         }
 #pragma unroll

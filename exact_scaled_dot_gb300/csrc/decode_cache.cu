@@ -33,12 +33,20 @@
 // 2^-14, which costs the sums 4 to 5 bits (measured: LSE off by 8e-6 instead of
 // 3e-7), too many for the scores and none that matter for O.
 //
-// fp16 weights: P <= 2^8 by the lazy running maximum (the reference moves
-// only when a score exceeds it by 2^8), times 2^6 s_j 2^-e with 2^e above the
-// largest scale seen so far, so w <= 2^14 whatever the values' scale; O is
-// rescaled when e grows.  Weights down to 2^-20 of the largest keep 11 bits.
-// Sums, maxima and O are fp32, and the sum of the P carries no scale of the
-// values: it cannot leave fp32's range, and the LSE does not depend on V.
+// fp16 weights: w = P s_j / top, with a power of two top for each query row and
+// group of 64 dims that leaves the largest P s_j the row has met at 2^5 to 2^6.
+// A large scale on a key that a row hardly weighs, in another group or under a
+// mask takes no bits from the row's other weights, and top falls with P when the
+// row's reference moves.  Both are set anew, and O rescaled, only when a score
+// passes the reference by 2^7 or the page has a scale that might take a weight
+// past fp16 (from 4 to 8 times the weighted one behind top on); P s_j of the page
+// is formed for that in fp32.  Weights down to 2^-19 of the row's largest keep 11
+// bits, smaller ones are rounded to multiples of 2^-29 of it.  Sums, maxima and O
+// are fp32, and the sum of the P carries no scale of the values: it cannot leave
+// fp32's range, and the LSE does not depend on V.  (One exponent for a warp, above
+// every scale it had met, lost the weights beside a scale 2^24 times theirs; the
+// cases below took the same time with it.  Scales that differ by octaves from
+// key to key set top in every page: up to 20 % more.)
 //
 // Work: for one (KV head, row tile), short sequences get a CTA each.  Else the
 // pages of all sequences, one after the other, are cut into equal ranges, one
@@ -76,7 +84,12 @@ namespace esd {
 namespace {
 
 constexpr float kNoKey = -1e30f;    // the reference (exp2 domain) of a row that has seen no key
-constexpr float kLazy = 8.f;        // a score may exceed its row's reference by this (exp2 domain)
+// Weights w = P s_j / top of a row and group: up to 2^kTopBits when top is set,
+// 2^kLazy more for a score above the row's reference and 2^kSlack more for a
+// larger scale before either is set again.
+constexpr int kLazy = 7, kSlack = 2, kTopBits = 6;
+static_assert(kLazy + kSlack + kTopBits <= 15, "weights are fp16");
+constexpr int kLeastTop = -118, kMostTop = 126;    // (exponents; P / top is at most 2^125)
 constexpr int kStages = 3;
 
 // d = A B + c (m16n8k16, fp16 operands, fp32 sums).
@@ -145,6 +158,11 @@ __device__ __forceinline__ void fma_halves(float& acc0, float& acc1, uint32_t w,
       : "+f"(acc0), "+f"(acc1)
       : "r"(w), "r"(z));
 }
+
+// Powers of two: the next one from x >= 0 up (0: 0), the nearest, and 1 / x of one.
+__device__ __forceinline__ uint32_t next_power(float x) { return (__float_as_uint(x) + 0x007FFFFFu) & 0x7F800000u; }
+__device__ __forceinline__ uint32_t near_power(float x) { return (__float_as_uint(x) + 0x00400000u) & 0x7F800000u; }
+__device__ __forceinline__ float inverse_power(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -407,9 +425,15 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
           for (int i = 0; i < 4; ++i) o[nt][gv][i][k] = 0.f;
         }
     }
-    int e_ref = -100;                // the weights carry 2^(6 - e_ref)
-    float s_lim = exp2_int(-100);    // 2^e_ref: above every scale so far
-    float w_up = exp2_int(106);      // 2^(6 - e_ref)
+    // 1 / top, and the scale from which on a weight may be too large for fp16
+    // (the least of the lane's rows).
+    float w_up[NT][GV][2], s_lim[GV];
+#pragma unroll
+    for (int gv = 0; gv < GV; ++gv) {
+      s_lim[gv] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) w_up[nt][gv][0] = w_up[nt][gv][1] = exp2_int(-kLeastTop);
+    }
     // The row of V's codes that this lane addresses in a transposed load: key
     // (lane & 7), of the second eight from lane 16 on, 16 bytes on for odd
     // groups of eight lanes.
@@ -492,7 +516,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
                 for (int gv = 0; gv < GV; ++gv) vw[kb][hf][gv] = 0u;
             }
         }
-        // ---- running maximum (lazy) and the weights' scale ----
+        // ---- running maximum (lazy) and the weights' scales ----
         bool need = false;
         float mx[NT][2];
 #pragma unroll
@@ -500,49 +524,64 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             mx[nt][k] = fmaxf(fmaxf(s[0][nt][k], s[0][nt][2 + k]), fmaxf(s[1][nt][k], s[1][nt][2 + k]));
-            need |= fmaf(mx[nt][k], f[nt][k], shift[nt][k]) > kLazy;
+            need |= fmaf(mx[nt][k], f[nt][k], shift[nt][k]) > static_cast<float>(kLazy);
           }
-        float smax = 0.f;
 #pragma unroll
-        for (int gv = 0; gv < GV; ++gv)
-          smax = fmax3(fmax3(smax, __uint_as_float(vw[0][0][gv]), __uint_as_float(vw[0][1][gv])),
-                       __uint_as_float(vw[1][0][gv]), __uint_as_float(vw[1][1][gv]));
-        need |= smax >= s_lim;
+        for (int gv = 0; gv < GV; ++gv) {
+          const float smax = fmax3(fmaxf(__uint_as_float(vw[0][0][gv]), __uint_as_float(vw[0][1][gv])),
+                                   __uint_as_float(vw[1][0][gv]), __uint_as_float(vw[1][1][gv]));
+          need |= smax > s_lim[gv];
+        }
         if (__any_sync(0xffffffffu, need)) {
-          const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
-          int e = static_cast<int>(all >> 23) - 126;              // 2^e > the largest scale
-          e = e > 126 ? 126 : (e < e_ref ? e_ref : e);
-          // (Below 2^-126 nothing of O is left beside the new weights.)
-          const float back = exp2_int(e_ref - e < -126 ? -126 : e_ref - e);
-          e_ref = e;
-          s_lim = exp2_int(e);
-          w_up = exp2_int(6 - e);
+          float least[GV];
+#pragma unroll
+          for (int gv = 0; gv < GV; ++gv) least[gv] = INFINITY;
+          auto max_lanes = [](float x) {         // over the 8 lanes of a query row
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          };
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float m = mx[nt][k];
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-              m *= f[nt][k];
+              const float m = ceilf(max_lanes(mx[nt][k]) * f[nt][k]);
               float alpha = 1.f;
-              if (m + shift[nt][k] > kLazy) {
+              if (m + shift[nt][k] > static_cast<float>(kLazy)) {    // (whole octaves: alpha is a power of two)
                 alpha = fast_exp2(-shift[nt][k] - m);
                 shift[nt][k] = -m;
               }
               l_sum[nt][k] *= alpha;
-              alpha *= back;
+              float p[2][2];
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                  p[kb][hf] = fast_exp2(fmaf(s[kb][nt][2 * hf + k], f[nt][k], shift[nt][k]));
 #pragma unroll
               for (int gv = 0; gv < GV; ++gv) {
-                oz[nt][gv][k] *= alpha;
+                float most = 0.f;                // of the page's P s_j
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf) most = fmaxf(most, p[kb][hf] * __uint_as_float(vw[kb][hf][gv]));
+                const float was = alpha * inverse_power(w_up[nt][gv][k]);
+                const uint32_t at_least = max(near_power(was), static_cast<uint32_t>(127 + kLeastTop) << 23);
+                const uint32_t now = max(at_least, next_power(max_lanes(most) * exp2_int(-kTopBits)));
+                const float top = __uint_as_float(min(now, static_cast<uint32_t>(127 + kMostTop) << 23));
+                w_up[nt][gv][k] = inverse_power(top);
+                const float back = was * w_up[nt][gv][k];          // at most 1
+                least[gv] = fminf(least[gv], top);
+                oz[nt][gv][k] *= back;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  o[nt][gv][i][k] *= alpha;
-                  o[nt][gv][i][2 + k] *= alpha;
+                  o[nt][gv][i][k] *= back;
+                  o[nt][gv][i][2 + k] *= back;
                 }
               }
             }
+#pragma unroll
+          for (int gv = 0; gv < GV; ++gv) s_lim[gv] = least[gv] * exp2_int(kTopBits + kSlack);
         }
         // ---- weights and O^T += V^T P^T ----
 #pragma unroll
@@ -557,11 +596,13 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
               p0 = fast_exp2(p0);
               p1 = fast_exp2(p1);
               fadd2(l_sum[nt][0], l_sum[nt][1], p0, p1);
-              fmul2(p0, p1, p0, p1, w_up, w_up);
 #pragma unroll
               for (int gv = 0; gv < GV; ++gv) {
                 const float sc = __uint_as_float(vw[kb][hf][gv]);
-                const uint32_t w = pack_half2(p0 * sc, p1 * sc);
+                float w0, w1;
+                fmul2(w0, w1, p0, p1, w_up[nt][gv][0], w_up[nt][gv][1]);
+                fmul2(w0, w1, w0, w1, sc, sc);
+                const uint32_t w = pack_half2(w0, w1);
                 fma_halves(oz[nt][gv][0], oz[nt][gv][1], w, vw[kb][hf][gv]);    // z as fp16 is z 2^-24
                 bw[nt][gv][hf] = transpose8x8(w);
               }
@@ -604,8 +645,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     float* oacc = reinterpret_cast<float*>(smem);                              // [warp][row][kOStride]
     float* mst = oacc + kWarps * C::kRows * C::kOStride;                       // [warp][row]
     float* lst = mst + kWarps * C::kRows;
-    // o and oz carry 2^(6 - e_ref) 2^-24 (the rows of the high nibbles 2^-20).
-    const float two_e = exp2_int(e_ref);
+    // o and oz carry 2^-24 / top (the rows of the high nibbles 2^-20 / top).
     auto add_lanes = [](float x) {             // over the 8 lanes of a query row
       x += __shfl_xor_sync(0xffffffffu, x, 4);
       x += __shfl_xor_sync(0xffffffffu, x, 8);
@@ -625,8 +665,9 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         for (int gv = 0; gv < GV; ++gv) {
           float4* dst = reinterpret_cast<float4*>(oacc + row * C::kOStride + 64 * gv + 4 * g);
           const float z = add_lanes(oz[nt][gv][k]);
-          auto lo = [&](int i) { return (o[nt][gv][i][k] - z) * 262144.0f * two_e; };
-          auto hi = [&](int i) { return fmaf(o[nt][gv][i][2 + k], 0.0625f, -z) * 262144.0f * two_e; };
+          const float up = 16777216.0f * inverse_power(w_up[nt][gv][k]);
+          auto lo = [&](int i) { return (o[nt][gv][i][k] - z) * up; };
+          auto hi = [&](int i) { return fmaf(o[nt][gv][i][2 + k], 0.0625f, -z) * up; };
           dst[0] = make_float4(lo(0), hi(0), lo(1), hi(1));
           dst[8] = make_float4(lo(2), hi(2), lo(3), hi(3));
         }

@@ -604,6 +604,11 @@ int attn_cache_read(const attn_cache* cache, int64_t tokens, const attn_strides*
  * with an infinity or a NaN gives NaN.  A page
  * number outside the pool leaves that page's keys out, and a length above
  * 32 max_pages is cut; both record ATTN_ERR_PAGE in the status word.
+ * Precision: scores, softmax statistics and sums in fp32 (|S_ij| < 2^24; an
+ * exp(S_ij - m_i) below 2^-126 counts as 0).  A_ij times the scale of the key's
+ * values is rounded to fp16 relative to the largest such product of the row and
+ * of the same 64 dims: 11 bits down to 2^-19 of it, multiples of 2^-29 of it
+ * below that (less for values below 2^-100).
  * `workspace`: attn_fwd_decode_cache_workspace_bytes() bytes, 256-byte
  * aligned (may be NULL when that is 0); it depends on the sizes only. */
 size_t attn_fwd_decode_cache_workspace_bytes(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q,

@@ -1,6 +1,7 @@
 """GPU tests of attention over the 4-bit cache with values of very different
-sizes along a sequence, each element against the 64-bit form under a bound that
-is relative to its own group's weighted values."""
+sizes: along a sequence, between keys of different weight, and between the two
+64-element groups of a row, each element against the 64-bit form under a bound
+that is relative to its own group's weighted values."""
 import numpy as np
 import pytest
 import torch
@@ -130,3 +131,109 @@ def test_many_keys_above_the_first():
     # that many roundings of 2^-24 in the sum, and some more in the scores and exponentials
     assert (O == 0).all()
     assert_within(f64(LSE), np.full((1, Hkv, 1), want), wide * 2.0 ** -24 + 2.0 ** -18, "LSE")
+
+
+# ---------------------------------------------------------------------------
+# A row's weights are as precise as its own largest one allows
+# ---------------------------------------------------------------------------
+def _along(rng, scores, Hkv, d):
+    """Queries [1, 2 Hkv, 1, d] and a K for _filled whose scores with a KV head's first query
+    are about `scores` [n] (natural log, at the scale d^-1/2), with its second about -`scores`."""
+    u = rng.normal(size=(Hkv, d))
+    Q = torch.from_numpy(np.stack([u, -u], 1).reshape(1, 2 * Hkv, 1, d)).to(torch.bfloat16)
+    unit = u * np.sqrt(d) / (u * u).sum(-1, keepdims=True)
+
+    def K(b, n):
+        return torch.from_numpy(scores[:, None, None] * unit + 0.02 * rng.normal(size=(n, Hkv, d))).to(torch.bfloat16)
+
+    return Q, K
+
+
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+@pytest.mark.parametrize("at", [0, 0.5, 1])
+@pytest.mark.parametrize("e", [24, 32, 40])
+def test_a_large_value_on_a_key_that_carries_no_weight(layout, at, e):
+    """One key 2^-80 below the others for the first query of each KV head, with values 2^e times
+    theirs; the second query of the head sees little else."""
+    n, Hkv, d, spare = LAYOUTS[layout]
+    rng = np.random.default_rng(41)
+    key = int(round(at * (n - 1)))
+    scores = 0.3 * rng.normal(size=n)
+    scores[key] = -80 * np.log(2)
+
+    def V(b, n):
+        v = 0.7 + 0.1 * rng.normal(size=(n, Hkv, d))
+        v[key] *= 2.0 ** e
+        return torch.from_numpy(v).to(torch.bfloat16)
+
+    Q, K = _along(rng, scores, Hkv, d)
+    cache, table, lens, vals = _filled(rng, [n], Hkv, d, d, K=K, V=V, wide=-(-n // PAGE) + spare)
+    O, _ = _check(Q, cache, table, lens, vals)
+    O = f64(O)[0].reshape(Hkv, 2, d)
+    assert (np.abs(O[:, 0] - 0.7) < 0.2).all() and (np.abs(O[:, 1]) > 0.1 * 2.0 ** e).all()
+
+
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+def test_a_large_value_whose_weight_fades(layout):
+    """The first pages have values of 2^40; scores that rise by 80 octaves along the sequence
+    leave nothing of them in the first query, and nothing of the last ones in the second."""
+    n, Hkv, d, spare = LAYOUTS[layout]
+    rng = np.random.default_rng(42)
+
+    def V(b, n):
+        size = np.where(np.arange(n) < n // 4, 2.0 ** 40, 1.0)[:, None, None]
+        return torch.from_numpy((0.7 + 0.1 * rng.normal(size=(n, Hkv, d))) * size).to(torch.bfloat16)
+
+    Q, K = _along(rng, np.linspace(-40, 40, n) * np.log(2), Hkv, d)
+    cache, table, lens, vals = _filled(rng, [n], Hkv, d, d, K=K, V=V, wide=-(-n // PAGE) + spare)
+    _check(Q, cache, table, lens, vals)
+
+
+@pytest.mark.parametrize("spare", [0, 70])
+@pytest.mark.parametrize("e", [-80, -40, -28, 28, 40, 80])
+@pytest.mark.parametrize("group,nq", [(2, 1), (3, 4)])
+def test_groups_of_different_scale(spare, e, group, nq):
+    """Dims 64-127 of every value 2^e times dims 0-63; up to 8 and more query rows."""
+    rng = np.random.default_rng(43)
+
+    def V(b, n):
+        v = rng.normal(size=(n, 2, 128))
+        v[..., 64:] *= 2.0 ** e
+        return torch.from_numpy(v).to(torch.bfloat16)
+
+    cache, table, lens, vals = _filled(rng, [700, 33], 2, 128, 128, V=V, wide=22 + spare)
+    _check(_bf16(rng, 2, 2 * group, nq, 128), cache, table, lens, vals)
+
+
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+@pytest.mark.parametrize("dv,group,nq", [(128, 2, 1), (64, 2, 1), (64, 3, 5)])
+def test_scores_and_scales_of_every_size(layout, dv, group, nq):
+    """Scores over some 100 octaves, the values' scales over 80, independent of each other."""
+    n, Hkv, d, spare = LAYOUTS[layout]
+    Hkv, d = min(Hkv, 8), max(d, dv)
+    rng = np.random.default_rng(44)
+
+    def V(b, n):
+        size = 2.0 ** rng.uniform(-40, 40, size=(n, Hkv, dv // GROUP, 1))
+        return torch.from_numpy((rng.normal(size=(n, Hkv, dv // GROUP, GROUP)) * size).reshape(n, Hkv, dv)).to(torch.bfloat16)
+
+    cache, table, lens, vals = _filled(rng, [n, n // 3], Hkv, d, dv, V=V, wide=-(-n // PAGE) + spare,
+                                       K=lambda b, n: _bf16(rng, n, Hkv, d, scale=12.0))
+    _check(_bf16(rng, 2, Hkv * group, nq, d), cache, table, lens, vals)
+
+
+@pytest.mark.parametrize("spare", [0, 70])
+def test_scores_of_some_millions(spare):
+    """One key far above the rest, at the size where neighbouring fp32 scores are 1/2 apart."""
+    rng = np.random.default_rng(45)
+    K = lambda b, n: torch.zeros((n, 1, 64), dtype=torch.bfloat16).index_fill_(0, torch.tensor([n // 2]), 15.0)  # noqa: E731
+    cache, table, lens, vals = _filled(rng, [300], 1, 64, 64, K=K, wide=10 + spare)
+    Q = torch.full((1, 4, 1, 64), 3.0, dtype=torch.bfloat16)
+    import exact_scaled_dot_gb300 as esd
+    O, LSE = esd.attn_fwd_decode_cache(Q.cuda(), cache, table, lens, scale=2100.0)
+    torch.cuda.synchronize()
+    score, v = 15 * 3 * 64 * 2100.0, vals[0][1][150, 0]
+    assert 2.0 ** 22 < score < 2.0 ** 23
+    # its weight is all there is: fp16's rounding of it, the sums' of codes and zero points, bf16's
+    assert_within(f64(O), np.broadcast_to(v, (1, 4, 1, 64)), ref.BF16 * np.abs(v) + ref.F16 * np.abs(v) + 2.0 ** -13 * np.abs(v).max(), "O")
+    assert_within(f64(LSE), np.full((1, 4, 1), score), 2.0 ** -20 * score, "LSE")

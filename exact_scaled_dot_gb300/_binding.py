@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+from operator import attrgetter
 from pathlib import Path
 from typing import Optional, Sequence, Tuple, Union
 
@@ -1076,20 +1077,29 @@ class QuantCache:
     """A key/value cache held in 4 bits (attn_cache): pool is a contiguous
     uint8 device tensor [pages, Hkv, block] of the layout in the C header, a
     page holding ATTN_CACHE_PAGE_TOKENS tokens.  Which page belongs to which
-    sequence is the caller's page table."""
+    sequence is the caller's page table.  Pool and sizes are those given for
+    good (a larger pool is another QuantCache)."""
 
     def __init__(self, pool: torch.Tensor, d_h: int, d_v: int):
         if not isinstance(pool, torch.Tensor) or pool.dim() != 3:
             raise ValueError("pool must be a [pages, Hkv, block] tensor")
-        self.pool, self.d_h, self.d_v = pool, int(d_h), int(d_v)
-        self.pages, self.Hkv, block = pool.shape
-        self.device = pool.device
+        d_h, d_v = int(d_h), int(d_v)
+        pages, Hkv, block = pool.shape
         _check_flat(pool, "pool", torch.uint8, pool.shape, pool.device)
         # Bytes of one page of one head: codes and a 32-bit word per 64 elements.
-        want = ATTN_CACHE_PAGE_TOKENS * (self.d_h + self.d_v) * 9 // 16
+        want = ATTN_CACHE_PAGE_TOKENS * (d_h + d_v) * 9 // 16
         if block != want:
             raise ValueError(f"pool blocks must have {want} bytes for widths ({d_h}, {d_v}), got {block}")
-        self._arg = AttnCache(self.Hkv, self.d_h, self.d_v, self.pages, pool.data_ptr())
+        self._pool, self._device, self._pages, self._Hkv, self._d_h, self._d_v = pool, pool.device, pages, Hkv, d_h, d_v
+        self._arg = AttnCache(Hkv, d_h, d_v, pages, pool.data_ptr())
+
+    # Read-only: the struct that the library gets holds the pool's address.
+    pool = property(attrgetter("_pool"))
+    device = property(attrgetter("_device"))
+    pages = property(attrgetter("_pages"))
+    Hkv = property(attrgetter("_Hkv"))
+    d_h = property(attrgetter("_d_h"))
+    d_v = property(attrgetter("_d_v"))
 
     @classmethod
     def empty(cls, pages: int, Hkv: int, d_h: int, d_v: int, device="cuda"):

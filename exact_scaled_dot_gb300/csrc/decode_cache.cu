@@ -405,6 +405,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         f[nt][k] = __shfl_sync(0xffffffffu, fac, (2 * t + k) * 4);
         const int row = r0 + 8 * nt + 2 * t + k;
         lim[nt][k] = row < R ? len - p.n_q + 1 + row % p.n_q : 0;
+        if (lim[nt][k] <= 0) f[nt][k] = 0x1p-126f;     // (sees no key: not NaN either)
       }
     }
 

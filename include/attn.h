@@ -601,7 +601,7 @@ int attn_cache_read(const attn_cache* cache, int64_t tokens, const attn_strides*
  * runs, so that a captured call follows them.  Since the host does not see
  * them, a row without a visible key is not refused: its O is 0 and its LSE
  * -inf (a sequence of length 0, or rows before its first token).  A row of Q
- * with an infinity or a NaN gives NaN.  A page
+ * with an infinity or a NaN gives NaN where it sees a key.  A page
  * number outside the pool leaves that page's keys out, and a length above
  * 32 max_pages is cut; both record ATTN_ERR_PAGE in the status word.
  * Precision: scores, softmax statistics and sums in fp32 (|S_ij| < 2^24; an

@@ -237,3 +237,25 @@ def test_scores_of_some_millions(spare):
     # its weight is all there is: fp16's rounding of it, the sums' of codes and zero points, bf16's
     assert_within(f64(O), np.broadcast_to(v, (1, 4, 1, 64)), ref.BF16 * np.abs(v) + ref.F16 * np.abs(v) + 2.0 ** -13 * np.abs(v).max(), "O")
     assert_within(f64(LSE), np.full((1, 4, 1), score), 2.0 ** -20 * score, "LSE")
+
+
+# ---------------------------------------------------------------------------
+# Rows without a key
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("spare", [0, 70])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_query_row_that_is_not_finite_and_sees_no_key(spare, value):
+    """O = 0 and LSE = -inf, as for any row without a key, in sequences of no and of few tokens."""
+    import exact_scaled_dot_gb300 as esd
+    rng = np.random.default_rng(46)
+    lengths, nq = [0, 1, 3, 40], 4
+    cache, table, lens, _ = _filled(rng, lengths, 1, 128, 64, wide=2 + spare)
+    Q = _bf16(rng, 4, 5, nq, 128).cuda()
+    O, LSE = esd.attn_fwd_decode_cache(Q, cache, table, lens)
+    unseen = torch.tensor([[i < nq - n for i in range(nq)] for n in lengths], device="cuda")[:, None].expand(4, 5, nq)
+    Q[unseen] = value
+    O2, LSE2 = esd.attn_fwd_decode_cache(Q, cache, table, lens)
+    torch.cuda.synchronize()
+    assert esd.attn_get_status() == 0
+    assert (O2[unseen] == 0).all() and LSE2[unseen].isneginf().all()
+    assert torch.equal(O, O2) and torch.equal(LSE, LSE2)

@@ -38,15 +38,17 @@
 // A large scale on a key that a row hardly weighs, in another group or under a
 // mask takes no bits from the row's other weights, and top falls with P when the
 // row's reference moves.  Both are set anew, and O rescaled, only when a score
-// passes the reference by 2^7 or the page has a scale that might take a weight
-// past fp16 (from 4 to 8 times the weighted one behind top on); P s_j of the page
+// passes the reference by 2^5 or the page has a scale that might take a weight
+// past fp16 (from 16 to 32 times the weighted one behind top on); P s_j of the page
 // is formed for that in fp32.  Weights down to 2^-19 of the row's largest keep 11
 // bits, smaller ones are rounded to multiples of 2^-29 of it.  Sums, maxima and O
 // are fp32, and the sum of the P carries no scale of the values: it cannot leave
 // fp32's range, and the LSE does not depend on V.  (One exponent for a warp, above
 // every scale it had met, lost the weights beside a scale 2^24 times theirs; the
-// cases below took the same time with it.  Scales that differ by octaves from
-// key to key set top in every page: up to 20 % more.)
+// cases below took 0.5 % less with it.  Scales spread over 16 octaves from key to
+// key set top in every page: 51.8 us for the long case below instead of 50.2, 48.2
+// for the ragged one instead of 43.8; over 4 octaves 50.1 and 44.4, with 2^7 and 4
+// in place of 2^5 and 16 52.9 and 49.0.)
 //
 // Work: for one (KV head, row tile), short sequences get a CTA each.  Else the
 // pages of all sequences, one after the other, are cut into equal ranges, one
@@ -87,7 +89,7 @@ constexpr float kNoKey = -1e30f;    // the reference (exp2 domain) of a row that
 // Weights w = P s_j / top of a row and group: up to 2^kTopBits when top is set,
 // 2^kLazy more for a score above the row's reference and 2^kSlack more for a
 // larger scale before either is set again.
-constexpr int kLazy = 7, kSlack = 2, kTopBits = 6;
+constexpr int kLazy = 5, kSlack = 4, kTopBits = 6;
 static_assert(kLazy + kSlack + kTopBits <= 15, "weights are fp16");
 constexpr int kLeastTop = -118, kMostTop = 126;    // (exponents; P / top is at most 2^125)
 constexpr int kStages = 3;

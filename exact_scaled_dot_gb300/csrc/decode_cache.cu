@@ -12,7 +12,8 @@
 // elements per SM and cycle).  So they stay in registers between shared
 // memory and the tensor core, as fragments of mma.sync (through shared
 // memory, tcgen05's operands would cost a 2-byte write and read per element,
-// several times the traffic of the codes), with the cache as the M side of
+// several times the traffic of the codes; through tensor memory, its A operand
+// would: not measured), with the cache as the M side of
 // both products and the R = group n_q query rows of a KV head as N = 8 NT
 // columns:
 //   S^T = K Q^T: A = 16 keys x 16 dims.  A lane's nibbles of one key are its
@@ -62,15 +63,16 @@
 // forward.  (attn_api.cu's plan has the rule and what both measured.)
 //
 // Measured (GB300, device time).  256 sequences of 2048 keys, 32 query heads on
-// 8, widths 128: 103 us for 604 MB, 5.9 TB/s.  Eight of 16-32 thousand keys:
-// 49 us, of which the merge 4; the 248 MB take 37 us at the measured copy rate,
+// 8, widths 128: 102 us for 604 MB, 5.9 TB/s.  Eight of 16-32 thousand keys:
+// 50 us, of which the merge 4; the 248 MB take 37 us at the measured copy rate,
 // and the kernel without its arithmetic 43.  48 sequences of 4-12000 keys, 4
-// queries, 16 heads on 4, widths 128 and 64: 43.6 us for 125 MB (19 us).  What
-// bounds it is the issue of instructions: a page costs a warp some 570 of them
-// (16 query rows: 600), 32 (48) of which are matrix products of 8 cycles.  The
-// schedulers issue in 0.6 of the cycles with the ALUs at 53 % (they take an
-// instruction every other cycle), the tensor pipe at 29 % (35); what warps wait
-// for is mostly one another's pipe (math throttle, dispatch, not selected).
+// queries, 16 heads on 4, widths 128 and 64: 43.8 us for 125 MB (19 us).  No unit
+// is full: in these two the schedulers issue in 0.59 and 0.53 of the cycles (some
+// 590 instructions a page), the ALUs are at 52 and 38 %, the tensor pipe at 28 and
+// 34.  The registers (128 and 168 a thread) leave 3.6 and 2.8 warps a scheduler,
+// and these wait for the fixed latencies of a page's chains (1.3 and 1.5 cycles an
+// issue), for one another (not selected 1.1 and 0.7, math pipe 0.9 and 0.6,
+// dispatch 0.4) and for pages (long scoreboard 0.6 and 0.4).
 // More or fewer warps, a page of lookahead for the scores, pages or lengths
 // requested across sequences, a deeper ring and an earlier or later start of
 // the merge changed nothing or cost up to 2 % (tried and left out).
@@ -224,8 +226,8 @@ struct CacheCfg {
   // Resident CTAs per SM that the registers are held to (four warps: 128 of a
   // thread for 8 rows, 168 for 16).  One more where key rows of 64 leave
   // registers and many CTAs take turns: 256 sequences of 2048 keys, 32 heads on
-  // 8, 65.0 to 61.7 us, 16 rows on 4 heads 52.7 to 47.8; but not for ranges
-  // (16 rows 21.3 to 23.3 us: more of them, each shorter).
+  // 8, 61.1 to 58.7 us, 16 rows on 4 heads 49.1 to 44.4; but not for ranges
+  // (16 rows 21.1 to 23.7 us: more of them, each shorter).
   static constexpr int kMore = WHOLE && DH == 64 ? 1 : 0;
   static constexpr int kResident =
       WARPS == kDecodeCacheWideWarps ? 1 : (NT == 1 ? kDecodeCacheResident8 : kDecodeCacheResident16) + kMore;

@@ -618,7 +618,8 @@ int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Device status word of the current device: ATTN_OK, or the first failure a
- * kernel recorded (ATTN_ERR_TIMEOUT).  Synchronises the device.  Writes the
+ * kernel recorded (ATTN_ERR_TIMEOUT, ATTN_ERR_RANGE or ATTN_ERR_PAGE; a
+ * timeout replaces the others).  Synchronises the device.  Writes the
  * status to *status and returns ATTN_OK, or ATTN_ERR_CUDA. */
 int attn_get_status(int* status);
 
@@ -634,7 +635,9 @@ int attn_selftest_wait_timeout(uint64_t limit_ns, void* stream);
 /* Human-readable name of a status code (static string). */
 const char* attn_strerror(int status);
 
-/* ATTN_ABI_VERSION of the loaded library. */
+/* ATTN_ABI_VERSION of the loaded library.  It changes when an entry point, a
+ * struct or the meaning of a call changes; entry points and codes that are only
+ * added leave it. */
 int attn_abi_version(void);
 
 #ifdef __cplusplus

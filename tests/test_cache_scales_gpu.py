@@ -240,6 +240,39 @@ def test_scores_of_some_millions(spare):
 
 
 # ---------------------------------------------------------------------------
+# Long sums
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("Hq,Hkv,d", [(320, 320, 64), (4800, 1, 128)])
+def test_the_mean_of_many_values(Hq, Hkv, d):
+    """Equal weights over 320000 keys of one CTA: O is the mean of the values, far below each of them.
+
+    A step of 16 keys may cut the sum of codes that it adds to by 2^-23 of itself: up to 64 steps
+    of 16 codes of 15 until the zero points are taken out, and what is left of the sum beside
+    (3 sqrt(80000) of a warp's keys, below 2^12 here), so 2^-23 (960 + 2^8) of a code for each key;
+    a key's zero point is added to up to 127 others in fp32: 2^-24 128 15."""
+    import exact_scaled_dot_gb300 as esd
+    rng = np.random.default_rng(47)
+    pages, wide = 60, 10000
+    V = torch.from_numpy(rng.normal(size=(pages * PAGE, Hkv, d))).to(torch.bfloat16)
+    cache = esd.QuantCache.empty(pages, Hkv, d, d)
+    esd.attn_cache_append(cache, torch.zeros_like(V).cuda(), V.cuda(), torch.arange(pages * PAGE, device="cuda"))
+    c, s, z = ref.quantize(f64(V))
+    table = rng.integers(0, pages, (1, wide)).astype(np.int32)
+    O, LSE = esd.attn_fwd_decode_cache(torch.zeros((1, Hq, 1, d), dtype=torch.bfloat16, device="cuda"), cache,
+                                       torch.from_numpy(table).cuda(),
+                                       torch.tensor([wide * PAGE], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert esd.attn_get_status() == 0
+    v = ref.values(c, s, z).reshape(pages, PAGE, Hkv, d).sum(1)
+    mean = np.einsum("p,phd->hd", np.bincount(table[0], minlength=pages).astype(np.float64), v) / (wide * PAGE)
+    mean = np.repeat(mean, Hq // Hkv, 0)[None, :, None]
+    cut = (2.0 ** -23 * (960 + 256) + 2.0 ** -24 * 128 * 15) * s.max()
+    assert_within(f64(O), mean, ref.BF16 * np.abs(mean) + cut, "O")
+    want = np.full((1, Hq, 1), np.log(wide * PAGE))
+    assert_within(f64(LSE), want, 2.0 ** -22 * want, "LSE")
+
+
+# ---------------------------------------------------------------------------
 # Rows without a key
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("spare", [0, 70])

@@ -953,13 +953,13 @@ int cache_io(const attn_cache* c, int64_t tokens, const attn_strides* strides, c
 //   there are few pages), and a merge of the sequences that ranges share.
 // Few CTAs of the first kind have eight warps.  Measured, ranges against whole
 // sequences (one KV head of 8 query rows unless given, widths 128):
-//   1 sequence of 8, 32, 48 pages: 6.9, 7.4, 7.8 us against 4.5, 7.4, 9.2
-//   64 of 32, 64: 10.8, 14.9 against 7.6, 11.5
-//   64 of 16, 64, 8 KV heads: 20.4, 38.6 against 13.1, 32.8
-//   256 of 64, 8 KV heads: 118 against 103
-// and one launch less for the host (19 us a call from Python against 14).  Eight
-// warps against four: 1 sequence of 32 pages 7.4 us against 9.2, but 512 CTAs of
-// 16 pages 21.2 us against 12.9.
+//   1 sequence of 8, 32, 48 pages: 6.7, 7.5, 7.9 us against 4.4, 7.4, 9.4
+//   64 of 32, 64: 10.8, 15.1 against 7.6, 11.7
+//   64 of 16, 64, 8 KV heads: 20.4, 38.9 against 13.2, 33.4
+//   256 of 64, 8 KV heads: 119 against 104
+// and one launch less for the host (20 us a call from Python against 14).  Eight
+// warps against four: 1 sequence of 32 pages 7.4 us against 9.3, but 512 CTAs of
+// 16 pages 21.3 us against 13.1.
 constexpr int kFewPages = 32, kManyPages = 64;
 struct DecodeCachePlan {
   int tile_rows, chunks, ranges;

@@ -52,9 +52,9 @@
 // fp32's range, and the LSE does not depend on V.  (One exponent for a warp, above
 // every scale it had met, lost the weights beside a scale 2^24 times theirs; the
 // cases below took 0.5 % less with it.  Scales spread over 16 octaves from key to
-// key set top in every page: 51.8 us for the long case below instead of 50.2, 48.2
-// for the ragged one instead of 43.8; over 4 octaves 50.1 and 44.4, with 2^7 and 4
-// in place of 2^5 and 16 52.9 and 49.0.)
+// key set top in every page: 52.2 us for the long case below instead of 49.8, 48.9
+// for the ragged one instead of 44.4; over 4 octaves 50.2 and 45.1, some 10 % more
+// for the ragged one with 2^7 and 4 in place of 2^5 and 16.)
 //
 // Work: for one (KV head, row tile), short sequences get a CTA each.  Else the
 // pages of all sequences, one after the other, are cut into equal ranges, one
@@ -71,13 +71,13 @@
 // 8, widths 128: 102 us for 604 MB, 5.9 TB/s.  Eight of 16-32 thousand keys:
 // 50 us, of which the merge 4; the 248 MB take 37 us at the measured copy rate,
 // and the kernel without its arithmetic 43.  48 sequences of 4-12000 keys, 4
-// queries, 16 heads on 4, widths 128 and 64: 43.8 us for 125 MB (19 us).  No unit
-// is full: in these two the schedulers issue in 0.59 and 0.53 of the cycles (some
+// queries, 16 heads on 4, widths 128 and 64: 44.5 us for 125 MB (19 us).  No unit
+// is full: in these two the schedulers issue in 0.59 and 0.52 of the cycles (some
 // 590 instructions a page), the ALUs are at 52 and 38 %, the tensor pipe at 28 and
-// 34.  The registers (128 and 168 a thread) leave 3.6 and 2.8 warps a scheduler,
-// and these wait for the fixed latencies of a page's chains (1.3 and 1.5 cycles an
-// issue), for one another (not selected 1.1 and 0.7, math pipe 0.9 and 0.6,
-// dispatch 0.4) and for pages (long scoreboard 0.6 and 0.4).
+// 34.  The registers (128 and 168 a thread) leave 3.7 and 2.8 warps a scheduler,
+// and these wait for the fixed latencies of a page's chains (1.4 and 1.5 cycles an
+// issue), for one another (not selected 1.1 and 0.7, math pipe 0.8 and 0.6,
+// dispatch 0.5 and 0.4) and for pages (long scoreboard 0.8 and 0.4).
 // More or fewer warps, a page of lookahead for the scores, pages or lengths
 // requested across sequences, a deeper ring and an earlier or later start of
 // the merge changed nothing or cost up to 2 % (tried and left out).
@@ -234,8 +234,8 @@ struct CacheCfg {
   // Resident CTAs per SM that the registers are held to (four warps: 128 of a
   // thread for 8 rows, 168 for 16).  One more where key rows of 64 leave
   // registers and many CTAs take turns: 256 sequences of 2048 keys, 32 heads on
-  // 8, 61.1 to 58.7 us, 16 rows on 4 heads 49.1 to 44.4; but not for ranges
-  // (16 rows 21.1 to 23.7 us: more of them, each shorter).
+  // 8, 62.3 to 59.7 us, 16 rows on 4 heads 51.2 to 45.0; but not for ranges
+  // (16 rows 21.4 to 24.0 us: more of them, each shorter).
   static constexpr int kMore = WHOLE && DH == 64 ? 1 : 0;
   static constexpr int kResident =
       WARPS == kDecodeCacheWideWarps ? 1 : (NT == 1 ? kDecodeCacheResident8 : kDecodeCacheResident16) + kMore;

@@ -16,4 +16,6 @@ from ._binding import (  # noqa: F401
     ATTN_CACHE_PAGE_TOKENS, ATTN_ERR_PAGE, ATTN_MAX_AXES, QuantCache, RotaryAxes, attn_cache_append,
     attn_cache_page_bytes, attn_cache_read, attn_fwd_decode_cache, attn_fwd_decode_cache_workspace_bytes,
     attn_qk_norm_rope, attn_qk_norm_rope_bwd, attn_qk_norm_rope_bwd_workspace_bytes, attn_rope_axes,
+    attn_cache_evict, attn_cache_evict_workspace_bytes, attn_cache_weigh, attn_fwd_prefix_cache,
+    attn_fwd_prefix_cache_workspace_bytes,
 )

@@ -181,11 +181,19 @@ def load(path: Optional[Path] = None) -> ctypes.CDLL:
     lib.attn_fwd_decode_cache_workspace_bytes.argtypes = [CA, i32, i32, i32, i32]
     lib.attn_fwd_decode_cache_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_fwd_decode_cache.argtypes = [CA, i32, i32, i32, i32, f, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_fwd_prefix_cache_workspace_bytes.argtypes = [CA, i32, i32, i32, i32, i32]
+    lib.attn_fwd_prefix_cache_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_fwd_prefix_cache.argtypes = [CA, i32, i32, i32, i32, i32, f] + [_vp] * 8 + [ctypes.c_size_t, _vp]
+    lib.attn_cache_weigh.argtypes = [CA, i32, i32, i32, i32, f] + [_vp] * 6
+    lib.attn_cache_evict_workspace_bytes.argtypes = [CA, i32, i32, i32, i32, i32]
+    lib.attn_cache_evict_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_cache_evict.argtypes = [CA, i32, i32, i32, i32, i32] + [_vp] * 7 + [ctypes.c_size_t, _vp]
     for name in ("attn_fwd", "attn_fwd_decode", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main", "attn_bwd_finalize",
                  "attn_get_status", "attn_clear_status", "attn_selftest_wait_timeout", "attn_fwd_varlen",
                  "attn_bwd_varlen", "attn_proj_fwd", "attn_proj_bwd_weight", "attn_proj_bwd_input",
                  "attn_rope", "attn_rope_qk", "attn_rope_axes", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
-                 "attn_cache_append", "attn_cache_read", "attn_fwd_decode_cache"):
+                 "attn_cache_append", "attn_cache_read", "attn_fwd_decode_cache", "attn_fwd_prefix_cache",
+                 "attn_cache_weigh", "attn_cache_evict"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -1200,3 +1208,138 @@ def attn_fwd_decode_cache(Q, cache: QuantCache, page_table, lengths, *, scale: O
                                         lengths.data_ptr(), O.data_ptr(), LSE.data_ptr(), _addr(workspace), size,
                                         torch._C._cuda_getCurrentRawStream(dev.index)), "attn_fwd_decode_cache")
     return O, LSE
+
+
+def _query_args(Q, cache: QuantCache, page_table, lengths):
+    """The arguments that the calls with queries over the cache share, checked:
+    (B, Hq, n_q, max_pages)."""
+    if Q.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("Q must be 4-D [B, Hq, n_q, d_h] and page_table 2-D [B, max_pages]")
+    B, Hq, n_q, _ = Q.shape
+    dev = cache.device
+    max_pages = page_table.shape[1]
+    _check_flat(Q, "Q", torch.bfloat16, (B, Hq, n_q, cache.d_h), dev)
+    _check_flat(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    _check_flat(lengths, "lengths", torch.int32, (B,), dev)
+    return B, Hq, n_q, max_pages
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_cache_bytes(Hkv, d_h, d_v, pages, B, Hq, n_q, prefix_pages, max_pages) -> int:
+    cache = AttnCache(Hkv, d_h, d_v, pages, None)
+    return int(load().attn_fwd_prefix_cache_workspace_bytes(ctypes.byref(cache), B, Hq, n_q, prefix_pages, max_pages))
+
+
+def attn_fwd_prefix_cache_workspace_bytes(cache: QuantCache, B, Hq, n_q, prefix_pages, max_pages) -> int:
+    return _prefix_cache_bytes(cache.Hkv, cache.d_h, cache.d_v, cache.pages, int(B), int(Hq), int(n_q),
+                               int(prefix_pages), int(max_pages))
+
+
+def attn_fwd_prefix_cache(Q, cache: QuantCache, prefix_table, prefix_length, page_table, lengths, *,
+                          scale: Optional[float] = None, O=None, LSE=None, workspace=None, stream=None):
+    """attn_fwd_decode_cache for a batch whose sequences all begin with the same
+    prefix, which is read and worked on once for all of them: prefix_table int32
+    [prefix_pages] and prefix_length int32 [1] (its tokens), page_table int32 [B, max_pages]
+    and lengths int32 [B] of the keys that follow in each sequence (the n_q new
+    tokens counted), all on the device.  Row i of sequence b sees the whole prefix
+    and its own keys j <= lengths[b] - n_q + i.
+    Returns (O [B, Hq, n_q, d_v] bf16, LSE [B, Hq, n_q] fp32)."""
+    B, Hq, n_q, max_pages = _query_args(Q, cache, page_table, lengths)
+    dev = cache.device
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be 1-D [prefix_pages]")
+    prefix_pages = prefix_table.shape[0]
+    _check_flat(prefix_table, "prefix_table", torch.int32, (prefix_pages,), dev)
+    _check_flat(prefix_length, "prefix_length", torch.int32, (1,), dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_fwd_prefix_cache(Q, cache, prefix_table, prefix_length, page_table, lengths, scale=scale, O=O,
+                                         LSE=LSE, workspace=workspace)
+    scale = 1.0 / math.sqrt(cache.d_h) if scale is None else float(scale)
+    os, ls = (B, Hq, n_q, cache.d_v), (B, Hq, n_q)
+    O = torch.empty(os, dtype=torch.bfloat16, device=dev) if O is None else _check_flat(O, "O", torch.bfloat16, os, dev)
+    LSE = (torch.empty(ls, dtype=torch.float32, device=dev) if LSE is None
+           else _check_flat(LSE, "LSE", torch.float32, ls, dev))
+    if workspace is None:
+        size = _prefix_cache_bytes(cache.Hkv, cache.d_h, cache.d_v, cache.pages, B, Hq, n_q, prefix_pages, max_pages)
+        workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _check(load().attn_fwd_prefix_cache(cache.arg(), B, Hq, n_q, prefix_pages, max_pages, scale, Q.data_ptr(),
+                                        prefix_table.data_ptr(), prefix_length.data_ptr(), page_table.data_ptr(),
+                                        lengths.data_ptr(), O.data_ptr(), LSE.data_ptr(), _addr(workspace), size,
+                                        torch._C._cuda_getCurrentRawStream(dev.index)), "attn_fwd_prefix_cache")
+    return O, LSE
+
+
+def attn_cache_weigh(Q, cache: QuantCache, page_table, lengths, LSE, weights, *, scale: Optional[float] = None,
+                     stream=None):
+    """Add to weights [B, Hkv, 32 max_pages] (fp32, in place) the attention weight
+    that each cached token gets from the rows of Q: exp(scale q.k - LSE), summed
+    over the query heads of a KV head and the rows that see the token.  Q,
+    page_table, lengths, scale and LSE are those of attn_fwd_decode_cache or
+    attn_fwd_prefix_cache (the sequences' own tokens).  Returns weights."""
+    B, Hq, n_q, max_pages = _query_args(Q, cache, page_table, lengths)
+    dev = cache.device
+    _check_flat(LSE, "LSE", torch.float32, (B, Hq, n_q), dev)
+    _check_flat(weights, "weights", torch.float32, (B, cache.Hkv, max_pages * ATTN_CACHE_PAGE_TOKENS), dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_cache_weigh(Q, cache, page_table, lengths, LSE, weights, scale=scale)
+    scale = 1.0 / math.sqrt(cache.d_h) if scale is None else float(scale)
+    _check(load().attn_cache_weigh(cache.arg(), B, Hq, n_q, max_pages, scale, Q.data_ptr(), page_table.data_ptr(),
+                                   lengths.data_ptr(), LSE.data_ptr(), weights.data_ptr(),
+                                   torch._C._cuda_getCurrentRawStream(dev.index)), "attn_cache_weigh")
+    return weights
+
+
+def attn_cache_evict_workspace_bytes(cache: QuantCache, B, max_pages, keep, *, first=0, recent=0) -> int:
+    return int(load().attn_cache_evict_workspace_bytes(cache.arg(), int(B), int(max_pages), int(keep), int(first),
+                                                       int(recent)))
+
+
+def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int, *, first: int = 0, recent: int = 0,
+                     new_lengths=None, new_weights=None, kept=None, workspace=None, stream=None):
+    """Cut every sequence of over `keep` tokens to `keep`, each KV head on its own:
+    the `first` first tokens, the `recent` last and, between, those with the
+    largest weights [B, Hkv, 32 max_pages] (fp32) stay and move to the front of the
+    sequence's pages; a token that already is below place keep - recent stays
+    where it is, and the last `recent` keep their order.  page_table int32
+    [B, max_pages], lengths int32 [B].  Returns (new_lengths int32 [B], new_weights
+    like weights, kept int32 [B, Hkv, keep]: the place that the token at each
+    place had, -1 past the new length).  new_weights may be weights; new_lengths
+    may not be lengths."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D [B, max_pages]")
+    B, max_pages = page_table.shape
+    dev, keep = cache.device, int(keep)
+    ws = (B, cache.Hkv, max_pages * ATTN_CACHE_PAGE_TOKENS)
+    ks = (B, cache.Hkv, keep)
+    _check_flat(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    _check_flat(lengths, "lengths", torch.int32, (B,), dev)
+    _check_flat(weights, "weights", torch.float32, ws, dev)
+    if keep <= 0:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_cache_evict")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_cache_evict(cache, page_table, lengths, weights, keep, first=first, recent=recent,
+                                    new_lengths=new_lengths, new_weights=new_weights, kept=kept, workspace=workspace)
+    new_lengths = (torch.empty((B,), dtype=torch.int32, device=dev) if new_lengths is None
+                   else _check_flat(new_lengths, "new_lengths", torch.int32, (B,), dev))
+    new_weights = (torch.empty(ws, dtype=torch.float32, device=dev) if new_weights is None
+                   else _check_flat(new_weights, "new_weights", torch.float32, ws, dev))
+    kept = (torch.empty(ks, dtype=torch.int32, device=dev) if kept is None
+            else _check_flat(kept, "kept", torch.int32, ks, dev))
+    if workspace is None:
+        size = attn_cache_evict_workspace_bytes(cache, B, max_pages, keep, first=first, recent=recent)
+        workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _check(load().attn_cache_evict(cache.arg(), B, max_pages, keep, int(first), int(recent), page_table.data_ptr(),
+                                   lengths.data_ptr(), weights.data_ptr(), new_lengths.data_ptr(),
+                                   new_weights.data_ptr(), kept.data_ptr(), _addr(workspace), size,
+                                   torch._C._cuda_getCurrentRawStream(dev.index)), "attn_cache_evict")
+    return new_lengths, new_weights, kept

@@ -987,6 +987,36 @@ DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
   return d;
 }
 
+// How attn_fwd_prefix_cache divides the work: the sequences' own keys as
+// attn_fwd_decode_cache does, and the prefix among row tiles (of the rows of
+// the whole batch) and ranges of its pages.
+struct PrefixCachePlan {
+  DecodeCachePlan own;
+  int tile_rows, chunks, ranges;
+  size_t off_own, off_oall, off_lall, off_opart, off_lpart, off_used, bytes;
+};
+
+PrefixCachePlan prefix_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int prefix_pages, int max_pages) {
+  PrefixCachePlan d;
+  d.own = decode_cache_plan(c, B, Hq, n_q, max_pages);
+  const int64_t R = static_cast<int64_t>(B) * (Hq / c->Hkv) * n_q;
+  d.tile_rows = R > 8 ? 16 : 8;
+  d.chunks = static_cast<int>((R + d.tile_rows - 1) / d.tile_rows);
+  const int64_t tiles = static_cast<int64_t>(c->Hkv) * d.chunks;
+  const int64_t resident = 152 * (d.tile_rows == 8 ? kDecodeCacheResident8 : kDecodeCacheResident16);
+  const int64_t most = (prefix_pages + kMinRangePages - 1) / kMinRangePages;
+  d.ranges = static_cast<int>(std::max<int64_t>(1, std::min(resident / tiles, most)));
+  const size_t rows = static_cast<size_t>(B) * Hq * n_q, parts = static_cast<size_t>(tiles) * d.ranges * d.tile_rows;
+  d.off_own = 0;
+  d.off_oall = d.off_own + d.own.bytes;
+  d.off_lall = d.off_oall + round256(rows * c->d_v * sizeof(float));
+  d.off_opart = d.off_lall + round256(rows * sizeof(float));
+  d.off_lpart = d.off_opart + round256(parts * c->d_v * sizeof(float));
+  d.off_used = d.off_lpart + round256(parts * sizeof(float));
+  d.bytes = d.off_used + 256;
+  return d;
+}
+
 int check_decode_cache(const attn_cache* c, int B, int Hq, int n_q, int max_pages) {
   const int rc = check_cache(c);
   if (rc) return rc;
@@ -995,6 +1025,72 @@ int check_decode_cache(const attn_cache* c, int B, int Hq, int n_q, int max_page
   if (static_cast<int64_t>(B) * max_pages > int64_t{1} << 30) return ATTN_ERR_SHAPE;
   if (static_cast<int64_t>(B) * Hq > (int64_t{1} << 31) / 16 - 1) return ATTN_ERR_SHAPE;
   if (n_q > 16) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// The parts of a call over the cache that attn_fwd_decode_cache and the own keys
+// of attn_fwd_prefix_cache share.
+void fill_decode_cache(DecCacheParams* p, const DecodeCachePlan& plan, const attn_cache* c, int B, int Hq, int n_q,
+                       int max_pages, float scale, const void* Q, const int32_t* table, const int32_t* lengths, void* O,
+                       float* LSE, uint8_t* ws, unsigned int* status) {
+  std::memset(p, 0, sizeof(*p));
+  p->B = B;
+  p->Hkv = c->Hkv;
+  p->group = Hq / c->Hkv;
+  p->n_q = n_q;
+  p->max_pages = max_pages;
+  p->pages = c->pages;
+  p->pool = static_cast<const uint8_t*>(c->pool);
+  p->table = table;
+  p->lengths = lengths;
+  p->scale_log2 = scale * kLog2e;
+  p->wait_limit_ns = kDefaultWaitLimitNs;
+  p->Q = Q;
+  p->O = O;
+  p->LSE = LSE;
+  if (plan.bytes > 0) {
+    p->Opart = reinterpret_cast<float*>(ws);
+    p->Lpart = reinterpret_cast<float*>(ws + plan.opart_bytes);
+    p->first_page = reinterpret_cast<int32_t*>(ws + plan.opart_bytes + plan.lpart_bytes);
+  }
+  p->tile_rows = plan.tile_rows;
+  p->chunks = plan.chunks;
+  p->ranges = plan.ranges;
+  p->whole_seqs = plan.whole_seqs;
+  p->wide = plan.wide;
+  p->status = status;
+  p->batch = B;
+}
+
+int check_prefix_cache(const attn_cache* c, int B, int Hq, int n_q, int prefix_pages, int max_pages) {
+  const int rc = check_decode_cache(c, B, Hq, n_q, max_pages);
+  if (rc) return rc;
+  if (prefix_pages <= 0 || prefix_pages > (1 << 26) - 1) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+int check_cache_evict(const attn_cache* c, int B, int max_pages, int keep, int first, int recent) {
+  const int rc = check_cache(c);
+  if (rc) return rc;
+  if (B <= 0 || max_pages <= 0 || max_pages > (1 << 26) - 1) return ATTN_ERR_SHAPE;
+  if (static_cast<int64_t>(B) * c->Hkv > (int64_t{1} << 31) - 1) return ATTN_ERR_SHAPE;
+  if (keep <= 0 || first < 0 || recent < 0 || static_cast<int64_t>(first) + recent > keep) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+// Tokens of one head of a sequence that may move to another place, besides the
+// newest: no more than are chosen by weight, nor than places behind the budget.
+int64_t evict_most_moves(int max_pages, int keep, int first, int recent) {
+  const int64_t cap = static_cast<int64_t>(max_pages) * kPageTokens;
+  return std::max<int64_t>(0, std::min<int64_t>(keep - first - recent, cap - keep));
+}
+
+// Pointers of 32-bit arrays: not NULL, 4-byte aligned.
+int check_words(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs) {
+    if (!p) return ATTN_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return ATTN_ERR_ALIGN;
+  }
   return ATTN_OK;
 }
 
@@ -1894,6 +1990,81 @@ int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
   rc = device_status_ptr(&status);
   if (rc) return rc;
   DecCacheParams p;
+  fill_decode_cache(&p, plan, cache, B, Hq, n_q, max_pages, scale, Q, page_table, lengths, O, LSE,
+                    static_cast<uint8_t*>(workspace), status);
+  const cudaError_t e = launch_decode_cache(cache->d_h, cache->d_v, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_fwd_prefix_cache_workspace_bytes(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q,
+                                             int32_t prefix_pages, int32_t max_pages) {
+  if (check_prefix_cache(cache, B, Hq, n_q, prefix_pages, max_pages) != ATTN_OK) return 0;
+  return prefix_cache_plan(cache, B, Hq, n_q, prefix_pages, max_pages).bytes;
+}
+
+int attn_fwd_prefix_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q, int32_t prefix_pages,
+                          int32_t max_pages, float scale, const void* Q, const int32_t* prefix_table,
+                          const int32_t* prefix_length, const int32_t* page_table, const int32_t* lengths, void* O,
+                          float* LSE, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_prefix_cache(cache, B, Hq, n_q, prefix_pages, max_pages);
+  if (rc) return rc;
+  rc = check_scale(scale);
+  if (rc) return rc;
+  rc = check_ptrs({cache->pool, Q, O, LSE});
+  if (rc) return rc;
+  rc = check_words({prefix_table, prefix_length, page_table, lengths});
+  if (rc) return rc;
+  const PrefixCachePlan plan = prefix_cache_plan(cache, B, Hq, n_q, prefix_pages, max_pages);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.bytes)
+    return ATTN_ERR_WORKSPACE;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PrefixMergeParams m;
+  fill_decode_cache(&m.own, plan.own, cache, B, Hq, n_q, max_pages, scale, Q, page_table, lengths, O, LSE,
+                    ws + plan.off_own, status);
+  m.own.Oall = reinterpret_cast<float*>(ws + plan.off_oall);
+  m.own.Lall = reinterpret_cast<float*>(ws + plan.off_lall);
+  DecCacheParams prefix = m.own;
+  prefix.B = 1;
+  prefix.max_pages = prefix_pages;
+  prefix.table = prefix_table;
+  prefix.lengths = prefix_length;
+  prefix.Opart = reinterpret_cast<float*>(ws + plan.off_opart);
+  prefix.Lpart = reinterpret_cast<float*>(ws + plan.off_lpart);
+  prefix.first_page = reinterpret_cast<int32_t*>(ws + plan.off_used);
+  prefix.tile_rows = plan.tile_rows;
+  prefix.chunks = plan.chunks;
+  prefix.ranges = plan.ranges;
+  prefix.whole_seqs = prefix.wide = 0;
+  m.Opart = prefix.Opart;
+  m.Lpart = prefix.Lpart;
+  m.used = prefix.first_page;
+  m.tile_rows = plan.tile_rows;
+  m.chunks = plan.chunks;
+  m.splits = plan.ranges;
+  const cudaError_t e = launch_prefix_cache(cache->d_h, cache->d_v, prefix, m, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_cache_weigh(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q, int32_t max_pages, float scale,
+                     const void* Q, const int32_t* page_table, const int32_t* lengths, const float* LSE, float* weights,
+                     void* stream) {
+  int rc = check_decode_cache(cache, B, Hq, n_q, max_pages);
+  if (rc) return rc;
+  rc = check_scale(scale);
+  if (rc) return rc;
+  rc = check_ptrs({cache->pool, Q});
+  if (rc) return rc;
+  rc = check_words({page_table, lengths, LSE, weights});
+  if (rc) return rc;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  CacheWeighParams p;
   p.B = B;
   p.Hkv = cache->Hkv;
   p.group = Hq / cache->Hkv;
@@ -1906,19 +2077,61 @@ int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
   p.scale_log2 = scale * kLog2e;
   p.wait_limit_ns = kDefaultWaitLimitNs;
   p.Q = Q;
-  p.O = O;
   p.LSE = LSE;
-  p.Opart = plan.bytes > 0 ? static_cast<float*>(workspace) : nullptr;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.Lpart = plan.bytes > 0 ? reinterpret_cast<float*>(ws + plan.opart_bytes) : nullptr;
-  p.first_page = plan.bytes > 0 ? reinterpret_cast<int32_t*>(ws + plan.opart_bytes + plan.lpart_bytes) : nullptr;
-  p.tile_rows = plan.tile_rows;
-  p.chunks = plan.chunks;
-  p.ranges = plan.ranges;
-  p.whole_seqs = plan.whole_seqs;
-  p.wide = plan.wide;
+  p.weights = weights;
+  const int64_t most = (static_cast<int64_t>(B) * max_pages + kMinRangePages - 1) / kMinRangePages;
+  p.ranges = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(152 * kCacheWeighResident / cache->Hkv, most)));
   p.status = status;
-  const cudaError_t e = launch_decode_cache(cache->d_h, cache->d_v, p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_cache_weigh(cache->d_h, p, cache->d_v, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_cache_evict_workspace_bytes(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep,
+                                        int32_t first, int32_t recent) {
+  if (check_cache_evict(cache, B, max_pages, keep, first, recent) != ATTN_OK) return 0;
+  return round256(static_cast<size_t>(B) * cache->Hkv * 2 * evict_most_moves(max_pages, keep, first, recent) *
+                  sizeof(int32_t));
+}
+
+int attn_cache_evict(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep, int32_t first, int32_t recent,
+                     const int32_t* page_table, const int32_t* lengths, const float* weights, int32_t* new_lengths,
+                     float* new_weights, int32_t* kept, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache_evict(cache, B, max_pages, keep, first, recent);
+  if (rc) return rc;
+  rc = check_ptrs({cache->pool});
+  if (rc) return rc;
+  rc = check_words({page_table, lengths, weights, new_lengths, new_weights});
+  if (rc) return rc;
+  if ((reinterpret_cast<uintptr_t>(kept) & 3u) != 0) return ATTN_ERR_ALIGN;
+  if (new_lengths == lengths) return ATTN_ERR_SHAPE;     // (the heads of a sequence read its length at any time)
+  const size_t need = attn_cache_evict_workspace_bytes(cache, B, max_pages, keep, first, recent);
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need))
+    return ATTN_ERR_WORKSPACE;
+  // ---- CUDA from here on ----
+  unsigned int* status = nullptr;
+  rc = device_status_ptr(&status);
+  if (rc) return rc;
+  CacheEvictParams p;
+  p.B = B;
+  p.Hkv = cache->Hkv;
+  p.dh = cache->d_h;
+  p.dv = cache->d_v;
+  p.max_pages = max_pages;
+  p.keep = keep;
+  p.first = first;
+  p.recent = recent;
+  p.pages = cache->pages;
+  p.pool = static_cast<uint8_t*>(cache->pool);
+  p.table = page_table;
+  p.lengths = lengths;
+  p.weights = weights;
+  p.new_lengths = new_lengths;
+  p.new_weights = new_weights;
+  p.kept = kept;
+  p.lists = static_cast<int32_t*>(workspace);
+  p.most_moves = static_cast<int32_t>(evict_most_moves(max_pages, keep, first, recent));
+  p.status = status;
+  const cudaError_t e = launch_cache_evict(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

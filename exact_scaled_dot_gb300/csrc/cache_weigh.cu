@@ -1,0 +1,298 @@
+// cache_weigh.cu -- attn_cache_weigh: the attention weight that each cached
+// token gets from the new queries, added to what it has had, on sm_103a.
+//
+//   w[b][h][j] += sum over the query heads r of KV head h and the rows i that
+//                 see key j of A_ij,  A_ij = exp(scale q_i . k_j - LSE_i)
+// ("Appendix A.10 -- Attention matrices and backpropagation", eqs. A.10.1 and
+// A.10.2 with the log-sum-exp of the attention, over whatever keys that had).
+// The normaliser is given, so there is no running maximum and every page is on
+// its own: keys are the M side of K Q^T, as in the attention over this cache,
+// and a key's weight is a sum over its row of the accumulators, in one order.
+//
+// Work: the pages of all sequences, end to end, are cut into equal ranges, one
+// per CTA of a KV head; its warps take every fourth page, K's codes and words of
+// which (half a page's block) two bulk copies bring into a ring of the warp's
+// own.  Q's fragments are kept in shared memory, a sequence at a time, so that
+// up to 256 query rows pass over a page that is read once.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "cache_mma.cuh"
+
+namespace esd {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStages = 4;
+constexpr int kResident = kCacheWeighResident;     // CTAs per SM that the registers are held to
+constexpr int kMostGroups = 32;       // of eight query rows in shared memory: more pass over the pages again
+
+// What a row of Q brings: p = exp2(f s + add) for the keys below lim.
+struct RowTerms {
+  float f, add;
+  int lim, unused;
+};
+
+template <int DH, int DV>
+struct WeighCfg {
+  static constexpr int GK = DH / kQuantGroup;
+  static constexpr int kCodes = kPageTokens * DH / 2, kWords = kPageTokens * GK * 4;
+  static constexpr int kStage = kCodes + kWords;
+  static constexpr int kBlock = page_head_bytes(DH, DV);
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kOffBar = kRing;
+  static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
+  static constexpr int kOffRows = (kOffAbort + 8 + 127) / 128 * 128;
+  // Eight query rows: their terms and, of each group of 64 dims, two 16-byte
+  // chunks of fp16 fragments per lane.
+  static constexpr int kRowBytes = 8 * static_cast<int>(sizeof(RowTerms)) + GK * 2 * 32 * 16;
+  static_assert(kCodes % 16 == 0 && kWords % 16 == 0 && kStage % 16 == 0, "bulk copies");
+  static int smem_bytes(int row_groups) { return kOffRows + row_groups * kRowBytes; }
+};
+
+template <int DH, int DV>
+__global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const __grid_constant__ CacheWeighParams p) {
+  using C = WeighCfg<DH, DV>;
+  constexpr int GK = C::GK;
+  extern __shared__ __align__(128) uint8_t smem[];
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int g = static_cast<int>(lane >> 2), t = static_cast<int>(lane & 3);
+  const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
+  const uint8_t* ring_ptr = smem + warp * kStages * C::kStage;
+  const uint32_t bars = smem_u32(smem) + C::kOffBar + warp * kStages * 8;
+  if (threadIdx.x == 0) *abort_flag = status_blocks(p.status) ? 2 : 0;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+    fence_mbar_init();
+  }
+  const Ranges rg = page_ranges(p, lane);
+  __syncthreads();
+
+  const int h = static_cast<int>(blockIdx.x) / p.ranges;
+  const int range = static_cast<int>(blockIdx.x) - h * p.ranges;
+  const int R = p.group * p.n_q, groups = (R + 7) / 8;
+  const int begin = range * rg.per;
+  const int end = begin + rg.per < rg.total ? begin + rg.per : rg.total;
+  int b = p.B, seq0 = 0;           // the sequence that `begin` lies in, and its first page's place
+  if (begin < rg.total) b = sequence_at(p, begin, lane, seq0);
+
+  uint32_t st = 0, parity = 0;
+  auto after = [](uint32_t s) { return s + 1 == kStages ? 0u : s + 1; };
+  for (; b < p.B && *abort_flag != 2; ++b) {
+    int len;
+    const int npages = pages_of(p, b, len);
+    if (seq0 >= end) break;
+    if (npages == 0) continue;
+    const int first = begin > seq0 ? begin - seq0 : 0;
+    const int last = end < seq0 + npages ? end - seq0 : npages;
+    seq0 += npages;
+
+    for (int g0 = 0; g0 < groups; g0 += kMostGroups) {
+    const int g_end = groups - g0 < kMostGroups ? groups - g0 : kMostGroups;
+    // This warp's pages: first + warp, + kWarps, ...
+    const int mine = (last - first - static_cast<int>(warp) + kWarps - 1) / kWarps;
+    const int n = mine > 0 ? mine : 0;
+    const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages + first + warp;
+    uint32_t bad = 0u;             // bit s: stage s stands for a page outside the pool
+    int issued = 0, ids = 0;
+    auto issue = [&](uint32_t s) {
+      if ((issued & 31) == 0) ids = issued + static_cast<int>(lane) < n ? table[(issued + static_cast<int>(lane)) * kWarps] : 0;
+      const int id = __shfl_sync(0xffffffffu, ids, issued & 31);
+      const bool in_pool = id >= 0 && id < p.pages;
+      bad = in_pool ? bad & ~(1u << s) : bad | (1u << s);
+      if (lane == 0) {
+        if (in_pool) {
+          const uint8_t* src = p.pool + (static_cast<int64_t>(id) * p.Hkv + h) * C::kBlock;
+          mbar_arrive_expect_tx(bars + 8 * s, C::kStage);
+          bulk_load(ring + s * C::kStage, src + off_k_codes(), C::kCodes, bars + 8 * s);
+          bulk_load(ring + s * C::kStage + C::kCodes, src + off_k_words(DH, DV), C::kWords, bars + 8 * s);
+        } else {
+          record_status(p.status, ATTN_ERR_PAGE);
+          mbar_arrive(bars + 8 * s);
+        }
+      }
+      ++issued;
+    };
+    for (uint32_t s = st; issued < kStages && issued < n; s = after(s)) issue(s);
+
+    // ---- Q's fragments and the rows' terms, eight rows a warp at a time ----
+    // (dims of a lane as in the attention: k-step 4 gk + 2 w + e holds the dims
+    // 64 gk + 16 t + 8 w + {2e, 2e+4} and {2e+1, 2e+5}.)
+    for (int nt = static_cast<int>(warp); nt < g_end; nt += kWarps) {
+      const int r = 8 * (g0 + nt) + g;
+      const int64_t row = (static_cast<int64_t>(b) * p.Hkv + h) * R + (r < R ? r : 0);
+      const uint4* q = reinterpret_cast<const uint4*>(p.Q) + row * (DH / 8);
+      uint4 qv[GK][2];
+      uint32_t m = 0u;
+#pragma unroll
+      for (int gk = 0; gk < GK; ++gk)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          qv[gk][w] = r < R ? q[gk * 8 + 2 * t + w] : make_uint4(0u, 0u, 0u, 0u);
+          m = bf16_absmax_fold(m, qv[gk][w]);
+        }
+      uint32_t mb = __float_as_uint(bf16_absmax_value(m));     // (as bits, so that a NaN is the largest)
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+      const float mx = __uint_as_float(mb);
+      int e = 0;                                               // 2^14 <= mx 2^e < 2^15
+      if (mx > 0.f && mx < INFINITY) e = 14 - ilogbf(mx);
+      e = e > 120 ? 120 : e;
+      uint8_t* to = smem + C::kOffRows + nt * C::kRowBytes;
+      uint4* frag = reinterpret_cast<uint4*>(to + 8 * sizeof(RowTerms)) + lane;
+#pragma unroll
+      for (int gk = 0; gk < GK; ++gk)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint4 u = bf16x8_to_f16x8_scaled(qv[gk][w], exp2_int(e));
+          frag[(gk * 2 + w) * 32] = make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
+                                               __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
+        }
+      if (t == 0) {
+        RowTerms x;
+        x.f = fmaxf(p.scale_log2 * exp2_int(-e) * 512.0f, 0x1p-126f);
+        if (!(mx < INFINITY)) x.f = __uint_as_float(0x7FC00000u);
+        x.lim = r < R ? len - p.n_q + 1 + r % p.n_q : 0;
+        const float lse = r < R ? p.LSE[row] : -INFINITY;
+        x.add = -lse * kLog2e;
+        // Rows without a key, and none at all, add nothing.
+        if (x.lim <= 0 || lse == -INFINITY) x.f = 0x1p-126f, x.add = -INFINITY;
+        x.unused = 0;
+        reinterpret_cast<RowTerms*>(to)[g] = x;
+      }
+    }
+    __syncthreads();
+
+    float* const wrow = p.weights + (static_cast<int64_t>(b) * p.Hkv + h) * p.max_pages * kPageTokens;
+    for (int done = 0; done < n; ++done) {
+      const int key0 = (first + static_cast<int>(warp) + done * kWarps) * kPageTokens;
+      // The key that the page's sums over rows end with in this lane.
+      const int key = key0 + 8 * t + g;
+      const bool mine_here = key < len && !((bad >> st) & 1u);
+      const float was = mine_here ? wrow[key] : 0.f;
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, parity, abort_flag, p.wait_limit_ns))) {
+        // Every copy already in flight must land before the CTA can exit.
+        int no_abort = 0;
+        for (; done < issued; ++done) {
+          mbar_wait(bars + 8 * st, parity, &no_abort, p.wait_limit_ns);
+          st = after(st);
+          parity ^= st == 0 ? 1u : 0u;
+        }
+        break;
+      }
+      const uint8_t* blk = ring_ptr + st * C::kStage;
+      // ---- the page's codes as fragments, (c - z) 2^-9 ----
+      uint32_t a[2][GK][4][4];
+      float sc[2][2][GK];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const int ka = 16 * kb + g;
+        uint32_t pa[GK], pb[GK];
+        lds_words<GK>(blk + C::kCodes + ka * (GK * 4), pa);
+        lds_words<GK>(blk + C::kCodes + (ka + 8) * (GK * 4), pb);
+#pragma unroll
+        for (int gk = 0; gk < GK; ++gk) {
+          const uint8_t* kc = blk + gk * 32 + t * 8;
+          const uint2 wa = lds64(kc + ka * (DH / 2)), wb = lds64(kc + (ka + 8) * (DH / 2));
+          const uint32_t za = hfma2_bits(__byte_perm(pa[gk], 0u, 0x4040), kMinusTwo15, 0u);
+          const uint32_t zb = hfma2_bits(__byte_perm(pb[gk], 0u, 0x4040), kMinusTwo15, 0u);
+#pragma unroll
+          for (int step = 0; step < 4; ++step) {
+            uint32_t xa = step < 2 ? wa.x : wa.y, xb = step < 2 ? wb.x : wb.y;
+            if (step & 1) xa >>= 8, xb >>= 8;
+            a[kb][gk][step][0] = hfma2_bits(low_nibbles(xa), kTwo15, za);
+            a[kb][gk][step][1] = hfma2_bits(low_nibbles(xb), kTwo15, zb);
+            a[kb][gk][step][2] = hfma2_bits(high_nibbles(xa), kTwo11, za);
+            a[kb][gk][step][3] = hfma2_bits(high_nibbles(xb), kTwo11, zb);
+          }
+          sc[kb][0][gk] = bf16_hi(pa[gk]);
+          sc[kb][1][gk] = bf16_hi(pb[gk]);
+        }
+      }
+      __syncwarp();            // every lane has read the stage
+      if (issued < n) issue(st);
+      st = after(st);
+      parity ^= st == 0 ? 1u : 0u;
+
+      // ---- the sums over all rows, eight at a time ----
+      const bool edge = key0 + kPageTokens > len - p.n_q + 1;   // some row does not see all of the page
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};                      // of the lane's rows: keys 8 i + g
+      for (int nt = 0; nt < g_end; ++nt) {
+        const uint8_t* from = smem + C::kOffRows + nt * C::kRowBytes;
+        const uint4* frag = reinterpret_cast<const uint4*>(from + 8 * sizeof(RowTerms)) + lane;
+        const RowTerms x0 = reinterpret_cast<const RowTerms*>(from)[2 * t];
+        const RowTerms x1 = reinterpret_cast<const RowTerms*>(from)[2 * t + 1];
+        float s[2][4];
+#pragma unroll
+        for (int gk = 0; gk < GK; ++gk) {
+          const uint4 q0 = frag[gk * 64], q1 = frag[gk * 64 + 32];
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            float acc[4];
+            const uint32_t(*x)[4] = a[kb][gk];
+            mma_f16(acc, x[0][0], x[0][1], x[0][2], x[0][3], q0.x, q0.y, 0.f, 0.f, 0.f, 0.f);
+            mma_f16(acc, x[1][0], x[1][1], x[1][2], x[1][3], q0.z, q0.w);
+            mma_f16(acc, x[2][0], x[2][1], x[2][2], x[2][3], q1.x, q1.y);
+            mma_f16(acc, x[3][0], x[3][1], x[3][2], x[3][3], q1.z, q1.w);
+            const float sa = sc[kb][0][gk], sb = sc[kb][1][gk];
+            if (gk == 0) {
+              fmul2(s[kb][0], s[kb][1], acc[0], acc[1], sa, sa);
+              fmul2(s[kb][2], s[kb][3], acc[2], acc[3], sb, sb);
+            } else {
+              ffma2(s[kb][0], s[kb][1], acc[0], acc[1], sa, sa, s[kb][0], s[kb][1]);
+              ffma2(s[kb][2], s[kb][3], acc[2], acc[3], sb, sb, s[kb][2], s[kb][3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float p0, p1;
+          ffma2(p0, p1, s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1], x0.f, x1.f, x0.add, x1.add);
+          p0 = fast_exp2(p0);
+          p1 = fast_exp2(p1);
+          if (edge) {
+            const int k = key0 + 8 * i + g;
+            p0 = k < x0.lim ? p0 : 0.f;
+            p1 = k < x1.lim ? p1 : 0.f;
+          }
+          sum[i] += p0 + p1;
+        }
+      }
+      // Over the four lanes of a key; lane t ends with the keys 8 t + g.
+      const float keep0 = t & 2 ? sum[2] : sum[0], keep1 = t & 2 ? sum[3] : sum[1];
+      const float give0 = t & 2 ? sum[0] : sum[2], give1 = t & 2 ? sum[1] : sum[3];
+      const float two0 = keep0 + __shfl_xor_sync(0xffffffffu, give0, 2);
+      const float two1 = keep1 + __shfl_xor_sync(0xffffffffu, give1, 2);
+      const float all = (t & 1 ? two1 : two0) + __shfl_xor_sync(0xffffffffu, t & 1 ? two0 : two1, 1);
+      if (mine_here) wrow[key] = was + all;
+    }
+    __syncthreads();           // the rows' fragments are free for the next ones
+    if (*abort_flag) break;
+    }
+  }
+  if (threadIdx.x == 0 && *abort_flag == 1) record_status(p.status, ATTN_ERR_TIMEOUT);
+}
+
+template <int DH, int DV>
+cudaError_t launch_t(const CacheWeighParams& p, cudaStream_t stream) {
+  using C = WeighCfg<DH, DV>;
+  const int groups = (p.group * p.n_q + 7) / 8;
+  const int bytes = C::smem_bytes(groups < kMostGroups ? groups : kMostGroups);
+  auto kern = cache_weigh_kernel<DH, DV>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(p.Hkv * p.ranges), kThreads, bytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weigh(int dh, const CacheWeighParams& p, int dv, cudaStream_t stream) {
+  if (dh == 128 && dv == 128) return launch_t<128, 128>(p, stream);
+  if (dh == 64 && dv == 64) return launch_t<64, 64>(p, stream);
+  if (dh == 128 && dv == 64) return launch_t<128, 64>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace esd

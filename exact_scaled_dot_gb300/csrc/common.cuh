@@ -346,7 +346,7 @@ struct CacheIoParams {
   unsigned int* status;
 };
 
-// Attention over the 4-bit cache (decode_cache.cu): warps of a CTA, resident
+// Attention over the 4-bit cache (decode_cache_kernel.cuh): warps of a CTA, resident
 // CTAs per SM of the kernels for 8 and 16 query rows, and the fewest pages
 // that a CTA takes (one per warp).  The wide kernel has a CTA per SM.
 constexpr int kDecodeCacheWarps = 4;
@@ -376,6 +376,55 @@ struct DecCacheParams {
   int32_t ranges;              // CTAs of one row tile, over the pages of all sequences
   int32_t whole_seqs;          // 1: each takes one whole sequence (ranges = B) and there is no merge
   int32_t wide;                // 1: kDecodeCacheWideWarps warps each
+  unsigned int* status;
+  // A prefix for the whole batch (attn_fwd_prefix_cache) and, besides it, each
+  // sequence's own keys.
+  int32_t batch;               // sequences whose rows see the prefix
+  float* Oall;                 // fp32 [B][Hq][n_q][d_v] of the sequences that one CTA has seen whole
+  float* Lall;                 // fp32 [B][Hq][n_q]
+};
+
+// Merge of attn_fwd_prefix_cache: for each query row the parts of the prefix
+// and those of its own sequence (as `own` describes them).
+struct PrefixMergeParams {
+  DecCacheParams own;          // O, LSE: the outputs
+  const float* Opart;          // fp32 [Hkv chunks][splits][tile_rows][d_v] of the prefix
+  const float* Lpart;
+  const int32_t* used;         // splits that have keys
+  int32_t tile_rows, chunks, splits;
+};
+
+// Attention weights added up per cached token (cache_weigh.cu): resident CTAs
+// per SM (fewer where a KV head has over 64 query rows).
+constexpr int kCacheWeighResident = 4;
+struct CacheWeighParams {
+  int32_t B, Hkv, group, n_q, max_pages;
+  int64_t pages;
+  const uint8_t* pool;
+  const int32_t* table;        // [B][max_pages]
+  const int32_t* lengths;      // [B]
+  float scale_log2;            // scale * log2(e)
+  uint64_t wait_limit_ns;
+  const void* Q;               // bf16 [B][Hq][n_q][d_h]
+  const float* LSE;            // fp32 [B][Hq][n_q]
+  float* weights;              // fp32 [B][Hkv][32 max_pages]
+  int32_t ranges;              // CTAs of one KV head, over the pages of all sequences
+  unsigned int* status;
+};
+
+// Tokens chosen by their weights and moved to the front (cache_evict.cu).
+struct CacheEvictParams {
+  int32_t B, Hkv, dh, dv, max_pages, keep, first, recent;
+  int64_t pages;
+  uint8_t* pool;
+  const int32_t* table;        // [B][max_pages]
+  const int32_t* lengths;      // [B]
+  const float* weights;        // fp32 [B][Hkv][32 max_pages]
+  int32_t* new_lengths;        // [B]
+  float* new_weights;          // fp32 [B][Hkv][32 max_pages], may be weights
+  int32_t* kept;               // [B][Hkv][keep], or nullptr
+  int32_t* lists;              // [B][Hkv][2][most_moves]: tokens that move, and their places
+  int32_t most_moves;
   unsigned int* status;
 };
 
@@ -417,6 +466,11 @@ cudaError_t launch_qk_bwd(QkParams p, float* dgq, float* dgk, cudaStream_t strea
 cudaError_t launch_cache_append(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_decode_cache(int dh, int dv, const DecCacheParams& p, cudaStream_t stream);
+// The prefix (as one sequence), then the sequences' own keys, then their merge.
+cudaError_t launch_prefix_cache(int dh, int dv, const DecCacheParams& prefix, const PrefixMergeParams& merge,
+                                cudaStream_t stream);
+cudaError_t launch_cache_weigh(int dh, const CacheWeighParams& p, int dv, cudaStream_t stream);
+cudaError_t launch_cache_evict(const CacheEvictParams& p, cudaStream_t stream);
 // Zero n floats (n a multiple of 4, 16-byte aligned).
 cudaError_t launch_zero_f32(float* p, int64_t n, cudaStream_t stream);
 // dK, dV (bf16, caller strides) from the fp32 sums of a query-head split:

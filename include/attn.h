@@ -617,6 +617,81 @@ int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
                           const void* Q, const int32_t* page_table, const int32_t* lengths, void* O, float* LSE,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* attn_fwd_decode_cache for a batch whose sequences all begin with the same
+ * prefix (a system prompt, a document, the prompt of several samples), which
+ * is read and worked on once for all of them: for every KV head the rows of
+ * the whole batch are one block of queries over it.  The keys of sequence b
+ * are the prefix's, 0 .. *prefix_length - 1 (key j in page prefix_table[j / 32]
+ * at place j % 32), and then its own lengths[b] (page_table[b], as in
+ * attn_fwd_decode_cache, the n_q new tokens among them).  Row i sees all of
+ * the prefix and its sequence's own keys j <= lengths[b] - n_q + i; O and LSE
+ * are those of the softmax over both.  prefix_table: device int32
+ * [prefix_pages]; prefix_length: device int32, one number; both are read when
+ * the call runs, like page_table [B][max_pages] and lengths [B].  A length of
+ * 0 (of the prefix, of a sequence's own keys, of both) leaves those keys out;
+ * rows without a visible key, rows of Q that are not finite, page numbers and
+ * lengths out of range are as in attn_fwd_decode_cache, and so is the
+ * precision.  (A prefix of several batches stays in its pages: its tokens are
+ * not among those that attn_cache_evict moves.)
+ * `workspace`: attn_fwd_prefix_cache_workspace_bytes() bytes, 256-byte
+ * aligned; it depends on the sizes only. */
+size_t attn_fwd_prefix_cache_workspace_bytes(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q,
+                                             int32_t prefix_pages, int32_t max_pages);
+int attn_fwd_prefix_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q, int32_t prefix_pages,
+                          int32_t max_pages, float scale, const void* Q, const int32_t* prefix_table,
+                          const int32_t* prefix_length, const int32_t* page_table, const int32_t* lengths, void* O,
+                          float* LSE, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The attention weight that each cached token gets from the new queries, added
+ * to weights, fp32 [B][Hkv][32 max_pages] (device, token j of sequence b for
+ * KV head h at [b][h][j]):
+ *   weights[b][h][j] += sum over the query heads r of h and the rows i that see
+ *                       j of exp(scale q_i . k_j - LSE[b][r][i]),
+ * the A_ij of the attention that gave LSE: attn_fwd_decode_cache's, or
+ * attn_fwd_prefix_cache's (the own tokens' share of the softmax over both).  Q, page_table,
+ * lengths and visible sets are that call's; scale too.  Only places below a
+ * sequence's length are touched, and the sums are taken in one order.  A row
+ * that sees no key, or whose LSE is -inf, adds nothing; a row of Q that is not
+ * finite gives NaN where it sees a key, as its LSE does.  Keys of a page outside
+ * the pool get nothing added, a length above 32 max_pages is cut; both record
+ * ATTN_ERR_PAGE. */
+int attn_cache_weigh(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q, int32_t max_pages, float scale,
+                     const void* Q, const int32_t* page_table, const int32_t* lengths, const float* LSE, float* weights,
+                     void* stream);
+
+/* Cut the sequences of a cache to `keep` tokens.  For each sequence of n =
+ * lengths[b] > keep tokens and each KV head on its own, these stay: the
+ * `first` first tokens, the `recent` last ones and, of those between, the
+ * keep - first - recent with the largest weights[b][h][j] (equal ones: the lowest
+ * places; NaN counts as the largest).  They move to places 0 .. keep - 1 of the
+ * sequence's pages: a token whose place is below keep - recent stays there,
+ * the places below keep - recent that become free take, in ascending order,
+ * those that stay from the places behind, and the last `recent` follow in
+ * their order at keep - recent .. keep - 1.  (The softmax does not depend on
+ * the order of the keys that a row sees, and positions are in the keys; new
+ * tokens are appended behind, so that the last ones are always in order.)
+ * Sequences of up to `keep` tokens stay as they are.
+ *   new_lengths [B]            min(lengths[b], keep)
+ *   new_weights [B][Hkv][32 max_pages]  the weights at the tokens' new
+ *                              places, 0 from there on; may be weights itself
+ *   kept [B][Hkv][keep]        (or NULL) the place that the token at each place had; -1 past
+ *                              the new length
+ * All device memory; lengths and page_table [B][max_pages] are read when the
+ * call runs.  new_lengths must not be lengths (ATTN_ERR_SHAPE).  first + recent <=
+ * keep (ATTN_ERR_SHAPE).  Pages that a token moves in or out of belong to one
+ * sequence only: tokens below `first` do not move, so that shared pages at the
+ * front are safe below it.  The pages behind the new length are free
+ * for other use when the call has run.  A page number outside the pool leaves
+ * its tokens' bytes unmoved and records ATTN_ERR_PAGE, as does a length above
+ * 32 max_pages (cut).
+ * `workspace`: attn_cache_evict_workspace_bytes() bytes, 256-byte aligned (may
+ * be NULL when that is 0). */
+size_t attn_cache_evict_workspace_bytes(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep,
+                                        int32_t first, int32_t recent);
+int attn_cache_evict(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep, int32_t first, int32_t recent,
+                     const int32_t* page_table, const int32_t* lengths, const float* weights, int32_t* new_lengths,
+                     float* new_weights, int32_t* kept, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Device status word of the current device: ATTN_OK, or the first failure a
  * kernel recorded (ATTN_ERR_TIMEOUT, ATTN_ERR_RANGE or ATTN_ERR_PAGE; a
  * timeout replaces the others).  Synchronises the device.  Writes the

@@ -1,0 +1,262 @@
+"""GPU tests of attention over a shared prefix and each sequence's own pages of the
+4-bit cache, against a 64-bit softmax over both (bounds: _serving_ref.attend_prefix,
+plus half a bf16 step of O)."""
+import numpy as np
+import pytest
+import torch
+
+import _serving_ref as srv
+from _qk_cache_ref import assert_within, bf16, f64
+
+pytestmark = pytest.mark.gpu
+PAGE = 32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    from exact_scaled_dot_gb300 import build as b
+    b.build()
+    import exact_scaled_dot_gb300 as esd
+    esd.load()
+    assert torch.cuda.is_available(), "a CUDA device is required"
+    esd.attn_clear_status()
+    yield
+    assert esd.attn_get_status() == 0
+
+
+def _dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+
+def _queries(rng, B, Hq, nq, dh, scale=1.0):
+    return bf16(rng.normal(size=(B, Hq, nq, dh)) * scale)
+
+
+def _case(seed, B, Hq, Hkv, nq, dh, dv, prefix, lengths, spread=0.0, more_pages=0):
+    """The cache with the prefix as its first row, Q, and what the library gets."""
+    rng = np.random.default_rng(seed)
+    lengths = [lengths] * B if isinstance(lengths, int) else lengths
+    wide = max(1, max(-(-n // PAGE) for n in [prefix] + lengths)) + more_pages
+    c = srv.Paged(rng, Hkv, dh, dv, [prefix] + lengths, max_pages=wide, spread=spread)
+    q = _queries(rng, B, Hq, nq, dh)
+    own = max(1, max(-(-n // PAGE) for n in lengths)) + more_pages
+    args = dict(prefix_table=_dev(c.table[0]), prefix_length=_dev(np.array([prefix], np.int32)),
+                page_table=_dev(c.table[1:, :own]), lengths=_dev(np.array(lengths, np.int32)))
+    return c, q, args
+
+
+def _check(c, q, O, LSE, nq, dh):
+    O, LSE = f64(O), f64(LSE)
+    for b, n in enumerate(c.lengths[1:]):
+        rO, rL, eO, eL = srv.attend_prefix(q[b], c.K[0], c.V[0], c.K[b + 1], c.V[b + 1], n, dh ** -0.5)
+        assert_within(O[b], rO, eO + 2.0 ** -8 * (np.abs(rO) + eO), "O")
+        empty = rL == -np.inf
+        assert np.array_equal(LSE[b] == -np.inf, empty) and (O[b][empty] == 0).all()
+        assert_within(np.where(empty, 0.0, LSE[b]), np.where(empty, 0.0, rL), eL, "LSE")
+
+
+def _run(c, q, args, dh, dv, **kw):
+    import exact_scaled_dot_gb300 as esd
+    cache = esd.QuantCache(_dev(c.pool), dh, dv)
+    return esd.attn_fwd_prefix_cache(_dev(q).to(torch.bfloat16), cache, **args, **kw)
+
+
+@pytest.mark.parametrize("dh,dv", [(64, 64), (128, 128), (128, 64)])
+@pytest.mark.parametrize("B,Hq,Hkv,nq,prefix,lengths", [
+    (1, 1, 1, 1, 1, 1),                                   # one key on each side
+    (1, 4, 2, 1, 0, 70),                                  # no prefix
+    (2, 4, 2, 1, 40, 0),                                  # no own keys
+    (2, 2, 1, 3, 33, [0, 2]),                             # rows that see the prefix alone
+    (3, 8, 2, 1, 500, [1, 40, 33]),
+    (2, 5, 1, 2, 31, [32, 64]),
+    (2, 6, 3, 5, 64, [5, 129]),
+    (4, 8, 8, 16, 65, [16, 20, 100, 31]),                 # the most rows per head
+    (40, 4, 1, 1, 127, 3),                                # more rows than a tile of 128
+    (30, 16, 2, 3, 300, [3 + 7 * i for i in range(30)]),  # 720 rows of a head
+    (2, 32, 1, 16, 129, [16, 50]),                        # 1024 rows of one head
+])
+def test_against_64_bits(B, Hq, Hkv, nq, prefix, lengths, dh, dv):
+    c, q, args = _case(B * 100 + prefix, B, Hq, Hkv, nq, dh, dv, prefix, lengths)
+    O, LSE = _run(c, q, args, dh, dv)
+    torch.cuda.synchronize()
+    _check(c, q, O, LSE, nq, dh)
+
+
+@pytest.mark.parametrize("prefix", [2047, 2048, 4100])
+def test_long_prefix(prefix):
+    """Many splits of the prefix, long own sequences that several CTAs share, wide tables."""
+    c, q, args = _case(prefix, 3, 8, 2, 2, 128, 128, prefix, [2, 1500, 3000 - 7], more_pages=90)
+    O, LSE = _run(c, q, args, 128, 128)
+    torch.cuda.synchronize()
+    _check(c, q, O, LSE, 2, 128)
+
+
+@pytest.mark.parametrize("B", [2, 64])
+def test_both_empty(B):
+    """Nothing to see at all: 0 and -inf, whatever the pages and the row hold."""
+    c, q, args = _case(5, B, 4, 2, 2, 128, 64, 0, 0)
+    q[0, 0] = np.nan
+    O, LSE = _run(c, q, args, 128, 64)
+    torch.cuda.synchronize()
+    assert (f64(O) == 0).all() and (f64(LSE) == -np.inf).all()
+
+
+@pytest.mark.parametrize("B", [2, 40])
+@pytest.mark.parametrize("spread", [4.0, 12.0])
+def test_values_of_very_different_sizes(B, spread):
+    """Scales of the values many octaves apart from key to key: every row keeps what it weighs."""
+    dh = dv = 128
+    c, q, args = _case(B, B, 8, 2, 1, dh, dv, 300, 33, spread=spread)
+    q *= 4.0
+    O, LSE = _run(c, q, args, dh, dv)
+    torch.cuda.synchronize()
+    O = f64(O)
+    for b in range(B):
+        K, V = np.concatenate([c.K[0], c.K[b + 1]]), np.concatenate([c.V[0], c.V[b + 1]])
+        for r in range(8):
+            s = K[:, r // 4] @ q[b, r, 0] * dh ** -0.5
+            p = np.exp(s - s.max())
+            A = p / p.sum()
+            want = A @ V[:, r // 4]
+            # Per group of 64 dims: what the weights times the group's largest values are off by
+            # together, 2^-11 of each product, 2^-29 of the largest, as the header says, and O's rounding.
+            size = np.repeat(np.abs(V[:, r // 4].reshape(len(V), -1, 64)).max(-1), 64, -1)
+            ds = 132 * 2.0 ** -24 * dh ** -0.5 * (np.abs(K[:, r // 4]) @ np.abs(q[b, r, 0]))
+            rel = 2.0 ** -11 + 2 * (ds + 2.0 ** -20 * (1 + np.abs(s - s.max()) + abs(s.max()) / 4))
+            prod = A[:, None] * size
+            bound = (rel[:, None] * prod).sum(0) + len(V) * 2.0 ** -27 * prod.max(0)
+            bound += 2 * (len(V) / 16 + 8) * 2.0 ** -23 * 2.2 * prod.sum(0)
+            assert_within(O[b, r, 0], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "O")
+
+
+@pytest.mark.parametrize("B", [1, 33])
+def test_rows_that_are_not_finite(B):
+    c, q, args = _case(9, B, 4, 1, 2, 64, 64, 50, 9)
+    q[0, 1, 0, 5] = np.inf
+    q[B - 1, 3, 1, 60] = np.nan
+    O, LSE = _run(c, q, args, 64, 64)
+    torch.cuda.synchronize()
+    bad = np.zeros((B, 4, 2), bool)
+    bad[0, 1, 0] = bad[B - 1, 3, 1] = True
+    assert np.array_equal(np.isnan(f64(LSE)), bad)
+    assert np.array_equal(np.isnan(f64(O)).all(-1), bad) and not np.isnan(f64(O)[~bad]).any()
+
+
+@pytest.mark.parametrize("B", [2, 36])
+@pytest.mark.parametrize("size", [2.0 ** -40, 2.0 ** 30])
+def test_queries_of_any_size(B, size):
+    """Scores that are all alike or far apart; the scale brings large rows back."""
+    c, q, args = _case(11, B, 4, 1, 1, 128, 128, 200, 40)
+    q = bf16(q * size)
+    O, LSE = _run(c, q, args, 128, 128, scale=dh_scale(size))
+    torch.cuda.synchronize()
+    O, LSE = f64(O), f64(LSE)
+    for b, n in enumerate(c.lengths[1:]):
+        rO, rL, eO, eL = srv.attend_prefix(q[b], c.K[0], c.V[0], c.K[b + 1], c.V[b + 1], n, dh_scale(size))
+        assert_within(O[b], rO, eO + 2.0 ** -8 * (np.abs(rO) + eO), "O")
+        assert_within(LSE[b], rL, eL, "LSE")
+
+
+def dh_scale(size):
+    return float(np.float32(128 ** -0.5 * (1.0 / size if size > 1 else 1.0)))
+
+
+def test_same_as_the_decode_over_one_table():
+    """With the prefix's pages in front of each sequence's (a prefix of whole pages), the decode
+    over the cache is the same function."""
+    import exact_scaled_dot_gb300 as esd
+    c, q, args = _case(3, 6, 16, 4, 2, 128, 64, 5 * PAGE, [2, 50, 64, 33, 7, 100])
+    cache = esd.QuantCache(_dev(c.pool), 128, 64)
+    Q = _dev(q).to(torch.bfloat16)
+    O, LSE = esd.attn_fwd_prefix_cache(Q, cache, **args)
+    table = torch.cat([args["prefix_table"][:5].expand(6, -1), args["page_table"]], 1).contiguous()
+    O2, LSE2 = esd.attn_fwd_decode_cache(Q, cache, table, args["lengths"] + 5 * PAGE)
+    torch.cuda.synchronize()
+    assert (LSE - LSE2).abs().max() < 1e-4
+    assert ((O - O2).abs().float() <= 2.0 ** -7 * O2.abs().float() + 2e-3).all()
+
+
+@pytest.mark.parametrize("B", [2, 40])
+def test_indices_out_of_range_are_left_out_and_reported(B):
+    import exact_scaled_dot_gb300 as esd
+    c, q, args = _case(21, B, 4, 2, 1, 128, 128, 4 * PAGE, [70] * B)
+    cache = esd.QuantCache(_dev(c.pool), 128, 128)
+    Q = _dev(q).to(torch.bfloat16)
+    good = dict(args)
+
+    def reported(**kw):
+        out = esd.attn_fwd_prefix_cache(Q, cache, **{**args, **kw})
+        torch.cuda.synchronize()
+        assert esd.attn_get_status() == esd.ATTN_ERR_PAGE
+        esd.attn_clear_status()
+        return out
+
+    # the prefix's second page: its keys are left out
+    t = args["prefix_table"].clone()
+    t[1] = 2 ** 31 - 1
+    O, LSE = reported(prefix_table=t)
+    keep = np.r_[0:PAGE, 2 * PAGE:4 * PAGE]
+    c.K[0], c.V[0], whole = c.K[0][keep], c.V[0][keep], (c.K[0], c.V[0])
+    _check(c, q, O, LSE, 1, 128)
+    c.K[0], c.V[0] = whole
+    # lengths past the tables are cut to them
+    O, LSE = reported(prefix_table=args["prefix_table"][:4].contiguous(),
+                      prefix_length=torch.tensor([1 << 30], dtype=torch.int32, device="cuda"))
+    _check(c, q, O, LSE, 1, 128)
+    O, LSE = reported(page_table=torch.full_like(args["page_table"], -5))
+    c.lengths = [4 * PAGE] + [0] * B
+    _check(c, q, O, LSE, 1, 128)
+    # negative lengths are no keys
+    O, LSE = esd.attn_fwd_prefix_cache(Q, cache, **{**good, "lengths": torch.full_like(args["lengths"], -3)})
+    _check(c, q, O, LSE, 1, 128)
+
+
+@pytest.mark.parametrize("B", [3, 50])
+def test_captured_call_follows_lengths_and_tables(B):
+    import exact_scaled_dot_gb300 as esd
+    c, q, args = _case(31, B, 8, 2, 1, 128, 128, 200, [5 + i for i in range(B)])
+    cache = esd.QuantCache(_dev(c.pool), 128, 128)
+    Q = _dev(q).to(torch.bfloat16)
+    O, LSE = (torch.empty((B, 8, 1, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((B, 8, 1), device="cuda"))
+    ws = torch.empty(esd.attn_fwd_prefix_cache_workspace_bytes(cache, B, 8, 1, len(args["prefix_table"]),
+                                                               args["page_table"].shape[1]),
+                     dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        esd.attn_fwd_prefix_cache(Q, cache, **args, O=O, LSE=LSE, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        esd.attn_fwd_prefix_cache(Q, cache, **args, O=O, LSE=LSE, workspace=ws)
+    O2, LSE2 = torch.empty_like(O), torch.empty_like(LSE)
+    with torch.cuda.graph(other):                    # the same workspace in another graph
+        esd.attn_fwd_prefix_cache(Q, cache, **args, O=O2, LSE=LSE2, workspace=ws)
+    for prefix, less in ((200, 0), (7, 3), (0, 1), (129, 2)):
+        args["prefix_length"].fill_(prefix)
+        lengths = [max(0, 5 + i - less) for i in range(B)]
+        args["lengths"].copy_(torch.tensor(lengths, dtype=torch.int32))
+        ws.fill_(0xFF)                               # what a workspace holds on entry does not matter
+        graph.replay()
+        other.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+        kp, vp = c.K[0], c.V[0]
+        c.K[0], c.V[0], c.lengths = kp[:prefix], vp[:prefix], [prefix] + lengths
+        _check(c, q, O, LSE, 1, 128)
+        c.K[0], c.V[0] = kp, vp
+
+
+@pytest.mark.parametrize("B", [4, 48])
+def test_repeatable_and_on_another_stream(B):
+    import exact_scaled_dot_gb300 as esd
+    c, q, args = _case(41, B, 8, 1, 2, 64, 64, 1000, [2 + 9 * i for i in range(B)])
+    cache = esd.QuantCache(_dev(c.pool), 64, 64)
+    Q = _dev(q).to(torch.bfloat16)
+    O, LSE = esd.attn_fwd_prefix_cache(Q, cache, **args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    O2, LSE2 = esd.attn_fwd_prefix_cache(Q, cache, **args, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+    _check(c, q, O, LSE, 2, 64)

@@ -52,7 +52,8 @@ EXPORTS = ("attn_fwd", "attn_fwd_workspace_bytes", "attn_fwd_varlen_workspace_by
            "attn_proj_bwd_input", "attn_rope", "attn_rope_qk", "attn_bwd_head_split", "attn_bwd_persistent",
            "attn_rope_axes", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes",
            "attn_cache_page_bytes", "attn_cache_append", "attn_cache_read", "attn_fwd_decode_cache",
-           "attn_fwd_decode_cache_workspace_bytes")
+           "attn_fwd_decode_cache_workspace_bytes", "attn_fwd_prefix_cache", "attn_fwd_prefix_cache_workspace_bytes",
+           "attn_cache_weigh", "attn_cache_evict", "attn_cache_evict_workspace_bytes")
 
 
 class AttnError(RuntimeError):

@@ -20,7 +20,7 @@ LIB = PKG / "libesd_attn.so"
 INCLUDE = PKG.parent / "include"
 
 SOURCES = ["attn_fwd.cu", "attn_bwd.cu", "attn_bwd_persist.cu", "attn_decode.cu", "proj_gemm.cu", "rope.cu",
-           "qk_norm.cu", "quant_cache.cu", "decode_cache.cu", "prefix_cache.cu", "cache_weigh.cu", "cache_evict.cu",
+           "qk_norm.cu", "quant_cache.cu", "decode_cache.cu", "prefix_cache.cu", "prefix_tile.cu", "cache_weigh.cu", "cache_evict.cu",
            "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

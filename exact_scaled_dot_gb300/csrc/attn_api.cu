@@ -990,8 +990,11 @@ DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
 // How attn_fwd_prefix_cache divides the work: the sequences' own keys as
 // attn_fwd_decode_cache does, and the prefix among row tiles (of the rows of
 // the whole batch) and ranges of its pages.
+constexpr int kFewPrefixRows = 16;
+constexpr int kMinPrefixTilePages = 4;
 struct PrefixCachePlan {
   DecodeCachePlan own;
+  int row_tiles;               // of prefix_tile.cu, or 0
   int tile_rows, chunks, ranges;
   size_t off_own, off_oall, off_lall, off_opart, off_lpart, off_used, bytes;
 };
@@ -1000,11 +1003,14 @@ PrefixCachePlan prefix_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
   PrefixCachePlan d;
   d.own = decode_cache_plan(c, B, Hq, n_q, max_pages);
   const int64_t R = static_cast<int64_t>(B) * (Hq / c->Hkv) * n_q;
-  d.tile_rows = R > 8 ? 16 : 8;
+  d.row_tiles = R > kFewPrefixRows ? (R > 128 ? 2 : 1) : 0;
+  d.tile_rows = d.row_tiles > 0 ? 128 * d.row_tiles : R > 8 ? 16 : 8;
   d.chunks = static_cast<int>((R + d.tile_rows - 1) / d.tile_rows);
   const int64_t tiles = static_cast<int64_t>(c->Hkv) * d.chunks;
-  const int64_t resident = 152 * (d.tile_rows == 8 ? kDecodeCacheResident8 : kDecodeCacheResident16);
-  const int64_t most = (prefix_pages + kMinRangePages - 1) / kMinRangePages;
+  const int64_t resident =
+      152 * (d.row_tiles > 0 ? 1 : d.tile_rows == 8 ? kDecodeCacheResident8 : kDecodeCacheResident16);
+  const int64_t least = d.row_tiles > 0 ? kMinPrefixTilePages : kMinRangePages;
+  const int64_t most = (prefix_pages + least - 1) / least;
   d.ranges = static_cast<int>(std::max<int64_t>(1, std::min(resident / tiles, most)));
   const size_t rows = static_cast<size_t>(B) * Hq * n_q, parts = static_cast<size_t>(tiles) * d.ranges * d.tile_rows;
   d.off_own = 0;
@@ -2039,13 +2045,32 @@ int attn_fwd_prefix_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
   prefix.chunks = plan.chunks;
   prefix.ranges = plan.ranges;
   prefix.whole_seqs = prefix.wide = 0;
+  PrefixTileParams tile{};
+  tile.B = B;
+  tile.Hkv = cache->Hkv;
+  tile.per = m.own.group * n_q;
+  tile.prefix_pages = prefix_pages;
+  tile.pages = cache->pages;
+  tile.pool = prefix.pool;
+  tile.table = prefix_table;
+  tile.length = prefix_length;
+  tile.scale_log2 = prefix.scale_log2;
+  tile.wait_limit_ns = prefix.wait_limit_ns;
+  tile.Q = Q;
+  tile.Opart = prefix.Opart;
+  tile.Lpart = prefix.Lpart;
+  tile.used = prefix.first_page;
+  tile.row_tiles = plan.row_tiles;
+  tile.row_blocks = plan.chunks;
+  tile.splits = plan.ranges;
+  tile.status = status;
   m.Opart = prefix.Opart;
   m.Lpart = prefix.Lpart;
   m.used = prefix.first_page;
   m.tile_rows = plan.tile_rows;
   m.chunks = plan.chunks;
   m.splits = plan.ranges;
-  const cudaError_t e = launch_prefix_cache(cache->d_h, cache->d_v, prefix, m, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_prefix_cache(cache->d_h, cache->d_v, prefix, tile, m, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

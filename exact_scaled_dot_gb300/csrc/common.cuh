@@ -384,6 +384,25 @@ struct DecCacheParams {
   float* Lall;                 // fp32 [B][Hq][n_q]
 };
 
+// The prefix for many rows (prefix_tile.cu): row r of KV head h is row r % per of
+// sequence r / per.
+struct PrefixTileParams {
+  int32_t B, Hkv, per, prefix_pages;
+  int64_t pages;
+  const uint8_t* pool;
+  const int32_t* table;        // [prefix_pages]
+  const int32_t* length;       // [1]
+  float scale_log2;            // scale * log2(e)
+  uint64_t wait_limit_ns;
+  const void* Q;               // bf16 [B][Hq][n_q][d_h]
+  float* Opart;                // fp32 [Hkv row_blocks][splits][128 row_tiles][d_v]
+  float* Lpart;                // fp32 [Hkv row_blocks][splits][128 row_tiles]
+  int32_t* used;               // [1] splits that have keys
+  int32_t row_tiles;           // 128-row tiles of a CTA: 1 or 2
+  int32_t row_blocks, splits;
+  unsigned int* status;
+};
+
 // Merge of attn_fwd_prefix_cache: for each query row the parts of the prefix
 // and those of its own sequence (as `own` describes them).
 struct PrefixMergeParams {
@@ -467,8 +486,10 @@ cudaError_t launch_cache_append(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_decode_cache(int dh, int dv, const DecCacheParams& p, cudaStream_t stream);
 // The prefix (as one sequence), then the sequences' own keys, then their merge.
-cudaError_t launch_prefix_cache(int dh, int dv, const DecCacheParams& prefix, const PrefixMergeParams& merge,
-                                cudaStream_t stream);
+// (tile.row_tiles > 0: by prefix_tile.cu.)
+cudaError_t launch_prefix_cache(int dh, int dv, const DecCacheParams& prefix, const PrefixTileParams& tile,
+                                const PrefixMergeParams& merge, cudaStream_t stream);
+cudaError_t launch_prefix_tile(int dh, int dv, const PrefixTileParams& p, cudaStream_t stream);
 cudaError_t launch_cache_weigh(int dh, const CacheWeighParams& p, int dv, cudaStream_t stream);
 cudaError_t launch_cache_evict(const CacheEvictParams& p, cudaStream_t stream);
 // Zero n floats (n a multiple of 4, 16-byte aligned).

@@ -126,8 +126,10 @@ cudaError_t launch_own(const DecCacheParams& p, cudaStream_t stream) {
 }
 
 template <int DH, int DV>
-cudaError_t launch_all(const DecCacheParams& prefix, const PrefixMergeParams& m, cudaStream_t stream) {
-  cudaError_t e = prefix.tile_rows == 8 ? launch_part<kShared, DH, DV, 1, kDecodeCacheWarps, false>(prefix, stream)
+cudaError_t launch_all(const DecCacheParams& prefix, const PrefixTileParams& tile, const PrefixMergeParams& m,
+                       cudaStream_t stream) {
+  cudaError_t e = tile.row_tiles > 0 ? launch_prefix_tile(DH, DV, tile, stream)
+                  : prefix.tile_rows == 8 ? launch_part<kShared, DH, DV, 1, kDecodeCacheWarps, false>(prefix, stream)
                                         : launch_part<kShared, DH, DV, 2, kDecodeCacheWarps, false>(prefix, stream);
   if (e != cudaSuccess) return e;
   e = launch_own<DH, DV>(m.own, stream);
@@ -151,11 +153,11 @@ cudaError_t launch_all(const DecCacheParams& prefix, const PrefixMergeParams& m,
 
 }  // namespace
 
-cudaError_t launch_prefix_cache(int dh, int dv, const DecCacheParams& prefix, const PrefixMergeParams& merge,
-                                cudaStream_t stream) {
-  if (dh == 128 && dv == 128) return launch_all<128, 128>(prefix, merge, stream);
-  if (dh == 64 && dv == 64) return launch_all<64, 64>(prefix, merge, stream);
-  if (dh == 128 && dv == 64) return launch_all<128, 64>(prefix, merge, stream);
+cudaError_t launch_prefix_cache(int dh, int dv, const DecCacheParams& prefix, const PrefixTileParams& tile,
+                                const PrefixMergeParams& merge, cudaStream_t stream) {
+  if (dh == 128 && dv == 128) return launch_all<128, 128>(prefix, tile, merge, stream);
+  if (dh == 64 && dv == 64) return launch_all<64, 64>(prefix, tile, merge, stream);
+  if (dh == 128 && dv == 64) return launch_all<128, 64>(prefix, tile, merge, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -16,18 +16,18 @@
 namespace esd {
 namespace {
 
-// LSE and O of each query row from its parts.  ROWS query rows per block, each
-// shared by kMergeWarps / ROWS warps, which take every so many parts.
+// LSE and O of each query row from its parts: a warp per row, a lane per part for
+// the weights, then DV / 32 dims a lane, eight parts in flight.  Launched while the
+// kernel before drains.
 constexpr int kMergeWarps = 4;
-template <int DV, int ROWS>
+template <int DV>
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __grid_constant__ PrefixMergeParams m) {
-  constexpr int kPer = DV / 32, kShare = kMergeWarps / ROWS;
+  constexpr int kPer = DV / 32, kAhead = 8;
   const DecCacheParams& p = m.own;
   const int R = p.group * p.n_q;
-  const uint32_t lane = lane_id(), warp = warp_id();
-  const int r = static_cast<int>(blockIdx.x * ROWS + warp / kShare);    // (b, KV head, row)
-  const int who = static_cast<int>(warp) % kShare;
-  if (r >= p.B * p.Hkv * R) return;          // (ROWS = 1: never)
+  const uint32_t lane = lane_id();
+  const int r = static_cast<int>(blockIdx.x * kMergeWarps + warp_id());    // (b, KV head, row)
+  if (r >= p.B * p.Hkv * R) return;
   const int bh = r / R, row = r - bh * R;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   // The row in the prefix's first part, and in its own sequence's.
@@ -50,57 +50,64 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __
     whole = own == 1;
   }
   const int n = used + own;
-  // Row of part i among Opart and Lpart of the prefix or of the sequence, or Oall and Lall.
-  auto part_row = [&](int i) -> int64_t {
-    if (i < used) return pre + static_cast<int64_t>(i) * m.tile_rows;
-    const int k = i0 + i - used;
+  const float* l_own = whole ? p.Lall : p.Lpart;
+  const float* o_own = (whole ? p.Oall : p.Opart) + lane * kPer;
+  const float* o_pre = m.Opart + lane * kPer;
+  // Row of part i of the prefix, or of the sequence.
+  auto own_row = [&](int i) -> int64_t {
+    const int k = i0 + i;
     return whole ? r : base_row + (2 * k + (seq0 > k * per ? 1 : 0)) * p.tile_rows;
   };
-  auto lse_of = [&](int i) { return (i < used ? m.Lpart : whole ? p.Lall : p.Lpart)[part_row(i)]; };
-  float M = -INFINITY;
-  for (int i = static_cast<int>(lane); i < n; i += 32) M = fmaxf(M, lse_of(i));
+  auto lse_of = [&](int i) {
+    return i >= n ? -INFINITY : i < used ? m.Lpart[pre + static_cast<int64_t>(i) * m.tile_rows] : l_own[own_row(i - used)];
+  };
+  float M = -INFINITY, first = lse_of(static_cast<int>(lane));     // (parts past the 32nd are read twice)
+  for (int i = static_cast<int>(lane); i < n; i += 32) M = fmaxf(M, i < 32 ? first : lse_of(i));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   const float base = M == -INFINITY ? 0.f : M;
   float acc[kPer], sum = 0.f;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-#pragma unroll 4
-  for (int i = who; i < n; i += kShare) {
-    const float w = fast_exp2((lse_of(i) - base) * kLog2e);
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const float w = fast_exp2(((j0 == 0 ? first : lse_of(j0 + static_cast<int>(lane))) - base) * kLog2e);   // (0: none)
     sum += w;
-    const float* part = i < used ? m.Opart : whole ? p.Oall : p.Opart;
-    const float2* src = reinterpret_cast<const float2*>(part + part_row(i) * DV + lane * kPer);
+    const int some = n - j0 < 32 ? n - j0 : 32;
+    for (int i0_ = 0; i0_ < some; i0_ += kAhead) {
+      float v[kAhead][kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; k += 2) {
-      const float2 v = src[k / 2];
-      acc[k] = fmaf(w, v.x, acc[k]);
-      acc[k + 1] = fmaf(w, v.y, acc[k + 1]);
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = j0 + i0_ + u;
+        if (i < n) {
+          const float* src =
+              i < used ? o_pre + (pre + static_cast<int64_t>(i) * m.tile_rows) * DV : o_own + own_row(i - used) * DV;
+          if constexpr (kPer == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[u][0] = x.x, v[u][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, (i0_ + u) & 31);
+        if (j0 + i0_ + u < n) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) acc[k] = fmaf(wu, v[u][k], acc[k]);
+        }
+      }
     }
   }
-  if constexpr (kShare > 1) {
-    __shared__ float acc_s[kShare][DV], sum_s[kShare];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc_s[who][k * 32 + lane] = acc[k];
-    if (lane == 0) sum_s[who] = sum;
-    __syncthreads();
-    if (who > 0) return;
-#pragma unroll
-    for (int w = 1; w < kShare; ++w) {
-      sum += sum_s[w];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] += acc_s[w][k * 32 + lane];
-    }
-  }
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.O) + static_cast<int64_t>(r) * DV + lane * kPer);
 #pragma unroll
   for (int k = 0; k < kPer; k += 2) dst[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
   if (lane == 0) p.LSE[r] = sum == 0.f ? -INFINITY : M + fast_log2(sum) * kLn2;
 }
-
-// Up to this many query rows, the merge gives each a block of its own.
-constexpr int kMergeBlockRows = 8 * 152;
 
 template <CacheKind KIND, int DH, int DV, int NT, int WARPS, bool WHOLE>
 cudaError_t launch_part(const DecCacheParams& p, cudaStream_t stream) {
@@ -143,12 +150,8 @@ cudaError_t launch_all(const DecCacheParams& prefix, const PrefixTileParams& til
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   const int rows = m.own.B * m.own.Hkv * m.own.group * m.own.n_q;
-  if (rows <= kMergeBlockRows) {
-    cfg.gridDim = dim3(static_cast<unsigned>(rows));
-    return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<DV, 1>, m);
-  }
   cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
-  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<DV, kMergeWarps>, m);
+  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<DV>, m);
 }
 
 }  // namespace

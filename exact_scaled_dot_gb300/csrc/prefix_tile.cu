@@ -6,33 +6,45 @@
 // 2 rows (d_h + d_v) operations per key and head for 0.5625 (d_h + d_v) bytes:
 // from a few hundred rows on it is bound by the tensor core, not by memory.  A
 // CTA takes a range of the prefix for one KV head and up to 256 rows, and turns
-// every tile of 64 keys (two pages) into fp16 operands once for all of them:
+// every tile of 64 keys (two pages) into fp16 operands once for all of them.
 //
-//   S_g = Q_g (c - z)_g^T   for each group g of 64 dims, exact products (c - z
-//     is a small integer, Q a bf16 number times a power of two), fp32 sums
-//   s_ij = f_i sum_g sk_gj S_g,ij  in fp32: the keys' scales stay out of the
-//     operands, where their product with c - z would not fit fp16
-//   O_g += W_g (c - z)_g,  W_g,ij = fp16(P_ij sv_gj / top_gi)
+// Scores.  With q = Q's row times a power of two and k = s (c - z) per group of
+// 64 dims, q . k = sum_g [ q_g . s_g (c - 8)_g + (sum q_g) s_g (8 - z_g) ].  s has
+// 8 significant bits and |c - 8| <= 8, so that s (c - 8) is exact in fp16 (times a
+// power of two 2^e of the tile; s (c - z) would need a bit more).  The second
+// term is one more step of the product's inner dimension, with sum q_g as three
+// fp16 numbers (33 bits).  So the scores are exact products summed in fp32, and
+// nothing is left to multiply per key.
 //
-// with the weights' powers of two `top` per row and group as in the attention
-// of a few rows over this cache (decode_cache_kernel.cuh, where they are
-// explained); the zero points are in the operands here, so that O's sums need
-// no correction.
+// Values.  O += P V with V = fp16(s (c - z) 2^E_g) and P = fp16(2^10 exp(..)): two
+// roundings of 2^-12.  One E_g per CTA serves while V's scales of a group lie
+// within four octaves.  (Scales as factors of the weights or scores cost a
+// shared-memory word per row and key each: 2.5 times the time, measured.)
 //
-// CTA: 512 threads, one per SM.  Warp 0 brings pages into a ring (bulk copies),
-// warps 12-15 turn them into K-major and MN-major operand tiles (128-byte
-// swizzle), warp 1 issues the products, warps 4-7 and 8-11 are two softmax
-// streams (thread = row).  With two row tiles (NT = 2) stream t has tile t and
-// both use every key tile; with one (NT = 1) the streams take the key tiles in
-// turn, each with accumulators of its own, merged at the end.  While one
-// stream's softmax runs, the tensor core works for the other.
+// The other way.  Where a tile's scales are further apart (K's: over 12 octaves),
+// a CTA goes on with operands c - z alone: S_g = Q_g (c - z)_g^T, s_ij = f_i sum_g
+// sk_gj S_g,ij in fp32, O_g += W_g (c - z)_g with W_g,ij = fp16(P_ij sv_gj /
+// top_gi), and the powers of two `top` per row and group of the attention of a
+// few rows over this cache (decode_cache_kernel.cuh, where they are explained).
 //
-// Tensor memory, stream t: S_0, S_1 in columns [128 t, 128 t + 128), the fp16
-// weights W_0, W_1 over its first 64 once the scores are read; O in
-// [256 + 128 t, + d_v).
+// CTA: 640 threads, one per SM.  Warp 0 brings pages into a ring (bulk copies),
+// warp 2 looks at a tile's scales, warps 12-19 turn it into K-major and MN-major
+// operand tiles (128-byte swizzle), warps 4-7 and 8-11 are two softmax streams
+// (thread = row), for which warps 1 and 3 issue the products.  With two row tiles
+// (NT = 2) stream t has tile t and both use every key tile; with one (NT = 1) the
+// streams take the key tiles in turn, each with accumulators of its own, merged
+// at the end.  The softmax takes its scores into registers at once, so that the
+// next tile's are made while it works.
 //
-// A 32-bit word of codes becomes four pairs of operands by one AND-OR and one
-// fp16 operation each (0x6400 | c is 1024 + c); the pairs are the dims (k, k + 4)
+// Tensor memory, stream t, from column 128 t: the scores in 64; Q's first 64 dims
+// in the next 32 (through shared memory Q is read again for every 64 keys) and
+// the weights in 32 more, or, with O 64 wide, Q's second half there and the
+// weights behind O.  O in [256 + 128 t, + d_v).  In the other way S_0, S_1 in the
+// 128 columns, then the scores over S_0 and W_0, W_1 over S_1, one tile after the
+// other.
+//
+// A 32-bit word of codes becomes four pairs of operands by one AND-OR and two
+// fp16 operations each (0x6400 | c is 1024 + c); the pairs are the dims (k, k + 4)
 // of eight, an order that Q's rows are given too and that O's columns lose again
 // when they are written.
 #include <cstdint>
@@ -48,65 +60,150 @@ constexpr float kNoKey = -1e30f;    // the reference (exp2 domain) of a row that
 constexpr int kLazy = 5, kSlack = 4, kTopBits = 6;      // as in decode_cache_kernel.cuh
 static_assert(kLazy + kSlack + kTopBits <= 15, "weights are fp16");
 constexpr int kLeastTop = -118, kMostTop = 126;
+// Scales that the folded operands take: V's of a group between 2^(X - 2) and
+// 2^(X + 2), X the exponent of the CTA's first; K's of a tile 2^12 apart; neither
+// beyond 2^+-100.
+constexpr int kBelow = 2, kAbove = 1, kSpreadK = 12, kMostExp = 100;
+constexpr int kFastBits = 10;       // P 2^10 is at most 2^15
+constexpr int kScaleK = 4;          // K's largest scale becomes 2^4 to 2^5
+constexpr int kSumShift = 6;        // sum q_g 2^-6 and s (8 - z) 2^6 are fp16
 constexpr int kKeys = 64;           // keys of a tile: two pages
 constexpr int kTilePages = kKeys / kPageTokens;
+
+// What the softmax and the products need to know of a tile.
+struct __align__(16) TileHead {
+  uint32_t mask[2];       // the keys there are, of each page
+  float unscale;          // 2^-e of K's operands
+  int32_t fast;           // 1: scales in the operands
+  float up[2];            // fast: the weights' and V's power of two of each group
+  float pad[2];
+  float most[2][2];       // else: the largest of V's scales, [group][page]
+};
 
 template <int DH, int DV, int NT>
 struct TileCfg {
   static constexpr int GK = DH / kQuantGroup, GV = DV / kQuantGroup;
   static constexpr int kBlock = page_head_bytes(DH, DV);
-  static constexpr int kRawStages = 6, kStages = NT == 2 ? 3 : 4;
-  static constexpr int kQTile = 128 * DH * 2;
-  static constexpr int kK16 = kKeys * DH * 2, kV16 = kKeys * DV * 2;
-  static constexpr int kScales = (GK + GV) * kKeys * 4;      // floats
+  static constexpr int kRawStages = 4, kStages = NT == 2 ? 3 : 4;
+  static constexpr int kQTile = 128 * DH * 2, kQx = 128 * 32;
+  static constexpr int kK16 = kKeys * DH * 2, kV16 = kKeys * DV * 2, kKx = kKeys * 32;
+  static constexpr int kOp = kK16 + kV16 + kKx;
+  static constexpr int kScales = (GK + GV) * kKeys * 4;
+  static constexpr int kPrep = kScales + kKeys * 4;          // and K's sums' factors
+  // Tensor memory of a stream: groups of Q there are, and where the weights are.
+  static constexpr int kTmemQ = DV == 64 ? GK : 1;
+  static constexpr uint32_t kColQ = 64, kColW = DV == 64 ? 256 + 64 : 96;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffOp = kOffQ + NT * kQTile;         // [stage] K16, V16
-  static constexpr int kOffRaw = kOffOp + kStages * (kK16 + kV16);
-  static constexpr int kOffScale = kOffRaw + kRawStages * kTilePages * kBlock;   // [stage] K's, V's
-  static constexpr int kOffMax = kOffScale + kStages * kScales;                  // [stage][GV][2]
-  static constexpr int kOffRawMask = kOffMax + kStages * 16;                     // [raw stage][2]
-  static constexpr int kOffMask = kOffRawMask + kRawStages * 8;                  // [stage][2]
-  static constexpr int kOffState = kOffMask + kStages * 8;   // [128] (l, shift) of stream 1 (NT = 1)
-  static constexpr int kOffBar = kOffState + 128 * 8;
+  static constexpr int kOffOp = kOffQ + NT * kQTile;         // [stage] K16, V16, K's sums
+  static constexpr int kOffQx = kOffOp + kStages * kOp;      // [row tile]
+  static constexpr int kOffRaw = kOffQx + NT * kQx;
+  static constexpr int kOffPrep = kOffRaw + kRawStages * kTilePages * kBlock;    // [raw stage] (scale, z) or scales
+  static constexpr int kOffRawHead = kOffPrep + kRawStages * kPrep;            // [raw stage]
+  static constexpr int kOffScale = kOffRawHead + kRawStages * static_cast<int>(sizeof(TileHead));   // [stage]
+  static constexpr int kOffHead = kOffScale + kStages * kScales;                 // [stage]
+  static constexpr int kOffRawMask = kOffHead + kStages * static_cast<int>(sizeof(TileHead));       // [raw stage][2]
+  // Of each row, while Q is put down; (l, shift) of stream 1 (NT = 1).
+  static constexpr int kOffState = (kOffRawMask + kRawStages * 8 + 15) / 16 * 16;
+  static constexpr int kOffBar = kOffState + NT * 128 * 16;
   static constexpr int kBarRawFull = 0;
   static constexpr int kBarRawEmpty = kBarRawFull + kRawStages;
-  static constexpr int kBarFull = kBarRawEmpty + kRawStages;
+  static constexpr int kBarPrep = kBarRawEmpty + kRawStages;
+  static constexpr int kBarFull = kBarPrep + kRawStages;
   static constexpr int kBarEmpty = kBarFull + kStages;
   static constexpr int kBarS = kBarEmpty + kStages;          // [2]
-  static constexpr int kBarP = kBarS + 2;                    // [2]
+  static constexpr int kBarSFree = kBarS + 2;                // [2]
+  static constexpr int kBarP = kBarSFree + 2;                // [2]
   static constexpr int kBarPV = kBarP + 2;                   // [2]
   static constexpr int kBarQ = kBarPV + 2;
-  static constexpr int kBarDrain = kBarQ + 1;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarDrain = kBarQ + 1;                // [2]
+  static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kSmemBytes = kOffAbort + 4 + 1024;    // slack for 1024-byte alignment
-  static constexpr int kThreads = 512;
-  // Registers: 128 a thread at launch, moved between the four warpgroups.
-  static constexpr uint32_t kRegsLaunch = 128, kRegsControl = 64, kRegsSoftmax = 176, kRegsOperands = 96;
-  static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsOperands <= 4 * kRegsLaunch, "the block's registers");
+  static constexpr int kThreads = 640, kOpThreads = 256;
+  // Registers: 96 a thread at launch, moved between the five warpgroups.
+  static constexpr uint32_t kRegsLaunch = 96, kRegsControl = 64, kRegsSoftmax = 136, kRegsOperands = 72;
+  static_assert(kRegsControl + 2 * kRegsSoftmax + 2 * kRegsOperands <= 5 * kRegsLaunch, "the block's registers");
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(kBlock % 16 == 0 && kOffRaw % 16 == 0 && kOffScale % 16 == 0 && kOffBar % 8 == 0, "alignment");
-  static_assert(NT == 2 || 128 * DV * 4 <= kStages * (kK16 + kV16), "stream 1's sums over the operand tiles");
+  static_assert(kOp % 1024 == 0 && kOffOp % 1024 == 0, "swizzled tiles");
+  static_assert(NT == 2 || 128 * DV * 4 <= kStages * kOp, "stream 1's sums over the operand tiles");
 };
 
-// The pairs (k, k + 4) of eight codes less their zero point, as fp16.
-__device__ __forceinline__ uint4 operand8(uint32_t codes, uint32_t word) {
-  const uint32_t z = __byte_perm(word, 0x64646464u, 0x4040);            // 1024 + z, twice
-  const uint32_t z16 = ((z & 0x00FF00FFu) << 4) + 0xD400D400u;          // -(64 + z)
-  auto low = [&](uint32_t x) {                                          // 1024 + c less 1024 + z
-    const uint32_t v = (x & 0x000F000Fu) | 0x64006400u;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&z));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hsub2_bits(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The pairs (k, k + 4) of eight codes less a number, as fp16: from 1024 + it (both
+// halves) and -(64 + it).
+__device__ __forceinline__ uint4 operand8(uint32_t codes, uint32_t z, uint32_t z16) {
+  auto low = [&](uint32_t x) { return hsub2_bits((x & 0x000F000Fu) | 0x64006400u, z); };
   auto high = [&](uint32_t x) {                                         // (1024 + 16 c) / 16 - (64 + z)
     return hfma2_bits((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, z16);
   };
   return make_uint4(low(codes), high(codes), low(codes >> 8), high(codes >> 8));
 }
+// ... less the zero point in the lowest byte of `word`.
+__device__ __forceinline__ uint4 operand8z(uint32_t codes, uint32_t word) {
+  const uint32_t z = __byte_perm(word, 0x64646464u, 0x4040);            // 1024 + z, twice
+  return operand8(codes, z, ((z & 0x00FF00FFu) << 4) + 0xD400D400u);
+}
+__device__ __forceinline__ uint4 times(uint4 x, uint32_t s) {
+  return make_uint4(hmul2_bits(x.x, s), hmul2_bits(x.y, s), hmul2_bits(x.z, s), hmul2_bits(x.w, s));
+}
+
+// K-major tile without a swizzle: 8 x 8 matrices of 128 bytes, the two of a
+// 16-element row next to each other.
+__device__ __forceinline__ SmemDesc plain_desc(uint32_t saddr) {
+  SmemDesc d = sw128_desc_words(saddr, 128, 256);
+  d.hi &= ~(7u << 29);
+  return d;
+}
+
+// Four products of 16 of the inner dimension, A in tensor memory 8 columns and B
+// kStep bytes apart; `accumulate`: the first adds to D.  One election, and the
+// operands' places by constants: the issue of a product of its own costs 70
+// cycles, more than the tensor core needs for 64 columns.  Called by whole warps.
+template <int kStep>
+__device__ __forceinline__ void umma_ts_four(uint32_t d, uint32_t a, SmemDesc b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 d0, d1, d2, d3;\n\t.reg .b32 r, b1, b2, b3, a1, a2, a3;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "add.u32 b1, %2, %6;\n\tadd.u32 b2, %2, 2 * %6;\n\tadd.u32 b3, %2, 3 * %6;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "mov.b64 d0, {%2, %3};\n\tmov.b64 d1, {b1, %3};\n\tmov.b64 d2, {b2, %3};\n\tmov.b64 d3, {b3, %3};\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], d0, %4, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], d1, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], d2, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], d3, %4, 1;\n\t}\n"
+      :: "r"(d), "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "n"(kStep >> 4) : "memory");
+}
+
+// The same with A in shared memory, 32 bytes apart like B.
+__device__ __forceinline__ void umma_ss_four(uint32_t d, SmemDesc a, SmemDesc b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 d0, d1, d2, d3, c0, c1, c2, c3;\n\t.reg .b32 r, b1, b2, b3, a1, a2, a3;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u32 b1, %3, 2;\n\tadd.u32 b2, %3, 4;\n\tadd.u32 b3, %3, 6;\n\t"
+      "add.u32 a1, %1, 2;\n\tadd.u32 a2, %1, 4;\n\tadd.u32 a3, %1, 6;\n\t"
+      "mov.b64 d0, {%3, %4};\n\tmov.b64 d1, {b1, %4};\n\tmov.b64 d2, {b2, %4};\n\tmov.b64 d3, {b3, %4};\n\t"
+      "mov.b64 c0, {%1, %2};\n\tmov.b64 c1, {a1, %2};\n\tmov.b64 c2, {a2, %2};\n\tmov.b64 c3, {a3, %2};\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c0, d0, %5, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c1, d1, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c2, d2, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], c3, d3, %5, 1;\n\t}\n"
+      :: "r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate) : "memory");
+}
 
 template <int DH, int DV, int NT>
-__global__ void __launch_bounds__(512, 1) prefix_tile_kernel(const __grid_constant__ PrefixTileParams p) {
+__global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_constant__ PrefixTileParams p) {
   using C = TileCfg<DH, DV, NT>;
   constexpr int GK = C::GK, GV = C::GV;
   extern __shared__ uint8_t smem_raw[];
@@ -137,19 +234,21 @@ __global__ void __launch_bounds__(512, 1) prefix_tile_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kRawStages; ++s) {
       mbar_init(bar(C::kBarRawFull + s), 1);
-      mbar_init(bar(C::kBarRawEmpty + s), 128);
+      mbar_init(bar(C::kBarRawEmpty + s), C::kOpThreads);
+      mbar_init(bar(C::kBarPrep + s), 1);
     }
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bar(C::kBarFull + s), 128);
-      mbar_init(bar(C::kBarEmpty + s), 1);
+      mbar_init(bar(C::kBarFull + s), C::kOpThreads);
+      mbar_init(bar(C::kBarEmpty + s), NT);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(C::kBarS + t), 1);
       mbar_init(bar(C::kBarP + t), 128);
+      mbar_init(bar(C::kBarSFree + t), 128);
       mbar_init(bar(C::kBarPV + t), 1);
+      mbar_init(bar(C::kBarDrain + t), 1);
     }
-    mbar_init(bar(C::kBarQ), 128 * NT);
-    mbar_init(bar(C::kBarDrain), 1);
+    mbar_init(bar(C::kBarQ), 256);
     fence_mbar_init();
     *abort_flag = status_blocks(p.status) ? 2 : 0;
   }
@@ -211,113 +310,236 @@ __global__ void __launch_bounds__(512, 1) prefix_tile_kernel(const __grid_consta
             mbar_wait(bar(C::kBarRawFull + j % C::kRawStages), phase(j, C::kRawStages), &no_abort, limit);
         }
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
       // ================= products =================
-      if (__all_sync(0xffffffffu, *abort_flag == 0)) {
+      const int t = warp == 1 ? 0 : 1, count = count_of(t);
+      if (__all_sync(0xffffffffu, *abort_flag == 0) && count > 0) {
         constexpr uint32_t kIdQK = idesc_f16_f32(128, kKeys, false, false);
-        constexpr uint32_t kIdPV = idesc_f16_f32(128, 64, false, true);
-        const SmemDesc dq0 = sw128_desc_words(sbase + C::kOffQ, 16, 1024);
+        constexpr uint32_t kIdPV = idesc_f16_f32(128, DV, false, true), kIdPVg = idesc_f16_f32(128, 64, false, true);
+        constexpr int kStep = NT == 2 ? 1 : 2;
+        const SmemDesc dq = sw128_desc_words(sbase + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile, 16, 1024);
+        const SmemDesc dqx = plain_desc(sbase + C::kOffQx + (NT == 2 ? t : 0) * C::kQx);
         const SmemDesc dk0 = sw128_desc_words(sbase + C::kOffOp, 16, 1024);
-        const SmemDesc dv0 = sw128_desc_words(sbase + C::kOffOp + C::kK16, 16, 1024);
-        auto scores = [&](int t, int k) {         // S_g of stream t's k-th tile
-          const SmemDesc dk = desc_step(dk0, tile_of(t, k) % C::kStages * (C::kK16 + C::kV16));
-          const SmemDesc dq = desc_step(dq0, (NT == 2 ? t : 0) * C::kQTile);
+        const SmemDesc dv0 = sw128_desc_words(sbase + C::kOffOp + C::kK16, kKeys * 128, 1024);
+        const SmemDesc dx0 = plain_desc(sbase + C::kOffOp + C::kK16 + C::kV16);
+        const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t;
+        auto fast_tile = [&](int st) {
+          return __shfl_sync(0xffffffffu, reinterpret_cast<const TileHead*>(smem + C::kOffHead)[st].fast, 0) != 0;
+        };
+        auto scores = [&](int st, bool fast) {     // of the tile in stage st
+          const SmemDesc dk = desc_step(dk0, st * C::kOp);
+          if (fast) {
 #pragma unroll
-          for (int g = 0; g < GK; ++g)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ss_we(tmem + 128 * t + 64 * g, desc_step(dq, g * 128 * 128 + kk * 32),
-                         desc_step(dk, g * kKeys * 128 + kk * 32), kIdQK, kk > 0 ? 1u : 0u);
+            for (int g = 0; g < GK; ++g) {
+              const SmemDesc dkg = desc_step(dk, g * kKeys * 128);
+              if (g < C::kTmemQ) umma_ts_four<32>(tS, tS + C::kColQ + 32 * g, dkg, kIdQK, g > 0 ? 1u : 0u);
+              else umma_ss_four(tS, desc_step(dq, g * 128 * 128), dkg, kIdQK, 1u);
+            }
+            umma_ss_we(tS, dqx, desc_step(dx0, st * C::kOp), kIdQK, 1u);
+          } else {
+#pragma unroll 1
+            for (int g = 0; g < GK; ++g)
+              umma_ss_four(tS + 64 * g, desc_step(dq, g * 128 * 128), desc_step(dk, g * kKeys * 128), kIdQK, 0u);
+          }
           umma_commit_we(bar(C::kBarS + t));
         };
-        bool ok = wait_all(C::kBarQ, 0);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (count_of(t) == 0) continue;
-          ok = wait_all(C::kBarFull + tile_of(t, 0) % C::kStages, phase(tile_of(t, 0), C::kStages));
-          if (!ok) break;
+        // Stage and phase of the tile at hand and of the next.
+        int st = NT == 2 ? 0 : t;
+        uint32_t ph = 0;
+        bool ok = wait_all(C::kBarQ, 0) && wait_all(C::kBarFull + st, ph), fast = true;
+        if (ok) {
           tc_fence_after_sync();
-          scores(t, 0);
+          fast = fast_tile(st);
+          scores(st, fast);
         }
-        for (int k = 0; k < count_of(0) && ok; ++k) {
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (k >= count_of(t)) continue;
-            ok = wait_all(C::kBarP + t, static_cast<uint32_t>(k & 1));
+        for (int k = 0; k < count && ok; ++k) {
+          int next = st + kStep;
+          uint32_t next_ph = ph;
+          if (next >= C::kStages) next -= C::kStages, next_ph ^= 1u;
+          bool next_fast = false;
+          if (k + 1 < count) {
+            ok = wait_all(C::kBarFull + next, next_ph);
             if (!ok) break;
-            tc_fence_after_sync();
-            const int st = tile_of(t, k) % C::kStages;
-            const SmemDesc dv = desc_step(dv0, st * (C::kK16 + C::kV16));
-#pragma unroll
-            for (int g = 0; g < GV; ++g)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_ts_we(tmem + 256 + 128 * t + 64 * g, tmem + 128 * t + 32 * g + kk * 8,
-                           desc_step(dv, g * kKeys * 128 + kk * 2048), kIdPV, (k > 0 || kk > 0) ? 1u : 0u);
-            umma_commit_we(bar(C::kBarPV + t));
-            if (NT == 1 || t == 1) umma_commit_we(bar(C::kBarEmpty + st));
-            if (k + 1 < count_of(t)) {
-              const int next = tile_of(t, k + 1);
-              ok = wait_all(C::kBarFull + next % C::kStages, phase(next, C::kStages));
+            next_fast = fast_tile(next);
+            if (next_fast) {                     // as soon as the scores before have been read
+              ok = wait_all(C::kBarSFree + t, static_cast<uint32_t>(k & 1));
               if (!ok) break;
               tc_fence_after_sync();
-              scores(t, k + 1);
+              scores(next, true);
             }
           }
+          ok = wait_all(C::kBarP + t, static_cast<uint32_t>(k & 1));
+          if (!ok) break;
+          tc_fence_after_sync();
+          const SmemDesc dv = desc_step(dv0, st * C::kOp);
+          if (fast) {
+            umma_ts_four<2048>(tO, tS + C::kColW, dv, kIdPV, k > 0 ? 1u : 0u);
+          } else {
+#pragma unroll 1
+            for (int g = 0; g < GV; ++g)
+              umma_ts_four<2048>(tO + 64 * g, tS + 64 + 32 * g, desc_step(dv, g * kKeys * 128), kIdPVg, k > 0 ? 1u : 0u);
+          }
+          umma_commit_we(bar(C::kBarPV + t));
+          umma_commit_we(bar(C::kBarEmpty + st));
+          if (k + 1 < count && !next_fast) scores(next, false);     // (over the weights just used)
+          st = next, ph = next_ph, fast = next_fast;
         }
         int no_abort = 0;
-        umma_commit_we(bar(C::kBarDrain));
-        mbar_wait(bar(C::kBarDrain), 0, &no_abort, limit);
+        umma_commit_we(bar(C::kBarDrain + t));
+        mbar_wait(bar(C::kBarDrain + t), 0, &no_abort, limit);
       }
       __syncwarp();
+    } else if (warp == 2) {
+      // ================= scales =================
+      bool ok = *abort_flag == 0, fast = true;
+      int x[GV];                             // exponents of V's scales, 0 before the first
+      bool set[GV];
+#pragma unroll
+      for (int g = 0; g < GV; ++g) x[g] = 0, set[g] = false;
+      for (int j = 0; j < n && ok; ++j) {
+        const int rs = j % C::kRawStages;
+        ok = wait_all(C::kBarRawFull + rs, phase(j, C::kRawStages));
+        if (!ok) break;
+        const uint8_t* raw = smem + C::kOffRaw + rs * kTilePages * C::kBlock;
+        const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + C::kOffRawMask) + 2 * rs;
+        TileHead& head = reinterpret_cast<TileHead*>(smem + C::kOffRawHead)[rs];
+        uint32_t word[GK + GV][kTilePages];    // of key `lane` of each page; 0 for keys that are not there
+        uint32_t most[GK + GV][kTilePages], all[GK + GV], least[GK + GV];
+#pragma unroll
+        for (int w = 0; w < GK + GV; ++w) {
+          least[w] = 0xFFFFFFFFu;
+#pragma unroll
+          for (int i = 0; i < kTilePages; ++i) {
+            const uint8_t* words = raw + i * C::kBlock + (w < GK ? off_k_words(DH, DV) : off_v_words(DH, DV));
+            const int of = w < GK ? static_cast<int>(lane) * GK + w : static_cast<int>(lane) * GV + w - GK;
+            word[w][i] = (masks[i] >> lane) & 1u ? reinterpret_cast<const uint32_t*>(words)[of] : 0u;
+            const uint32_t scale = word[w][i] & 0xFFFF0000u;
+            most[w][i] = __reduce_max_sync(0xffffffffu, scale);
+            least[w] = min(least[w], scale ? scale : 0xFFFFFFFFu);
+          }
+          least[w] = __reduce_min_sync(0xffffffffu, least[w]);
+          all[w] = max(most[w][0], most[w][1]);
+        }
+        uint32_t k_most = all[0], k_least = least[0];
+        if (GK == 2) k_most = max(k_most, all[GK - 1]), k_least = min(k_least, least[GK - 1]);
+        // Exponents of the bits of a scale (those of 0 do not count).
+        auto exponent = [](uint32_t bits) { return static_cast<int>(bits >> 23) - 127; };
+        const int k_exp = k_most ? exponent(k_most) : 0;
+        fast = fast && (!k_most || (k_exp <= kMostExp && k_exp >= -kMostExp && exponent(k_least) >= k_exp - kSpreadK));
+#pragma unroll
+        for (int g = 0; g < GV; ++g) {
+          if (all[GK + g] == 0u) continue;
+          const int hi = exponent(all[GK + g]), lo = exponent(least[GK + g]);
+          if (!set[g]) x[g] = hi, set[g] = true;
+          fast = fast && hi <= kMostExp && hi >= -kMostExp && hi <= x[g] + kAbove && lo >= x[g] - kBelow;
+        }
+        uint32_t* prep = reinterpret_cast<uint32_t*>(smem + C::kOffPrep + rs * C::kPrep) + lane;
+#pragma unroll
+        for (int w = 0; w < GK + GV; ++w)
+#pragma unroll
+          for (int i = 0; i < kTilePages; ++i) {
+            const float scale = bf16_hi(word[w][i]);
+            // (bf16 has 16 bits, so that the zero point has a place beside it too.)
+            uint32_t out = word[w][i];
+            if (fast) out = pack_half2(0.f, scale * exp2_int(w < GK ? kScaleK - k_exp : -x[w < GK ? 0 : w - GK])) |
+                            (word[w][i] & 0xFFu);
+            prep[w * kKeys + i * kPageTokens] = out;
+          }
+        if (fast) {                              // s (8 - z) 2^kSumShift of both groups
+#pragma unroll
+          for (int i = 0; i < kTilePages; ++i) {
+            float x[2] = {0.f, 0.f};
+#pragma unroll
+            for (int g = 0; g < GK; ++g)
+              x[g] = bf16_hi(word[g][i]) * exp2_int(kScaleK + kSumShift - k_exp) *
+                     static_cast<float>(8 - static_cast<int>(word[g][i] & 0xFFu));
+            prep[(GK + GV) * kKeys + i * kPageTokens] = pack_half2(x[0], x[1]);
+          }
+        }
+        if (lane == 0) {
+          head.mask[0] = masks[0], head.mask[1] = masks[1];
+          head.unscale = exp2_int(k_exp - kScaleK);
+          head.fast = fast ? 1 : 0;
+#pragma unroll
+          for (int g = 0; g < GV; ++g) {
+            head.up[g] = exp2_int(kFastBits - x[g]);
+#pragma unroll
+            for (int i = 0; i < kTilePages; ++i) head.most[g][i] = __uint_as_float(most[GK + g][i]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarPrep + rs));
+      }
     }
   } else if (warp >= 12) {
     // ================= codes into operands =================
     setmaxnreg_to<C::kRegsOperands, C::kRegsLaunch>();
-    const int tid = static_cast<int>(threadIdx.x) - 384, w4 = static_cast<int>(warp) - 12;
+    const int tid = static_cast<int>(threadIdx.x) - 384, w8 = static_cast<int>(warp) - 12;
+    // The second half of the sums' inner step is 0.
+    for (int i = tid; i < C::kStages * kKeys; i += C::kOpThreads)
+      *reinterpret_cast<uint4*>(smem + C::kOffOp + i / kKeys * C::kOp + C::kK16 + C::kV16 + i % kKeys / 8 * 256 + 128 +
+                                i % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
     bool ok = *abort_flag == 0;
+    int st = C::kStages - 1;
+    uint32_t ph = 0;                       // of the stage's next release
     for (int j = 0; j < n && ok; ++j) {
-      const int rs = j % C::kRawStages, st = j % C::kStages;
-      ok = wait_all(C::kBarRawFull + rs, phase(j, C::kRawStages));
-      if (ok && j >= C::kStages) ok = wait_all(C::kBarEmpty + st, phase(j - C::kStages, C::kStages));
+      const int rs = j % C::kRawStages;
+      if (++st == C::kStages) st = 0, ph ^= 1u;
+      ok = wait_all(C::kBarRawFull + rs, phase(j, C::kRawStages)) && wait_all(C::kBarPrep + rs, phase(j, C::kRawStages));
+      if (ok && j >= C::kStages) ok = wait_all(C::kBarEmpty + st, ph);
       if (!ok) break;
       const uint8_t* raw = smem + C::kOffRaw + rs * kTilePages * C::kBlock;
-      uint8_t* k16 = smem + C::kOffOp + st * (C::kK16 + C::kV16);
-      // A row of D dims is D / 8 words; a warp takes 256 / D rows at a time.
-      auto convert = [&](auto width, int codes_at, int words_at, uint8_t* out) {
-        constexpr int D = decltype(width)::value, kWords = D / 8, kRows = 32 / kWords, G = D / kQuantGroup;
-        const int c = static_cast<int>(lane) % kWords;
+      const uint32_t* prep = reinterpret_cast<const uint32_t*>(smem + C::kOffPrep + rs * C::kPrep);
+      const TileHead& head = reinterpret_cast<const TileHead*>(smem + C::kOffRawHead)[rs];
+      uint8_t* op = smem + C::kOffOp + st * C::kOp;
+      const bool fast = head.fast != 0;
+      // A row of D dims is D / 8 words; a warp takes 256 / D rows at a time, all of
+      // its words requested before the first is converted.
+      auto convert = [&](auto width, int codes_at, const uint32_t* scale, uint8_t* out, auto&& operand) {
+        constexpr int D = decltype(width)::value, kWords = D / 8, kRows = 32 / kWords, kTimes = kKeys / (8 * kRows);
+        const int c = static_cast<int>(lane) % kWords, g = c / 8;
+        const int key0 = w8 * kRows + static_cast<int>(lane) / kWords;
+        uint8_t* to = out + g * (kKeys * 128);
+        uint32_t codes[kTimes], word[kTimes];
 #pragma unroll
-        for (int i = 0; i < kKeys / (4 * kRows); ++i) {
-          const int key = (i * 4 + w4) * kRows + static_cast<int>(lane) / kWords;
-          const uint8_t* blk = raw + key / kPageTokens * C::kBlock;
-          const int at = key % kPageTokens;
-          const uint32_t codes = *reinterpret_cast<const uint32_t*>(blk + codes_at + at * (D / 2) + 4 * c);
-          const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + words_at + (at * G + c / 8) * 4);
-          *reinterpret_cast<uint4*>(out + c / 8 * (kKeys * 128) + key * 128 + (((c & 7) ^ (key & 7)) * 16)) =
-              operand8(codes, word);
+        for (int i = 0; i < kTimes; ++i) {
+          const int key = i * 8 * kRows + key0;
+          codes[i] = *reinterpret_cast<const uint32_t*>(raw + key / kPageTokens * C::kBlock + codes_at +
+                                                        key % kPageTokens * (D / 2) + 4 * c);
+          word[i] = scale[g * kKeys + key];
+        }
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+          const int key = i * 8 * kRows + key0;
+          *reinterpret_cast<uint4*>(to + key * 128 + (((c & 7) ^ (key & 7)) * 16)) = operand(codes[i], word[i]);
         }
       };
-      convert(std::integral_constant<int, DH>{}, off_k_codes(), off_k_words(DH, DV), k16);
-      convert(std::integral_constant<int, DV>{}, off_v_codes(DH), off_v_words(DH, DV), k16 + C::kK16);
-      // The keys' scales as fp32 (0 for keys that are not there), and the
-      // largest of V's in each page.
-      const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + C::kOffRawMask) + 2 * rs;
-      float* scales = reinterpret_cast<float*>(smem + C::kOffScale + st * C::kScales);
-#pragma unroll
-      for (int i = 0; i < (GK + GV) * kKeys / 128 + ((GK + GV) * kKeys % 128 != 0); ++i) {
-        const int at = i * 128 + tid, which = at / kKeys, key = at % kKeys;     // (a warp: one `which`, one page)
-        if (which < GK + GV) {
-          const int page = key / kPageTokens;
-          const uint8_t* words = raw + page * C::kBlock + (which < GK ? off_k_words(DH, DV) : off_v_words(DH, DV));
-          const int of = which < GK ? (key % kPageTokens) * GK + which : (key % kPageTokens) * GV + which - GK;
-          const bool there = (masks[page] >> (key % kPageTokens)) & 1u;
-          const uint32_t bits = there ? reinterpret_cast<const uint32_t*>(words)[of] & 0xFFFF0000u : 0u;
-          scales[which * kKeys + key] = __uint_as_float(bits);
-          const uint32_t most = __reduce_max_sync(0xffffffffu, bits);
-          if (which >= GK && lane == 0)
-            reinterpret_cast<uint32_t*>(smem + C::kOffMax)[st * 4 + (which - GK) * 2 + page] = most;
-        }
+      constexpr std::integral_constant<int, DH> kDH{};
+      constexpr std::integral_constant<int, DV> kDV{};
+      if (fast) {
+        convert(kDH, off_k_codes(), prep, op, [](uint32_t codes, uint32_t word) {
+          return times(operand8(codes, 0x64086408u, 0xD480D480u), __byte_perm(word, 0u, 0x3232));
+        });
+        convert(kDV, off_v_codes(DH), prep + GK * kKeys, op + C::kK16, [](uint32_t codes, uint32_t word) {
+          return times(operand8z(codes, word), __byte_perm(word, 0u, 0x3232));
+        });
+      } else {
+        convert(kDH, off_k_codes(), prep, op, operand8z);
+        convert(kDV, off_v_codes(DH), prep + GK * kKeys, op + C::kK16, operand8z);
       }
-      if (tid < 2) (reinterpret_cast<uint32_t*>(smem + C::kOffMask) + 2 * st)[tid] = masks[tid];
+      if (fast) {
+        if (tid < kKeys) {                      // s (8 - z) of each group, three times
+          const uint32_t x = prep[(GK + GV) * kKeys + tid];
+          *reinterpret_cast<uint4*>(op + C::kK16 + C::kV16 + tid / 8 * 256 + tid % 8 * 16) =
+              make_uint4(__byte_perm(x, 0u, 0x1010), x, __byte_perm(x, 0u, 0x3232), 0u);
+        }
+      } else {
+        uint32_t* scales = reinterpret_cast<uint32_t*>(smem + C::kOffScale + st * C::kScales);
+        for (int i = tid; i < (GK + GV) * kKeys; i += C::kOpThreads) scales[i] = prep[i] & 0xFFFF0000u;
+      }
+      if (tid < static_cast<int>(sizeof(TileHead) / 4))
+        reinterpret_cast<uint32_t*>(smem + C::kOffHead + st * sizeof(TileHead))[tid] =
+            reinterpret_cast<const uint32_t*>(&head)[tid];
       fence_proxy_async_smem();
       mbar_arrive(bar(C::kBarFull + st));
       mbar_arrive(bar(C::kBarRawEmpty + rs));
@@ -327,182 +549,314 @@ __global__ void __launch_bounds__(512, 1) prefix_tile_kernel(const __grid_consta
     setmaxnreg_to<C::kRegsSoftmax, C::kRegsLaunch>();
     const int t = static_cast<int>(warp) / 4 - 1;          // stream
     const uint32_t quad = warp & 3;
-    const int row = static_cast<int>(quad * 32 + lane), r = r0 + (NT == 2 ? 128 * t : 0) + row;
+    const int row = static_cast<int>(quad * 32 + lane), tile0 = r0 + (NT == 2 ? 128 * t : 0), r = tile0 + row;
     const bool valid = r < R;
     const uint32_t lane_base = (quad * 32u) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + 256 + 128 * t;
-    // ---- the row of Q: its power of two, its fp16 operands ----
+    // ---- Q: each row's power of two, its fp16 operands and sums ----
+    // The warp's rows (with one row tile the streams share its rows) are read
+    // 16 bytes a lane, 128 / D rows at a time, and put down swizzled; then a
+    // thread takes its own row into tensor memory.
     float f;
     {
-      const int of = valid ? r / p.per : 0;
-      const int64_t q_row = (static_cast<int64_t>(of) * p.Hkv + h) * p.per + (valid ? r - of * p.per : 0);
-      const uint4* q = reinterpret_cast<const uint4*>(p.Q) + q_row * (DH / 8);
-      uint4 v[DH / 8];
-      uint32_t m = 0u;
+      constexpr int kLanes = DH / 8, kAt = 32 / kLanes, kWarpRows = NT == 2 ? 32 : 16, kTimes = kWarpRows / kAt;
+      constexpr int kBatch = kTimes < 8 ? kTimes : 8;
+      uint8_t* tile = smem + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile;
+      // Of each row: sum q_g and the largest magnitude.
+      float(*rows_of)[4] = reinterpret_cast<float(*)[4]>(smem + C::kOffState) + (NT == 2 ? 128 * t : 0);
+      const int c = static_cast<int>(lane) % kLanes;
+      const int first = static_cast<int>(quad) * 32 + (NT == 2 ? 0 : 16 * t) + static_cast<int>(lane) / kLanes;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
+        uint4 v[kBatch];
 #pragma unroll
-      for (int c = 0; c < DH / 8; ++c) {
-        v[c] = valid ? q[c] : make_uint4(0u, 0u, 0u, 0u);
-        m = bf16_absmax_fold(m, v[c]);
-      }
-      const float mx = bf16_absmax_value(m);
-      int e = 0;                                           // 2^14 <= mx 2^e < 2^15
-      if (mx > 0.f && mx < INFINITY) e = 14 - ilogbf(mx);
-      e = e > 120 ? 120 : e;
-      // (Not 0, which a masked -inf must not meet; NaN for a row that is not finite.)
-      f = fmaxf(p.scale_log2 * exp2_int(-e), 0x1p-126f);
-      if (!(mx < INFINITY)) f = __uint_as_float(0x7FC00000u);
-      if (NT == 2 || t == 0) {
-        uint8_t* to = smem + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile + row * 128;
+        for (int i = 0; i < kBatch; ++i) {
+          const int rr = tile0 + first + (i0 + i) * kAt;
+          const int of = rr < R ? rr / p.per : 0;
+          const int64_t at = (static_cast<int64_t>(of) * p.Hkv + h) * p.per + (rr < R ? rr - of * p.per : 0);
+          v[i] = rr < R ? reinterpret_cast<const uint4*>(p.Q)[at * kLanes + c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+        // (Each step for all rows of the batch, so that their shuffles overlap.)
+        uint32_t mb[kBatch];
+        float sum[kBatch];
 #pragma unroll
-        for (int c = 0; c < DH / 8; ++c) {
-          const uint4 u = bf16x8_to_f16x8_scaled(v[c], exp2_int(e));
-          *reinterpret_cast<uint4*>(to + c / 8 * (128 * 128) + (((c & 7) ^ (row & 7)) * 16)) =
+        for (int i = 0; i < kBatch; ++i) mb[i] = __float_as_uint(bf16_absmax_value(bf16_absmax_fold(0u, v[i])));
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1)
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) mb[i] = max(mb[i], __shfl_xor_sync(0xffffffffu, mb[i], off));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int rr = first + (i0 + i) * kAt;
+          // 2^14 <= max 2^e < 2^15; below 2^-106, and for 0 and what is not finite, less.
+          const int ex = static_cast<int>(mb[i] >> 23) - 127;
+          const int e = ex == 128 || mb[i] == 0u ? 0 : min(14 - ex, 120);
+          const float times_e = exp2_int(e);
+          const uint4 u = bf16x8_to_f16x8_scaled(v[i], times_e);
+          *reinterpret_cast<uint4*>(tile + c / 8 * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) * 16)) =
               make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
                          __byte_perm(u.y, u.w, 0x7632));
+          const uint32_t xs[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          float a = 0.f, b = 0.f;
+#pragma unroll
+          for (int o = 0; o < 4; ++o) a = fmaf(bf16_lo(xs[o]), times_e, a), b = fmaf(bf16_hi(xs[o]), times_e, b);
+          sum[i] = a + b;
+        }
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1)
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if ((c & 7) == 0) rows_of[first + (i0 + i) * kAt][c / 8] = sum[i];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (c == 0) rows_of[first + (i0 + i) * kAt][2] = __uint_as_float(mb[i]);
+      }
+      fence_proxy_async_smem();
+      if (NT == 1) named_bar_sync(1, 256);
+      else __syncwarp();
+      {
+        const float4 of = *reinterpret_cast<const float4*>(rows_of[row]);
+        const uint32_t mb = __float_as_uint(of.z);
+        const int ex = static_cast<int>(mb >> 23) - 127;
+        const int e = ex == 128 || mb == 0u ? 0 : min(14 - ex, 120);
+        // (Not 0, which a masked -inf must not meet; NaN for a row that is not finite.)
+        f = fmaxf(p.scale_log2 * exp2_int(-e), 0x1p-126f);
+        if (ex == 128) f = __uint_as_float(0x7FC00000u);
+        if (NT == 2 || t == 0) {                           // sum q_g 2^-6: three fp16 numbers of each group
+          uint32_t h16[6] = {0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int g = 0; g < GK; ++g) {
+            float left = (g == 0 ? of.x : of.y) * exp2_int(-kSumShift);
+#pragma unroll
+            for (int o = 0; o < 3; ++o) {
+              const __half x = __float2half_rn(left);
+              left -= __half2float(x);
+              h16[3 * g + o] = __half_as_ushort(x);
+            }
+          }
+          uint4* to = reinterpret_cast<uint4*>(smem + C::kOffQx + (NT == 2 ? t : 0) * C::kQx + row / 8 * 256 + row % 8 * 16);
+          to[0] = make_uint4(h16[0] | h16[1] << 16, h16[2] | h16[3] << 16, h16[4] | h16[5] << 16, 0u);
+          to[8] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::kBarQ));
       }
+#pragma unroll 1
+      for (int k = 0; k < C::kTmemQ * 8; k += 2) {
+        uint32_t q16[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(tile + k / 8 * (128 * 128) + row * 128 +
+                                                          (((k + i) & 7) ^ (row & 7)) * 16);
+          q16[4 * i] = x.x, q16[4 * i + 1] = x.y, q16[4 * i + 2] = x.z, q16[4 * i + 3] = x.w;
+        }
+        tmem_st8_nowait(tS + C::kColQ + 4 * k, q16);
+      }
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(bar(C::kBarQ));
     }
-    float shift = -kNoKey, l_sum = 0.f;        // less the reference that P is relative to; the sum of P
-    float up[GV], s_lim[GV];                   // 1 / top; the scale from which on a weight may be too large
+    // Less the reference that P is relative to; the sum of P, times 2^kFastBits
+    // until the first tile without folded scales.
+    float shift = -kNoKey, l_sum = 0.f;
+    // 1 / top, of the folded operands or each row's; the scale from which on a
+    // weight may be too large.
+    float up[GV], s_lim[GV];
 #pragma unroll
     for (int g = 0; g < GV; ++g) up[g] = exp2_int(-kLeastTop), s_lim[g] = 0.f;
+    bool folded = true;
     uint32_t seen = 0u;                        // keys there were
     const int mine = count_of(t);
     bool ok = *abort_flag == 0;
-    for (int k = 0; k < mine && ok; ++k) {
-      const int j = tile_of(t, k), st = j % C::kStages;
-      ok = wait_all(C::kBarS + t, static_cast<uint32_t>(k & 1)) && wait_all(C::kBarFull + st, phase(j, C::kStages));
-      if (!ok) break;
+    // O's columns of each group times a factor, once the products before have been added.
+    auto rescale = [&](int k, float back0, float back1) {
+      if (!wait_all(C::kBarPV + t, static_cast<uint32_t>((k - 1) & 1))) return false;
       tc_fence_after_sync();
-      const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale + st * C::kScales);
-      // ---- scores ----
-      float s[kKeys];
+#pragma unroll 1
+      for (int c = 0; c < DV; c += 16) {
+        const float times_b = c < 64 ? back0 : back1;
+        uint32_t o[16];
+        tmem_ld16_nowait(tO + c, o);
+        tmem_wait_ld16(o);
 #pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c) {
-        uint32_t a[GK][32];
-#pragma unroll
-        for (int g = 0; g < GK; ++g) tmem_ld32_nowait(tS + 64 * g + 32 * c, a[g]);
-#pragma unroll
-        for (int g = 0; g < GK; ++g) tmem_wait_ld32(a[g]);
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float* x = s + 32 * c + i;
-#pragma unroll
-          for (int g = 0; g < GK; ++g) {
-            const float4 sk = *reinterpret_cast<const float4*>(scales + g * kKeys + 32 * c + i);
-            auto at = [&](int o) { return __uint_as_float(a[g][i + o]); };
-            if (g == 0) {
-              fmul2(x[0], x[1], at(0), at(1), sk.x, sk.y);
-              fmul2(x[2], x[3], at(2), at(3), sk.z, sk.w);
-            } else {
-              ffma2(x[0], x[1], at(0), at(1), sk.x, sk.y, x[0], x[1]);
-              ffma2(x[2], x[3], at(2), at(3), sk.z, sk.w, x[2], x[3]);
-            }
-          }
-        }
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * times_b);
+        tmem_st16_nowait(tO + c, o);
       }
-      const uint2 mask = *reinterpret_cast<const uint2*>(smem + C::kOffMask + 8 * st);
-      seen |= mask.x | mask.y;
-      if ((mask.x & mask.y) != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i)
-          if (!(((i < 32 ? mask.x : mask.y) >> (i & 31)) & 1u)) s[i] = -INFINITY;
-      }
-      // ---- running maximum (lazy) and the weights' scales ----
-      float mx = fmaxf(s[0], s[1]), mx2 = fmaxf(s[2], s[3]);
+      return true;
+    };
+    auto row_max = [](const float* s) {
+      float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
 #pragma unroll
       for (int i = 4; i < kKeys; i += 4) {
-        mx = fmax3(mx, s[i], s[i + 1]);
-        mx2 = fmax3(mx2, s[i + 2], s[i + 3]);
+        a = fmax3(a, s[i], s[i + 1]);
+        b = fmax3(b, s[i + 2], s[i + 3]);
       }
-      mx = fmaxf(mx, mx2);
-      bool need = fmaf(mx, f, shift) > static_cast<float>(kLazy);
+      return fmaxf(a, b);
+    };
+    auto hide = [](uint2 mask, float* s) {
+      if ((mask.x & mask.y) == 0xFFFFFFFFu) return;
 #pragma unroll
-      for (int g = 0; g < GV; ++g) {
-        const float2 sm = *reinterpret_cast<const float2*>(smem + C::kOffMax + st * 16 + g * 8);
-        need |= fmaxf(sm.x, sm.y) > s_lim[g];
-      }
-      const float* sv = scales + GK * kKeys;
-      if (__any_sync(0xffffffffu, need)) {
-        const float m = ceilf(mx * f);
-        float alpha = 1.f;
-        if (m + shift > static_cast<float>(kLazy)) {       // (whole octaves: alpha is a power of two)
-          alpha = fast_exp2(-shift - m);
-          shift = -m;
+      for (int i = 0; i < kKeys; ++i)
+        if (!(((i < 32 ? mask.x : mask.y) >> (i & 31)) & 1u)) s[i] = -INFINITY;
+    };
+    int st = NT == 2 ? -1 : t - 2;             // stage of the tile at hand, and its phase
+    uint32_t ph = 0;
+    for (int k = 0; k < mine && ok; ++k) {
+      st += NT == 2 ? 1 : 2;
+      if (st >= C::kStages) st -= C::kStages, ph ^= 1u;
+      ok = wait_all(C::kBarS + t, static_cast<uint32_t>(k & 1)) && wait_all(C::kBarFull + st, ph);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const TileHead& head = reinterpret_cast<const TileHead*>(smem + C::kOffHead)[st];
+      const uint2 mask = *reinterpret_cast<const uint2*>(head.mask);
+      seen |= mask.x | mask.y;
+      if (__shfl_sync(0xffffffffu, head.fast, 0)) {
+        // ---- scales in the operands ----
+        float s[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_ld32_nowait(tS + c, reinterpret_cast<uint32_t(&)[32]>(s[c]));
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(s[c]));
+        tc_fence_before_sync();
+        mbar_arrive(bar(C::kBarSFree + t));
+        hide(mask, s);
+        float fk = f * head.unscale;              // (not 0, as f)
+        fk = fk < 0x1p-126f ? 0x1p-126f : fk;
+        const float mx = row_max(s) * fk;
+        if (__any_sync(0xffffffffu, mx + shift > static_cast<float>(kLazy))) {
+          const float m = ceilf(mx);
+          float alpha = 1.f;
+          if (m + shift > static_cast<float>(kLazy)) {     // (whole octaves: alpha is a power of two)
+            alpha = fast_exp2(-shift - m);
+            shift = -m;
+          }
+          l_sum *= alpha;
+          if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            ok = rescale(k, alpha, alpha);
+            if (!ok) break;
+          }
         }
-        l_sum *= alpha;
-        float most[GV], back[GV];
-        bool change = false;
-#pragma unroll
-        for (int g = 0; g < GV; ++g) most[g] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) {
-          const float w = fast_exp2(fmaf(s[i], f, shift));
-#pragma unroll
-          for (int g = 0; g < GV; ++g) most[g] = fmaxf(most[g], w * sv[g * kKeys + i]);
-        }
-#pragma unroll
-        for (int g = 0; g < GV; ++g) {
-          const float was = alpha * inverse_power(up[g]);
-          const uint32_t at_least = max(near_power(was), static_cast<uint32_t>(127 + kLeastTop) << 23);
-          const uint32_t now = max(at_least, next_power(most[g] * exp2_int(-kTopBits)));
-          const float top = __uint_as_float(min(now, static_cast<uint32_t>(127 + kMostTop) << 23));
-          up[g] = inverse_power(top);
-          back[g] = was * up[g];                           // at most 1
-          s_lim[g] = top * exp2_int(kTopBits + kSlack);
-          change |= back[g] != 1.f;
-        }
-        if (k > 0 && __any_sync(0xffffffffu, change)) {
+        if (k > 0) {                             // the weights before have been used
           ok = wait_all(C::kBarPV + t, static_cast<uint32_t>((k - 1) & 1));
           if (!ok) break;
           tc_fence_after_sync();
-#pragma unroll
-          for (int g = 0; g < GV; ++g)
-#pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-              uint32_t o[16];
-              tmem_ld16_nowait(tO + 64 * g + c, o);
-              tmem_wait_ld16(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * back[g]);
-              tmem_st16_nowait(tO + 64 * g + c, o);
-            }
         }
-      }
-      // ---- weights ----
+        const float add = shift + static_cast<float>(kFastBits);
+        float l[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) {
-        uint32_t w[GV][16];
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float e[4];
-          const float* x = s + c + i;
-          ffma2(e[0], e[1], x[0], x[1], f, f, shift, shift);
-          ffma2(e[2], e[3], x[2], x[3], f, f, shift, shift);
+          for (int i = 0; i < 32; i += 2) {
+            float e0, e1;
+            ffma2(e0, e1, s[c + i], s[c + i + 1], fk, fk, add, add);
+            e0 = fast_exp2(e0);
+            e1 = fast_exp2(e1);
+            fadd2(l[0], l[1], e0, e1);
+            w[i / 2] = pack_half2(e0, e1);
+          }
+          tmem_st16_nowait(tS + C::kColW + c / 2, w);
+        }
+        l_sum += l[0] + l[1];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) e[u] = fast_exp2(e[u]);
-          l_sum += (e[0] + e[1]) + (e[2] + e[3]);
+        for (int g = 0; g < GV; ++g) up[g] = head.up[g];
+      } else {
+        // ---- scales beside the operands ----
+        const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale + st * C::kScales);
+        const float* sv = scales + GK * kKeys;
+        if (folded) {
+          folded = false;
+          l_sum *= exp2_int(-kFastBits);
+        }
+        // The scores put together, over S_0, and their maximum; then W in the next
+        // 64 columns.  (Loops: this is not where the time goes.)
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kKeys; c += 16) {
+          uint32_t a[16], b[16];
+          tmem_ld16_nowait(tS + c, a);
+          if (GK == 2) tmem_ld16_nowait(tS + 64 + c, b);
+          tmem_wait_ld16(a);
+          if (GK == 2) tmem_wait_ld16(b);
+          const uint32_t bits = (c < 32 ? mask.x : mask.y) >> (c & 31);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x = __uint_as_float(a[i]) * scales[c + i];
+            if (GK == 2) x = fmaf(__uint_as_float(b[i]), scales[kKeys + c + i], x);
+            if (!((bits >> i) & 1u)) x = -INFINITY;
+            mx = fmaxf(mx, x);
+            a[i] = __float_as_uint(x);
+          }
+          tmem_st16_nowait(tS + c, a);
+        }
+        tmem_wait_st();
+        bool need = fmaf(mx, f, shift) > static_cast<float>(kLazy);
+#pragma unroll
+        for (int g = 0; g < GV; ++g) need |= fmaxf(head.most[g][0], head.most[g][1]) > s_lim[g];
+        if (__any_sync(0xffffffffu, need)) {
+          const float m = ceilf(mx * f);
+          float alpha = 1.f;
+          if (m + shift > static_cast<float>(kLazy)) {
+            alpha = fast_exp2(-shift - m);
+            shift = -m;
+          }
+          l_sum *= alpha;
+          float most[GV], back[GV];
+          bool change = false;
+#pragma unroll
+          for (int g = 0; g < GV; ++g) most[g] = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 16) {
+            uint32_t a[16];
+            tmem_ld16_nowait(tS + c, a);
+            tmem_wait_ld16(a);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float w = fast_exp2(fmaf(__uint_as_float(a[i]), f, shift));
+#pragma unroll
+              for (int g = 0; g < GV; ++g) most[g] = fmaxf(most[g], w * sv[g * kKeys + c + i]);
+            }
+          }
 #pragma unroll
           for (int g = 0; g < GV; ++g) {
-            const float4 sc = *reinterpret_cast<const float4*>(sv + g * kKeys + c + i);
-            float y[4];
-            fmul2(y[0], y[1], e[0], e[1], up[g], up[g]);
-            fmul2(y[2], y[3], e[2], e[3], up[g], up[g]);
-            fmul2(y[0], y[1], y[0], y[1], sc.x, sc.y);
-            fmul2(y[2], y[3], y[2], y[3], sc.z, sc.w);
-            w[g][i / 2] = pack_half2(y[0], y[1]);
-            w[g][i / 2 + 1] = pack_half2(y[2], y[3]);
+            const float was = alpha * inverse_power(up[g]);
+            const uint32_t at_least = max(near_power(was), static_cast<uint32_t>(127 + kLeastTop) << 23);
+            const uint32_t now = max(at_least, next_power(most[g] * exp2_int(-kTopBits)));
+            const float top = __uint_as_float(min(now, static_cast<uint32_t>(127 + kMostTop) << 23));
+            up[g] = inverse_power(top);
+            back[g] = was * up[g];                           // at most 1
+            s_lim[g] = top * exp2_int(kTopBits + kSlack);
+            change |= back[g] != 1.f;
+          }
+          if (k > 0 && __any_sync(0xffffffffu, change)) {
+            ok = rescale(k, back[0], back[GV - 1]);
+            if (!ok) break;
           }
         }
+#pragma unroll 1
+        for (int c = 0; c < kKeys; c += 16) {
+          uint32_t a[16], w[GV][8];
+          tmem_ld16_nowait(tS + c, a);
+          tmem_wait_ld16(a);
 #pragma unroll
-        for (int g = 0; g < GV; ++g) tmem_st16_nowait(tS + 32 * g + c / 2, w[g]);
+          for (int i = 0; i < 16; i += 2) {
+            const float e0 = fast_exp2(fmaf(__uint_as_float(a[i]), f, shift));
+            const float e1 = fast_exp2(fmaf(__uint_as_float(a[i + 1]), f, shift));
+            l_sum += e0 + e1;
+#pragma unroll
+            for (int g = 0; g < GV; ++g)
+              w[g][i / 2] = pack_half2(e0 * up[g] * sv[g * kKeys + c + i], e1 * up[g] * sv[g * kKeys + c + i + 1]);
+          }
+#pragma unroll
+          for (int g = 0; g < GV; ++g) tmem_st8_nowait(tS + 64 + 32 * g + c / 2, w[g]);
+        }
       }
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(bar(C::kBarP + t));
     }
+    if (folded) l_sum *= exp2_int(-kFastBits);
     if (ok && mine > 0) ok = wait_all(C::kBarPV + t, static_cast<uint32_t>((mine - 1) & 1));
     tc_fence_after_sync();
     if (seen == 0u) l_sum = 0.f;
@@ -515,14 +869,15 @@ __global__ void __launch_bounds__(512, 1) prefix_tile_kernel(const __grid_consta
       if (t == 1) {
         state[row] = make_float2(l_sum, shift);
         if (mine > 0) {
-#pragma unroll
+          const float down0 = inverse_power(up[0]), down1 = inverse_power(up[GV - 1]);
+#pragma unroll 1
           for (int c = 0; c < DV; c += 16) {
             uint32_t o[16];
             tmem_ld16_nowait(tO + c, o);
             tmem_wait_ld16(o);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              theirs[(c + i) * 128 + row] = __uint_as_float(o[i]) * inverse_power(up[c / 64]);
+              theirs[(c + i) * 128 + row] = __uint_as_float(o[i]) * (c < 64 ? down0 : down1);
           }
         }
       }
@@ -540,27 +895,38 @@ __global__ void __launch_bounds__(512, 1) prefix_tile_kernel(const __grid_consta
       const float inv = l_sum > 0.f ? 1.0f / l_sum : (l_sum == 0.f ? 0.f : l_sum);    // (NaN stays NaN)
       const int64_t out = static_cast<int64_t>(item) * 128 * NT + r - r0;
       if (valid) p.Lpart[out] = l_sum == 0.f ? -INFINITY : (fast_log2(l_sum) - shift) * kLn2;
-      float* dst = p.Opart + out * DV;
+      const float down0 = inverse_power(up[0]) * weight, down1 = inverse_power(up[GV - 1]) * weight;
+      // 32 dims at a time over this tile's Q, then whole lines out of there.
+      uint8_t* mine_at = smem + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile + quad * 4096;
+#pragma unroll 1
+      for (int c = 0; c < DV; c += 32) {
+        uint32_t o[32];
+        tmem_ld32_nowait(tO + c, o);
+        tmem_wait_ld32(o);
+        const float mul = c < 64 ? down0 : down1;
 #pragma unroll
-      for (int c = 0; c < DV; c += 16) {
-        uint32_t o[16];
-        tmem_ld16_nowait(tO + c, o);
-        tmem_wait_ld16(o);
-        const float mul = inverse_power(up[c / 64]) * weight;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] = __uint_as_float(o[i]) * mul;
-          if (NT == 1 && count_of(1) > 0) x[i] = fmaf(theirs[(c + i) * 128 + row], other, x[i]);
-          x[i] *= inv;
+        for (int i = 0; i < 32; ++i) {
+          float x = __uint_as_float(o[i]) * mul;
+          if (NT == 1 && count_of(1) > 0) x = fmaf(theirs[(c + i) * 128 + row], other, x);
+          o[i] = __float_as_uint(x * inv);
         }
-        if (valid) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 8) {                // columns (0, 4, 1, 5, 2, 6, 3, 7) of eight
-            *reinterpret_cast<float4*>(dst + c + i) = make_float4(x[i], x[i + 2], x[i + 4], x[i + 6]);
-            *reinterpret_cast<float4*>(dst + c + i + 4) = make_float4(x[i + 1], x[i + 3], x[i + 5], x[i + 7]);
-          }
+        for (int i = 0; i < 32; i += 8) {                  // columns (0, 4, 1, 5, 2, 6, 3, 7) of eight
+          uint4* to = reinterpret_cast<uint4*>(mine_at + lane * 128);
+          to[(i / 4) ^ (lane & 7)] = make_uint4(o[i], o[i + 2], o[i + 4], o[i + 6]);
+          to[(i / 4 + 1) ^ (lane & 7)] = make_uint4(o[i + 1], o[i + 3], o[i + 5], o[i + 7]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = i * 4 + static_cast<int>(lane >> 3), chunk = static_cast<int>(lane & 7);
+          const int rr = static_cast<int>(quad) * 32 + at;
+          const uint4 x = *reinterpret_cast<const uint4*>(mine_at + at * 128 + (chunk ^ (at & 7)) * 16);
+          if (tile0 + rr < R)
+            *reinterpret_cast<uint4*>(p.Opart + (static_cast<int64_t>(item) * 128 * NT + tile0 - r0 + rr) * DV + c +
+                                      4 * chunk) = x;
+        }
+        __syncwarp();
       }
     }
     tc_fence_before_sync();

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import _qk_cache_ref as ref
 import _serving_ref as srv
 from _qk_cache_ref import assert_within, bf16, f64
 
@@ -118,15 +119,57 @@ def test_values_of_very_different_sizes(B, spread):
             p = np.exp(s - s.max())
             A = p / p.sum()
             want = A @ V[:, r // 4]
-            # Per group of 64 dims: what the weights times the group's largest values are off by
-            # together, 2^-11 of each product, 2^-29 of the largest, as the header says, and O's rounding.
-            size = np.repeat(np.abs(V[:, r // 4].reshape(len(V), -1, 64)).max(-1), 64, -1)
-            ds = 132 * 2.0 ** -24 * dh ** -0.5 * (np.abs(K[:, r // 4]) @ np.abs(q[b, r, 0]))
-            rel = 2.0 ** -11 + 2 * (ds + 2.0 ** -20 * (1 + np.abs(s - s.max()) + abs(s.max()) / 4))
-            prod = A[:, None] * size
-            bound = (rel[:, None] * prod).sum(0) + len(V) * 2.0 ** -27 * prod.max(0)
-            bound += 2 * (len(V) / 16 + 8) * 2.0 ** -23 * 2.2 * prod.sum(0)
+            bound = _weighted_bound(A, s, K[:, r // 4], V[:, r // 4], q[b, r, 0], dh)
             assert_within(O[b, r, 0], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "O")
+
+
+@pytest.mark.parametrize("Hq", [4, 16])
+@pytest.mark.parametrize("at", [40, 700])
+@pytest.mark.parametrize("of", ["k", "v", "both"])
+def test_scales_that_change_along_the_prefix(Hq, at, of):
+    """Keys or values whose scales leave what went before, from one token on: some tiles are
+    taken with their scales in the operands, the others with the scales beside them."""
+    dh = dv = 128
+    rng = np.random.default_rng(at)
+    B, Hkv, prefix = 24, 1, 1200
+    c = srv.Paged(rng, Hkv, dh, dv, [prefix] + [2] * B)
+    size = np.where(np.arange(prefix) < at, 1.0, np.exp2(rng.integers(-15, 12, prefix)))[:, None, None]
+    K, V = rng.normal(size=(prefix, Hkv, dh)), rng.normal(size=(prefix, Hkv, dv))
+    # (large keys would leave one score each row: they get small ones)
+    K, V = bf16(K * (np.minimum(size, 2.0) if of != "v" else 1.0)), bf16(V * (size if of != "k" else 1.0))
+    if of != "v":
+        K[at + 5] *= 2.0 ** -14                     # further apart than a tile's scales may be
+    K[:, :, 64:] = np.abs(K[:, :, 64:])             # a zero point of 0
+    ref.store(c.pool, c.slots(0, prefix), K, V)
+    c.K[0], c.V[0] = ref.load(c.pool, c.slots(0, prefix), dh, dv)
+    q = _queries(rng, B, Hq, 1, dh)
+    args = dict(prefix_table=_dev(c.table[0]), prefix_length=_dev(np.array([prefix], np.int32)),
+                page_table=_dev(c.table[1:, :1]), lengths=_dev(np.array([2] * B, np.int32)))
+    O, LSE = _run(c, q, args, dh, dv)
+    torch.cuda.synchronize()
+    O, LSE = f64(O), f64(LSE)
+    for b in range(B):
+        K, V = np.concatenate([c.K[0], c.K[b + 1]])[:, 0], np.concatenate([c.V[0], c.V[b + 1]])[:, 0]
+        _, rL, _, eL = srv.attend_prefix(q[b], c.K[0], c.V[0], c.K[b + 1], c.V[b + 1], 2, dh ** -0.5)
+        assert_within(LSE[b], rL, eL, "LSE")
+        for r in range(Hq):
+            s = K @ q[b, r, 0] * dh ** -0.5
+            A = np.exp(s - s.max())
+            A /= A.sum()
+            want, bound = A @ V, _weighted_bound(A, s, K, V, q[b, r, 0], dh)
+            assert_within(O[b, r, 0], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "O")
+
+
+def _weighted_bound(A, s, K, V, q, dh):
+    """Per group of 64 dims: what the weights times the group's largest values are off by
+    together, 2^-11 of each product, 2^-29 of the largest, as the header says; the scores'
+    errors; the sums'."""
+    size = np.repeat(np.abs(V.reshape(len(V), -1, 64)).max(-1), 64, -1)
+    ds = 132 * 2.0 ** -24 * dh ** -0.5 * (np.abs(K) @ np.abs(q))
+    rel = 2.0 ** -11 + 2 * (ds + 2.0 ** -20 * (1 + np.abs(s - s.max()) + abs(s.max()) / 4))
+    prod = A[:, None] * size
+    bound = (rel[:, None] * prod).sum(0) + len(V) * 2.0 ** -27 * prod.max(0)
+    return bound + 2 * (len(V) / 16 + 8) * 2.0 ** -23 * 2.2 * prod.sum(0)
 
 
 @pytest.mark.parametrize("B", [1, 33])

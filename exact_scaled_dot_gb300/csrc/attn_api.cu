@@ -1091,6 +1091,11 @@ int64_t evict_most_moves(int max_pages, int keep, int first, int recent) {
   return std::max<int64_t>(0, std::min<int64_t>(keep - first - recent, cap - keep));
 }
 
+size_t evict_lists_bytes(const attn_cache* c, int B, int max_pages, int keep, int first, int recent) {
+  return round256(static_cast<size_t>(B) * c->Hkv * 2 * evict_most_moves(max_pages, keep, first, recent) *
+                  sizeof(int32_t));
+}
+
 // Pointers of 32-bit arrays: not NULL, 4-byte aligned.
 int check_words(std::initializer_list<const void*> ptrs) {
   for (const void* p : ptrs) {
@@ -2114,8 +2119,9 @@ int attn_cache_weigh(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q
 size_t attn_cache_evict_workspace_bytes(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep,
                                         int32_t first, int32_t recent) {
   if (check_cache_evict(cache, B, max_pages, keep, first, recent) != ATTN_OK) return 0;
-  return round256(static_cast<size_t>(B) * cache->Hkv * 2 * evict_most_moves(max_pages, keep, first, recent) *
-                  sizeof(int32_t));
+  return evict_lists_bytes(cache, B, max_pages, keep, first, recent) +
+         round256(static_cast<size_t>(B) * cache->Hkv * sizeof(int32_t)) *
+             (evict_most_moves(max_pages, keep, first, recent) > 0 ? 1 : 0);
 }
 
 int attn_cache_evict(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep, int32_t first, int32_t recent,
@@ -2154,6 +2160,9 @@ int attn_cache_evict(const attn_cache* cache, int32_t B, int32_t max_pages, int3
   p.new_weights = new_weights;
   p.kept = kept;
   p.lists = static_cast<int32_t*>(workspace);
+  p.counts = need > 0 ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) +
+                                                   evict_lists_bytes(cache, B, max_pages, keep, first, recent))
+                      : nullptr;
   p.most_moves = static_cast<int32_t>(evict_most_moves(max_pages, keep, first, recent));
   p.status = status;
   const cudaError_t e = launch_cache_evict(p, static_cast<cudaStream_t>(stream));

@@ -13,9 +13,16 @@
 //
 // The smallest weight that stays is found by its digits, most significant
 // first: the weights as integers in their order, a histogram of 11, 11 and 10
-// bits of those that agree with the digits so far.  Then each warp counts, in a
-// stretch of its own, the tokens that make places free and those that move;
-// sums over the warps give every one its rank, without atomics on the lists.
+// bits of those that agree with the digits so far.  Then every thread decides on
+// runs of eight tokens, and sums over the threads give the tokens that make
+// places free and those that move their ranks, without atomics on the lists.
+//
+// Work: a CTA per sequence and head, with the weights as integers in its shared
+// memory where they fit.  It moves the tokens too; or, where there are few
+// sequences and heads and many tokens to move, a second kernel with several CTAs
+// for each does: one for the tokens between `front` and m, whose places the
+// newest take, and then the newest, the others for those from m on, in whose
+// way nothing is.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -28,9 +35,19 @@
 namespace esd {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kUnroll = 4;
+constexpr int kBins = 2048, kPasses = 3;
+constexpr int kRun = 8;                   // tokens that a thread decides on at a time
+constexpr int kUnroll = 4, kUnrollFirst = 8;
+// Threads of a CTA: few where there are many sequences and heads (four CTAs per
+// SM), many where there are not.  Weights kept in shared memory, beside histograms
+// of 24 KB: longer sequences are read from device memory each time.
+constexpr int kFewThreads = 256, kManyThreads = 1024;
+constexpr int kFewResident = 4, kManyResident = 1;
+constexpr int kFewWeights = 6144, kManyWeights = 45056;
+constexpr int kManyCtas = 304;            // up to here, many threads
+// The second kernel's CTAs per sequence and head and their threads, and the tokens
+// past the budget from which on it is worth a launch.
+constexpr int kMoveParts = 8, kMoveThreads = 256, kMoveLeast = 2048;
 
 // Weights as integers that order like them: NaN above all, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -40,44 +57,101 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A token of one head in the pool, in pieces: 16 bytes of codes or one 32-bit
-// word of a group.
-template <int DH, int DV>
-struct Token {
-  static constexpr int kK = DH / 32, kV = DV / 32, kKw = DH / kQuantGroup, kVw = DV / kQuantGroup;
-  static constexpr int kPieces = kK + kV + kKw + kVw;
-  // Byte of a piece in the block of a page and head, for the token at `at`.
-  __device__ static __forceinline__ int offset(int piece, int at) {
-    if (piece < kK) return off_k_codes() + at * (DH / 2) + 16 * piece;
-    piece -= kK;
-    if (piece < kV) return off_v_codes(DH) + at * (DV / 2) + 16 * piece;
-    piece -= kV;
-    if (piece < kKw) return off_k_words(DH, DV) + at * (4 * kKw) + 4 * piece;
-    return off_v_words(DH, DV) + at * (4 * kVw) + 4 * (piece - kKw);
-  }
+// The tokens get(0), get(1) .. of one head to the places put(0), put(1) ..,
+// by a CTA, kBatch at a time: first where each is and goes to, then the codes and
+// words of K and V, a 16-byte piece or a word a thread and load, so that
+// neighbouring tokens are neighbouring addresses.  Everything of a batch is
+// requested before any of it is stored; with `between`, after all threads have
+// it.  Tokens in or to a page that block_of does not know are left out.
+constexpr int kBatch = 256;
+struct Moving {
+  const uint8_t* src[kBatch];     // the block of the token's page, and of its new one
+  uint8_t* dst[kBatch];
+  int32_t at[kBatch];             // the places in the pages, the new one times 256
 };
+template <int DH, int DV, int THREADS, typename Block, typename Get, typename Put>
+__device__ __forceinline__ void copy_tokens(Moving& mv, int tid, int count, bool between, Block&& block_of, Get&& get,
+                                            Put&& put) {
+  // K codes, V codes, K words, V words: pieces of a token, and where they are.
+  constexpr int kPieces[4] = {DH / 32, DV / 32, DH / kQuantGroup, DV / kQuantGroup};
+  constexpr int kAt[4] = {off_k_codes(), off_v_codes(DH), off_k_words(DH, DV), off_v_words(DH, DV)};
+  constexpr int kToken[4] = {DH / 2, DV / 2, DH / kQuantGroup * 4, DV / kQuantGroup * 4};
+  constexpr int kMost = (kBatch * 4 + THREADS - 1) / THREADS;       // pieces of a thread, of each of the four
+  for (int k0 = 0; k0 < count; k0 += kBatch) {
+    const int here = count - k0 < kBatch ? count - k0 : kBatch;
+    if (tid < here) {
+      const int j = get(k0 + tid), to = put(k0 + tid);
+      const uint8_t* src = block_of(j);
+      mv.src[tid] = src;
+      mv.dst[tid] = src ? block_of(to) : nullptr;
+      mv.at[tid] = j % kPageTokens | to % kPageTokens << 8;
+    }
+    __syncthreads();
+    uint4 v[2][kMost];
+    uint32_t word[2][kMost];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) {
+        const int i = u * THREADS + tid, k = i / kPieces[f], piece = i % kPieces[f];
+        if (k < here && mv.dst[k]) {
+          const uint8_t* src = mv.src[k] + kAt[f] + piece * (f < 2 ? 16 : 4) + (mv.at[k] & 255) * kToken[f];
+          if (f < 2) v[f & 1][u] = *reinterpret_cast<const uint4*>(src);
+          else word[f & 1][u] = *reinterpret_cast<const uint32_t*>(src);
+        }
+      }
+    if (between) __syncthreads();
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) {
+        const int i = u * THREADS + tid, k = i / kPieces[f], piece = i % kPieces[f];
+        if (k < here && mv.dst[k]) {
+          uint8_t* dst = mv.dst[k] + kAt[f] + piece * (f < 2 ? 16 : 4) + (mv.at[k] >> 8) * kToken[f];
+          if (f < 2) *reinterpret_cast<uint4*>(dst) = v[f & 1][u];
+          else *reinterpret_cast<uint32_t*>(dst) = word[f & 1][u];
+        }
+      }
+    __syncthreads();
+  }
+}
 
+// The block of place j's page and head h in the pool, or nullptr (recorded).
 template <int DH, int DV>
-__global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_constant__ CacheEvictParams p) {
-  using T = Token<DH, DV>;
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t warp_sum[kWarps];
+__device__ __forceinline__ uint8_t* block_at(const CacheEvictParams& p, const int32_t* table, int h, int j) {
+  const int id = table[j / kPageTokens];
+  if (id < 0 || id >= p.pages) {
+    record_status(p.status, ATTN_ERR_PAGE);
+    return nullptr;
+  }
+  return p.pool + (static_cast<int64_t>(id) * p.Hkv + h) * page_head_bytes(DH, DV);
+}
+
+template <int DH, int DV, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == kFewThreads ? kFewResident : kManyResident)
+cache_evict_kernel(const __grid_constant__ CacheEvictParams p) {
+  constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+  extern __shared__ __align__(16) uint32_t smem_words[];
+  __shared__ __align__(16) uint32_t hist[kPasses][kBins];
   __shared__ uint32_t found[3];          // a digit, what is still to be taken at it, how many have it
-  __shared__ int warp_a[kWarps], warp_b[kWarps];
+  __shared__ int cells[2][kWarps];       // sums of each warp
   const uint32_t warp = warp_id(), lane = lane_id();
   const int tid = static_cast<int>(threadIdx.x);
-  const int b = static_cast<int>(blockIdx.x) / p.Hkv, h = static_cast<int>(blockIdx.x) - b * p.Hkv;
+  const int bh = static_cast<int>(blockIdx.x);
+  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int cap = p.max_pages * kPageTokens;
-  if (status_blocks(p.status)) return;
   int n = p.lengths[b];
-  if (n > cap && h == 0 && tid == 0) record_status(p.status, ATTN_ERR_PAGE);
+  const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages;
+  for (int i = tid; i < kPasses * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (__syncthreads_or(status_blocks(p.status))) return;
+  const bool report = h == 0 && tid == 0;
+  if (report && n > cap) record_status(p.status, ATTN_ERR_PAGE);
   n = n < 0 ? 0 : (n > cap ? cap : n);
   const int m = n < p.keep ? n : p.keep;
-  if (h == 0 && tid == 0) p.new_lengths[b] = m;
-  const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
-  const float* w = p.weights + bh * cap;
-  float* nw = p.new_weights + bh * cap;
-  int32_t* kept = p.kept ? p.kept + bh * p.keep : nullptr;
+  if (report) p.new_lengths[b] = m;
+  const float* w = p.weights + static_cast<int64_t>(bh) * cap;
+  float* nw = p.new_weights + static_cast<int64_t>(bh) * cap;
+  int32_t* kept = p.kept ? p.kept + static_cast<int64_t>(bh) * p.keep : nullptr;
   const bool in_place = nw == w;
   if (n <= p.keep) {
     for (int j = tid; j < cap; j += kThreads)
@@ -88,59 +162,83 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
   }
   const int c0 = p.first, c1 = n - p.recent;     // the candidates' places
   const int front = m - p.recent;                // places below it keep their token or take one from behind
+  const bool held = c1 - c0 <= p.held_weights;
+  uint32_t* keys = smem_words;
+  // A place that keeps its token (those that do not are written again below).
+  auto stay = [&](int j, float x) {
+    if (kept) kept[j] = j;
+    if (!in_place) nw[j] = x;
+  };
+  for (int j = tid; j < c0; j += kThreads) stay(j, in_place ? 0.f : w[j]);
 
   // ---- the smallest key that stays, and how many of its equals ----
   uint32_t least = 0xFFFFFFFFu, equals = 0u, had = 0u;
   uint32_t take = static_cast<uint32_t>(p.keep - p.first - p.recent);
-  if (take > 0) {
-    uint32_t above = 0u;
+  // (Also with nothing to take: the keys come into shared memory here.)
+  for (int j0 = c0; j0 < c1; j0 += kThreads * kUnrollFirst) {
+    float x[kUnrollFirst];
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int low = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0u;
-      __syncthreads();
+    for (int u = 0; u < kUnrollFirst; ++u) {
+      const int j = j0 + u * kThreads + tid;
+      x[u] = j < c1 ? w[j] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnrollFirst; ++u) {
+      const int j = j0 + u * kThreads + tid;
+      if (j < c1) {
+        const uint32_t key = order_key(x[u]);
+        if (held) keys[j - c0] = key;
+        atomicAdd(&hist[0][key >> 21], 1u);
+        if (j < front) stay(j, x[u]);
+      }
+    }
+  }
+  // (Up to a whole run: 0, which is below every weight's key.)
+  if (held && tid < kRun && (c1 - c0) % kRun + tid < kRun && (c1 - c0) % kRun != 0) keys[c1 - c0 + tid] = 0u;
+  uint32_t above = 0u;
+#pragma unroll 1
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int low = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    uint32_t* my_hist = hist[pass];
+    if (pass > 0 && held) {
+      for (int i = tid * 4; i < c1 - c0; i += kThreads * 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        const uint32_t four[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (four[u] >> (low + bits) == above) atomicAdd(&my_hist[(four[u] >> low) & ((1u << bits) - 1u)], 1u);
+      }
+    } else if (pass > 0) {
       for (int j0 = c0; j0 < c1; j0 += kThreads * kUnroll) {
-        float x[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           const int j = j0 + u * kThreads + tid;
-          x[u] = j < c1 ? w[j] : 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const uint32_t key = order_key(x[u]);
-          const bool in = j0 + u * kThreads + tid < c1 && (pass == 0 || key >> (low + bits) == above);
-          const uint32_t digit = (key >> low) & ((1u << bits) - 1u);
-          // Warps whose keys are all alike (weights that are still 0) add once.
-          const uint32_t who = __ballot_sync(0xffffffffu, in);
-          if (who == 0u) continue;
-          const uint32_t lead = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
-          if (__all_sync(0xffffffffu, !in || digit == lead)) {
-            if (lane == 0) atomicAdd(&hist[lead], static_cast<uint32_t>(__popc(who)));
-          } else if (in) {
-            atomicAdd(&hist[digit], 1u);
-          }
+          const uint32_t key = j >= c1 ? 0u : order_key(w[j]);
+          if (j < c1 && key >> (low + bits) == above) atomicAdd(&my_hist[(key >> low) & ((1u << bits) - 1u)], 1u);
         }
       }
-      __syncthreads();
-      // From the largest digit down: this thread's bins, and those above them.
-      constexpr int kOwn = kBins / kThreads;
-      uint32_t mine[kOwn], sum = 0u;
+    }
+    __syncthreads();
+    if (take == 0u) break;
+    // From the largest digit down: this thread's bins, and those above them.
+    constexpr int kOwn = kBins / kThreads;
+    uint32_t mine[kOwn];
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        mine[i] = hist[kBins - 1 - (tid * kOwn + i)];
-        sum += mine[i];
-      }
-      uint32_t incl = sum;
+    for (int i = 0; i < kOwn; ++i) mine[i] = my_hist[kBins - 1 - tid * kOwn - i];
+    uint32_t sum = 0u;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (static_cast<int>(lane) >= off) incl += v;
-      }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      uint32_t before = incl - sum;
-      for (uint32_t k = 0; k < warp; ++k) before += warp_sum[k];
+    for (int i = 0; i < kOwn; ++i) sum += mine[i];
+    uint32_t incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (static_cast<int>(lane) >= off) incl += v;
+    }
+    if (lane == 31) cells[pass & 1][warp] = static_cast<int>(incl);
+    __syncthreads();
+    uint32_t before =
+        incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? static_cast<uint32_t>(cells[pass & 1][lane]) : 0u);
+    if (before < take && take <= before + sum) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         if (before < take && take <= before + mine[i]) {
@@ -150,179 +248,222 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
         }
         before += mine[i];
       }
-      __syncthreads();
-      above = (above << bits) | found[0];
-      take = found[1];
-      had = found[2];
     }
+    __syncthreads();
+    above = (above << bits) | found[0];
+    take = found[1];
+    had = found[2];
     least = above;
     equals = take;
+    // (found is written again behind the next sync.)
   }
 
-  // ---- each warp's stretch of the candidates: ranks of equals, counts ----
-  const int per = ((c1 - c0 + kWarps * 32 - 1) / (kWarps * 32)) * 32;
-  const int s0 = c0 + static_cast<int>(warp) * per, s1 = s0 + per < c1 ? s0 + per : c1;
-  // Sum over the warps before this one (all warps call it).
-  auto before_me = [&](int mine, int* cell) {
-    if (lane == 0) cell[warp] = mine;
+  // ---- who stays: runs of eight tokens a thread, a byte of bits each ----
+  uint32_t turn = 0;
+  // Sum over the threads before this one, and over all.
+  auto before_me = [&](int mine, int& all) {
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (static_cast<int>(lane) >= off) incl += v;
+    }
+    turn ^= 1u;
+    if (lane == 31) cells[turn][warp] = incl;
     __syncthreads();
-    int sum = 0;
-    for (uint32_t k = 0; k < warp; ++k) sum += cell[k];
-    return sum;
+    const int theirs = lane < kWarps ? cells[turn][lane] : 0;
+    all = __reduce_add_sync(0xffffffffu, theirs);
+    return incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0);
   };
-  int eq0 = 0;
+  constexpr int kStep = kThreads * kRun;
+  const int steps = (c1 - c0 + kStep - 1) / kStep;
+  // The bits of a run's tokens that are there, that are above the smallest key, equal to it.
+  auto compare = [&](int j, uint32_t& above_it, uint32_t& equal) {
+    above_it = equal = 0u;
+    if (j >= c1) return;
+    uint32_t k[kRun];
+    if (held) {
+      const uint4 a = *reinterpret_cast<const uint4*>(keys + j - c0), c = *reinterpret_cast<const uint4*>(keys + j - c0 + 4);
+      k[0] = a.x, k[1] = a.y, k[2] = a.z, k[3] = a.w, k[4] = c.x, k[5] = c.y, k[6] = c.z, k[7] = c.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) k[i] = j + i < c1 ? order_key(w[j + i]) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      above_it |= k[i] > least ? 1u << i : 0u;
+      equal |= k[i] == least ? 1u << i : 0u;
+    }
+  };
+  // The bits of a run's places below `front`.
+  auto below_front = [&](int j) { return front - j >= kRun ? 0xFFu : front > j ? (1u << (front - j)) - 1u : 0u; };
   const bool some = equals < had;         // not all of the equals stay: the lowest places do
-  if (some) {
-    int c = 0;
-    for (int j = s0 + static_cast<int>(lane); j - static_cast<int>(lane) < s1; j += 32)
-      c += __popc(__ballot_sync(0xffffffffu, j < s1 && order_key(w[j]) == least));
-    eq0 = before_me(c, warp_a);
-    __syncthreads();
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  int eq = eq0;
-  // Whether the candidate at j stays; called for 32 of them in order.
-  auto stays = [&](int j) {
-    const uint32_t key = j < s1 ? order_key(w[j]) : 0u;
-    bool yes = j < s1 && key > least;
+  int eq = 0;                             // equals before the step
+  __syncthreads();                         // (the histograms have been read)
+  uint8_t* const bytes = reinterpret_cast<uint8_t*>(&hist[0][0]);
+  const bool held_bytes = steps * kThreads <= kPasses * kBins * 4;
+  // The run's tokens that stay; with `some`, called by all threads step by step.
+  auto decide = [&](int j) {
+    uint32_t yes, equal;
+    compare(j, yes, equal);
     if (equals > 0u) {
-      const bool is = j < s1 && key == least;
       if (some) {
-        const uint32_t all = __ballot_sync(0xffffffffu, is);
-        yes |= is && static_cast<uint32_t>(eq + __popc(all & below)) < equals;
-        eq += __popc(all);
-      } else {
-        yes |= is;
+        int all;
+        const int at = eq + before_me(__popc(equal), all);
+        eq += all;
+        const int left = static_cast<int>(equals) - at;
+        while (__popc(equal) > (left > 0 ? left : 0)) equal &= ~(0x80000000u >> __clz(equal));
       }
+      yes |= equal;
     }
     return yes;
   };
-  int holes = 0, moves = 0;
-  for (int j = s0 + static_cast<int>(lane); j - static_cast<int>(lane) < s1; j += 32) {
-    const bool yes = stays(j);
-    holes += __popc(__ballot_sync(0xffffffffu, j < s1 && !yes && j < front));
-    moves += __popc(__ballot_sync(0xffffffffu, yes && j >= front));
+  int moves = 0;
+  for (int i = 0; i < steps; ++i) {
+    const int j = c0 + i * kStep + tid * kRun;
+    const uint32_t yes = decide(j);
+    if (held_bytes) bytes[i * kThreads + tid] = static_cast<uint8_t>(yes);
+    const uint32_t low = below_front(j);
+    moves += __popc(yes & ~low);
   }
-  int hole = before_me(holes, warp_a), move = before_me(moves, warp_b);
-  int total = 0;
-  for (int k = 0; k < kWarps; ++k) total += warp_b[k];
-  int32_t* from = p.lists + bh * 2 * p.most_moves;      // tokens that move, and where to
+  int hole = 0, move = 0, total;            // before the step
+  before_me(moves, total);
+  int32_t* from = p.lists + static_cast<int64_t>(bh) * 2 * p.most_moves;      // tokens that move, and where to
   int32_t* to = from + p.most_moves;
-  eq = eq0;
-  for (int j = s0 + static_cast<int>(lane); j - static_cast<int>(lane) < s1; j += 32) {
-    const bool yes = stays(j);
-    const bool is_hole = j < s1 && !yes && j < front, is_move = yes && j >= front;
-    const uint32_t hs = __ballot_sync(0xffffffffu, is_hole), ms = __ballot_sync(0xffffffffu, is_move);
-    if (is_hole) to[hole + __popc(hs & below)] = j;
-    if (is_move) from[move + __popc(ms & below)] = j;
-    hole += __popc(hs);
-    move += __popc(ms);
-    if (yes && j < front) {
-      if (kept) kept[j] = j;
-      if (!in_place) nw[j] = w[j];
+  eq = 0;
+  for (int i = 0; i < steps; ++i) {
+    const int j = c0 + i * kStep + tid * kRun;
+    const uint32_t yes = held_bytes ? bytes[i * kThreads + tid] : decide(j);
+    const uint32_t there = c1 - j >= kRun ? 0xFFu : c1 > j ? (1u << (c1 - j)) - 1u : 0u, low = below_front(j);
+    uint32_t hs = ~yes & there & low, ms = yes & ~low;
+    int all;
+    const int at = before_me(__popc(hs) | __popc(ms) << 16, all);             // (8192 at most: both in a word)
+    int at_hole = hole + (at & 0xFFFF), at_move = move + (at >> 16);
+    while (hs) {
+      to[at_hole++] = j + __ffs(hs) - 1;
+      hs &= hs - 1u;
     }
-  }
-  for (int j = tid; j < c0; j += kThreads) {
-    if (kept) kept[j] = j;
-    if (!in_place) nw[j] = w[j];
+    while (ms) {
+      from[at_move++] = j + __ffs(ms) - 1;
+      ms &= ms - 1u;
+    }
+    hole += all & 0xFFFF;
+    move += all >> 16;
   }
   __syncthreads();
 
   // ---- the moves: sources at and behind `front`, places below it ----
-  const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages;
-  auto block_of = [&](int j) -> uint8_t* {       // the block of place j's page and this head, or nullptr
-    const int id = table[j / kPageTokens];
-    if (id < 0 || id >= p.pages) {
-      record_status(p.status, ATTN_ERR_PAGE);
-      return nullptr;
-    }
-    return p.pool + (static_cast<int64_t>(id) * p.Hkv + h) * page_head_bytes(DH, DV);
-  };
-  auto load_piece = [&](int j, int piece, uint4& v) {
-    const uint8_t* src = block_of(j);
-    if (!src) return false;
-    src += T::offset(piece, j % kPageTokens);
-    if (piece < T::kK + T::kV) v = *reinterpret_cast<const uint4*>(src);
-    else v.x = *reinterpret_cast<const uint32_t*>(src);
-    return true;
-  };
-  auto store_piece = [&](int j, int piece, uint4 v) {
-    uint8_t* dst = block_of(j);
-    if (!dst) return;
-    dst += T::offset(piece, j % kPageTokens);
-    if (piece < T::kK + T::kV) *reinterpret_cast<uint4*>(dst) = v;
-    else *reinterpret_cast<uint32_t*>(dst) = v.x;
-  };
+  auto block_of = [&](int j) { return block_at<DH, DV>(p, table, h, j); };
+  static_assert(sizeof(Moving) <= sizeof(hist), "over the histograms");
+  Moving& mv = *reinterpret_cast<Moving*>(&hist[0][0]);
   for (int i = tid; i < total; i += kThreads) {
-    if (kept) kept[to[i]] = from[i];
-    nw[to[i]] = w[from[i]];
+    const int j = from[i], to_j = to[i];
+    const float x = w[j];
+    if (kept) kept[to_j] = j;
+    nw[to_j] = x;
   }
-  const int64_t all_pieces = static_cast<int64_t>(total) * T::kPieces;
-  for (int64_t i0 = tid; i0 < all_pieces; i0 += kThreads * kUnroll) {
-    uint4 v[kUnroll];
-    int at[kUnroll], piece[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = i0 + u * kThreads;
-      at[u] = -1;
-      if (i < all_pieces) {
-        const int k = static_cast<int>(i / T::kPieces);
-        piece[u] = static_cast<int>(i - static_cast<int64_t>(k) * T::kPieces);
-        if (load_piece(from[k], piece[u], v[u])) at[u] = to[k];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (at[u] >= 0) store_piece(at[u], piece[u], v[u]);
+  if (p.counts) {
+    if (tid == 0) p.counts[bh] = total;
+  } else {
+    copy_tokens<DH, DV, kThreads>(mv, tid, total, false, block_of, [&](int k) { return from[k]; }, [&](int k) { return to[k]; });
   }
   // ---- the newest, in their order: all of a stretch read before it is written ----
   const int shift = n - m;
   __syncthreads();
   for (int i0 = 0; i0 < p.recent; i0 += kThreads) {
-    const int i = front + i0 + tid;
-    const bool here = i < m;
-    const float x = here ? w[i + shift] : 0.f;
-    __syncthreads();
-    if (here) {
-      nw[i] = x;
-      if (kept) kept[i] = i + shift;
+    const int j = front + i0 + tid;
+    const float x = j < m ? w[j + shift] : 0.f;
+    if (in_place) __syncthreads();
+    if (j < m) {
+      if (kept) kept[j] = j + shift;
+      nw[j] = x;
     }
   }
-  const int64_t tail_pieces = static_cast<int64_t>(p.recent) * T::kPieces;
-  for (int64_t i0 = 0; i0 < tail_pieces; i0 += kThreads * kUnroll) {
-    uint4 v[kUnroll];
-    int at[kUnroll], piece[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = i0 + u * kThreads + tid;
-      at[u] = -1;
-      if (i < tail_pieces) {
-        const int k = static_cast<int>(i / T::kPieces);
-        piece[u] = static_cast<int>(i - static_cast<int64_t>(k) * T::kPieces);
-        if (load_piece(front + k + shift, piece[u], v[u])) at[u] = front + k;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (at[u] >= 0) store_piece(at[u], piece[u], v[u]);
-  }
-  __syncthreads();
+  if (!p.counts)
+    copy_tokens<DH, DV, kThreads>(mv, tid, p.recent, true, block_of, [&](int k) { return front + shift + k; },
+                                  [&](int k) { return front + k; });
+  __syncthreads();                         // (in place: the newest tokens' weights have been read)
   for (int j = m + tid; j < cap; j += kThreads) nw[j] = 0.f;
 }
 
+// The second kernel: the tokens of the lists, and the newest.
 template <int DH, int DV>
-cudaError_t launch_t(const CacheEvictParams& p, cudaStream_t stream) {
-  cache_evict_kernel<DH, DV><<<static_cast<unsigned>(p.B * p.Hkv), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+__global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const __grid_constant__ CacheEvictParams p) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const int bh = static_cast<int>(blockIdx.x) / kMoveParts, part = static_cast<int>(blockIdx.x) % kMoveParts;
+  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int cap = p.max_pages * kPageTokens;
+  int n = p.lengths[b];
+  n = n < 0 ? 0 : (n > cap ? cap : n);
+  cudaGridDependencySynchronize();
+  if (n <= p.keep) return;
+  const int m = p.keep, front = m - p.recent, shift = n - m;
+  const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages;
+  const int32_t* from = p.lists + static_cast<int64_t>(bh) * 2 * p.most_moves;
+  const int32_t* to = from + p.most_moves;
+  __shared__ Moving mv;
+  auto block_of = [&](int j) { return block_at<DH, DV>(p, table, h, j); };
+  if (__syncthreads_or(status_blocks(p.status))) return;
+  const int total = p.counts[bh];
+  // The lists ascend: the first `near` tokens come from places below m.
+  int near = 0, above = total;
+  while (near < above) {
+    const int mid = (near + above) / 2;
+    if (from[mid] < m) near = mid + 1;
+    else above = mid;
+  }
+  if (part == 0) {
+    copy_tokens<DH, DV, kMoveThreads>(mv, tid, near, false, block_of, [&](int k) { return from[k]; },
+                                      [&](int k) { return to[k]; });
+    copy_tokens<DH, DV, kMoveThreads>(mv, tid, p.recent, true, block_of, [&](int k) { return front + shift + k; },
+                                      [&](int k) { return front + k; });
+  } else {
+    const int far = total - near, share = (far + kMoveParts - 2) / (kMoveParts - 1);
+    const int k0 = near + (part - 1) * share, k1 = k0 + share < total ? k0 + share : total;
+    copy_tokens<DH, DV, kMoveThreads>(mv, tid, k1 - k0, false, block_of, [&](int k) { return from[k0 + k]; },
+                                      [&](int k) { return to[k0 + k]; });
+  }
+}
+
+template <int DH, int DV, int THREADS>
+cudaError_t launch_t(CacheEvictParams p, cudaStream_t stream) {
+  const int most = THREADS == kFewThreads ? kFewWeights : kManyWeights;
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * kPageTokens;
+  p.held_weights = cap <= most ? static_cast<int32_t>(cap) : 0;
+  const int bytes = p.held_weights * 4;
+  auto kern = cache_evict_kernel<DH, DV, THREADS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  // (In two kernels: most_moves are the places past the budget, if not fewer are chosen.)
+  const bool two = THREADS == kManyThreads && p.most_moves >= kMoveLeast;
+  if (!two) p.counts = nullptr;
+  kern<<<static_cast<unsigned>(p.B * p.Hkv), THREADS, bytes, stream>>>(p);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || !two) return err;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * kMoveParts));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_move_kernel<DH, DV>, p);
+}
+
+template <int DH, int DV>
+cudaError_t launch_heads(const CacheEvictParams& p, cudaStream_t stream) {
+  return static_cast<int64_t>(p.B) * p.Hkv <= kManyCtas ? launch_t<DH, DV, kManyThreads>(p, stream)
+                                                        : launch_t<DH, DV, kFewThreads>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_evict(const CacheEvictParams& p, cudaStream_t stream) {
-  if (p.dh == 128 && p.dv == 128) return launch_t<128, 128>(p, stream);
-  if (p.dh == 64 && p.dv == 64) return launch_t<64, 64>(p, stream);
-  if (p.dh == 128 && p.dv == 64) return launch_t<128, 64>(p, stream);
+  if (p.dh == 128 && p.dv == 128) return launch_heads<128, 128>(p, stream);
+  if (p.dh == 64 && p.dv == 64) return launch_heads<64, 64>(p, stream);
+  if (p.dh == 128 && p.dv == 64) return launch_heads<128, 64>(p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -27,10 +27,9 @@ constexpr int kStages = 4;
 constexpr int kResident = kCacheWeighResident;     // CTAs per SM that the registers are held to
 constexpr int kMostGroups = 32;       // of eight query rows in shared memory: more pass over the pages again
 
-// What a row of Q brings: p = exp2(f s + add) for the keys below lim.
-struct RowTerms {
-  float f, add;
-  int lim, unused;
+// What two rows of Q bring, row r and r + 1: p = exp2(f s + add) for the keys below lim.
+struct __align__(16) RowTerms {
+  float f[2], add[2];
 };
 
 template <int DH, int DV>
@@ -43,9 +42,10 @@ struct WeighCfg {
   static constexpr int kOffBar = kRing;
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kOffRows = (kOffAbort + 8 + 127) / 128 * 128;
-  // Eight query rows: their terms and, of each group of 64 dims, two 16-byte
-  // chunks of fp16 fragments per lane.
-  static constexpr int kRowBytes = 8 * static_cast<int>(sizeof(RowTerms)) + GK * 2 * 32 * 16;
+  // Eight query rows: their terms, their limits and, of each group of 64 dims, two
+  // 16-byte chunks of fp16 fragments per lane.
+  static constexpr int kLimits = 4 * static_cast<int>(sizeof(RowTerms)), kFragments = kLimits + 64;
+  static constexpr int kRowBytes = kFragments + GK * 2 * 32 * 16;
   static_assert(kCodes % 16 == 0 && kWords % 16 == 0 && kStage % 16 == 0, "bulk copies");
   static int smem_bytes(int row_groups) { return kOffRows + row_groups * kRowBytes; }
 };
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
       if (mx > 0.f && mx < INFINITY) e = 14 - ilogbf(mx);
       e = e > 120 ? 120 : e;
       uint8_t* to = smem + C::kOffRows + nt * C::kRowBytes;
-      uint4* frag = reinterpret_cast<uint4*>(to + 8 * sizeof(RowTerms)) + lane;
+      uint4* frag = reinterpret_cast<uint4*>(to + C::kFragments) + lane;
 #pragma unroll
       for (int gk = 0; gk < GK; ++gk)
 #pragma unroll
@@ -150,16 +150,17 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
                                                __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
         }
       if (t == 0) {
-        RowTerms x;
-        x.f = fmaxf(p.scale_log2 * exp2_int(-e) * 512.0f, 0x1p-126f);
-        if (!(mx < INFINITY)) x.f = __uint_as_float(0x7FC00000u);
-        x.lim = r < R ? len - p.n_q + 1 + r % p.n_q : 0;
+        float fac = fmaxf(p.scale_log2 * exp2_int(-e) * 512.0f, 0x1p-126f);
+        if (!(mx < INFINITY)) fac = __uint_as_float(0x7FC00000u);
+        const int lim = r < R ? len - p.n_q + 1 + r % p.n_q : 0;
         const float lse = r < R ? p.LSE[row] : -INFINITY;
-        x.add = -lse * kLog2e;
+        float add = -lse * kLog2e;
         // Rows without a key, and none at all, add nothing.
-        if (x.lim <= 0 || lse == -INFINITY) x.f = 0x1p-126f, x.add = -INFINITY;
-        x.unused = 0;
-        reinterpret_cast<RowTerms*>(to)[g] = x;
+        if (lim <= 0 || lse == -INFINITY) fac = 0x1p-126f, add = -INFINITY;
+        RowTerms& x = reinterpret_cast<RowTerms*>(to)[g >> 1];
+        x.f[g & 1] = fac;
+        x.add[g & 1] = add;
+        reinterpret_cast<int*>(to + C::kLimits)[g] = lim;
       }
     }
     __syncthreads();
@@ -182,11 +183,14 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
         break;
       }
       const uint8_t* blk = ring_ptr + st * C::kStage;
-      // ---- the page's codes as fragments, (c - z) 2^-9 ----
-      uint32_t a[2][GK][4][4];
-      float sc[2][2][GK];
-#pragma unroll
+      const bool edge = key0 + kPageTokens > len - p.n_q + 1;   // some row does not see all of the page
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};                      // of the lane's rows: keys 8 i + g
+      // (A loop, so that the fragments of 16 keys are in registers and not of 32.)
+#pragma unroll 1
       for (int kb = 0; kb < 2; ++kb) {
+        // ---- 16 keys' codes as fragments, (c - z) 2^-9 ----
+        uint32_t a[GK][4][4];
+        float sa[GK], sb[GK];
         const int ka = 16 * kb + g;
         uint32_t pa[GK], pb[GK];
         lds_words<GK>(blk + C::kCodes + ka * (GK * 4), pa);
@@ -201,63 +205,61 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
           for (int step = 0; step < 4; ++step) {
             uint32_t xa = step < 2 ? wa.x : wa.y, xb = step < 2 ? wb.x : wb.y;
             if (step & 1) xa >>= 8, xb >>= 8;
-            a[kb][gk][step][0] = hfma2_bits(low_nibbles(xa), kTwo15, za);
-            a[kb][gk][step][1] = hfma2_bits(low_nibbles(xb), kTwo15, zb);
-            a[kb][gk][step][2] = hfma2_bits(high_nibbles(xa), kTwo11, za);
-            a[kb][gk][step][3] = hfma2_bits(high_nibbles(xb), kTwo11, zb);
+            a[gk][step][0] = hfma2_bits(low_nibbles(xa), kTwo15, za);
+            a[gk][step][1] = hfma2_bits(low_nibbles(xb), kTwo15, zb);
+            a[gk][step][2] = hfma2_bits(high_nibbles(xa), kTwo11, za);
+            a[gk][step][3] = hfma2_bits(high_nibbles(xb), kTwo11, zb);
           }
-          sc[kb][0][gk] = bf16_hi(pa[gk]);
-          sc[kb][1][gk] = bf16_hi(pb[gk]);
+          sa[gk] = bf16_hi(pa[gk]);
+          sb[gk] = bf16_hi(pb[gk]);
         }
-      }
-      __syncwarp();            // every lane has read the stage
-      if (issued < n) issue(st);
-      st = after(st);
-      parity ^= st == 0 ? 1u : 0u;
-
-      // ---- the sums over all rows, eight at a time ----
-      const bool edge = key0 + kPageTokens > len - p.n_q + 1;   // some row does not see all of the page
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};                      // of the lane's rows: keys 8 i + g
-      for (int nt = 0; nt < g_end; ++nt) {
-        const uint8_t* from = smem + C::kOffRows + nt * C::kRowBytes;
-        const uint4* frag = reinterpret_cast<const uint4*>(from + 8 * sizeof(RowTerms)) + lane;
-        const RowTerms x0 = reinterpret_cast<const RowTerms*>(from)[2 * t];
-        const RowTerms x1 = reinterpret_cast<const RowTerms*>(from)[2 * t + 1];
-        float s[2][4];
+        if (kb == 1) {
+          __syncwarp();          // every lane has read the stage
+          if (issued < n) issue(st);
+          st = after(st);
+          parity ^= st == 0 ? 1u : 0u;
+        }
+        // ---- the sums over all rows, eight at a time ----
+        float s0 = 0.f, s1 = 0.f;
+        for (int nt = 0; nt < g_end; ++nt) {
+          const uint8_t* from = smem + C::kOffRows + nt * C::kRowBytes;
+          const uint4* frag = reinterpret_cast<const uint4*>(from + C::kFragments) + lane;
+          const float4 x = *reinterpret_cast<const float4*>(from + t * sizeof(RowTerms));
+          float s[4];
 #pragma unroll
-        for (int gk = 0; gk < GK; ++gk) {
-          const uint4 q0 = frag[gk * 64], q1 = frag[gk * 64 + 32];
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
+          for (int gk = 0; gk < GK; ++gk) {
+            const uint4 q0 = frag[gk * 64], q1 = frag[gk * 64 + 32];
             float acc[4];
-            const uint32_t(*x)[4] = a[kb][gk];
-            mma_f16(acc, x[0][0], x[0][1], x[0][2], x[0][3], q0.x, q0.y, 0.f, 0.f, 0.f, 0.f);
-            mma_f16(acc, x[1][0], x[1][1], x[1][2], x[1][3], q0.z, q0.w);
-            mma_f16(acc, x[2][0], x[2][1], x[2][2], x[2][3], q1.x, q1.y);
-            mma_f16(acc, x[3][0], x[3][1], x[3][2], x[3][3], q1.z, q1.w);
-            const float sa = sc[kb][0][gk], sb = sc[kb][1][gk];
+            const uint32_t(*k)[4] = a[gk];
+            mma_f16(acc, k[0][0], k[0][1], k[0][2], k[0][3], q0.x, q0.y, 0.f, 0.f, 0.f, 0.f);
+            mma_f16(acc, k[1][0], k[1][1], k[1][2], k[1][3], q0.z, q0.w);
+            mma_f16(acc, k[2][0], k[2][1], k[2][2], k[2][3], q1.x, q1.y);
+            mma_f16(acc, k[3][0], k[3][1], k[3][2], k[3][3], q1.z, q1.w);
             if (gk == 0) {
-              fmul2(s[kb][0], s[kb][1], acc[0], acc[1], sa, sa);
-              fmul2(s[kb][2], s[kb][3], acc[2], acc[3], sb, sb);
+              fmul2(s[0], s[1], acc[0], acc[1], sa[gk], sa[gk]);
+              fmul2(s[2], s[3], acc[2], acc[3], sb[gk], sb[gk]);
             } else {
-              ffma2(s[kb][0], s[kb][1], acc[0], acc[1], sa, sa, s[kb][0], s[kb][1]);
-              ffma2(s[kb][2], s[kb][3], acc[2], acc[3], sb, sb, s[kb][2], s[kb][3]);
+              ffma2(s[0], s[1], acc[0], acc[1], sa[gk], sa[gk], s[0], s[1]);
+              ffma2(s[2], s[3], acc[2], acc[3], sb[gk], sb[gk], s[2], s[3]);
             }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float p0, p1;
-          ffma2(p0, p1, s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1], x0.f, x1.f, x0.add, x1.add);
-          p0 = fast_exp2(p0);
-          p1 = fast_exp2(p1);
-          if (edge) {
-            const int k = key0 + 8 * i + g;
-            p0 = k < x0.lim ? p0 : 0.f;
-            p1 = k < x1.lim ? p1 : 0.f;
+          for (int i = 0; i < 2; ++i) {
+            float p0, p1;
+            ffma2(p0, p1, s[2 * i], s[2 * i + 1], x.x, x.y, x.z, x.w);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            if (edge) {
+              const int k = key0 + 16 * kb + 8 * i + g;
+              const int2 lim = reinterpret_cast<const int2*>(from + C::kLimits)[t];
+              p0 = k < lim.x ? p0 : 0.f;
+              p1 = k < lim.y ? p1 : 0.f;
+            }
+            (i == 0 ? s0 : s1) += p0 + p1;
           }
-          sum[i] += p0 + p1;
         }
+        sum[0] = kb == 0 ? s0 : sum[0], sum[1] = kb == 0 ? s1 : sum[1];
+        sum[2] = s0, sum[3] = s1;
       }
       // Over the four lanes of a key; lane t ends with the keys 8 t + g.
       const float keep0 = t & 2 ? sum[2] : sum[0], keep1 = t & 2 ? sum[3] : sum[1];

@@ -415,7 +415,7 @@ struct PrefixMergeParams {
 
 // Attention weights added up per cached token (cache_weigh.cu): resident CTAs
 // per SM (fewer where a KV head has over 64 query rows).
-constexpr int kCacheWeighResident = 4;
+constexpr int kCacheWeighResident = 5;
 struct CacheWeighParams {
   int32_t B, Hkv, group, n_q, max_pages;
   int64_t pages;
@@ -444,6 +444,8 @@ struct CacheEvictParams {
   int32_t* kept;               // [B][Hkv][keep], or nullptr
   int32_t* lists;              // [B][Hkv][2][most_moves]: tokens that move, and their places
   int32_t most_moves;
+  int32_t* counts;             // [B][Hkv] tokens that move: workspace (nullptr: one kernel does all)
+  int32_t held_weights;        // weights kept in shared memory (by the launcher)
   unsigned int* status;
 };
 

@@ -10,10 +10,12 @@
 // and a key's weight is a sum over its row of the accumulators, in one order.
 //
 // Work: the pages of all sequences, end to end, are cut into equal ranges, one
-// per CTA of a KV head; its warps take every fourth page, K's codes and words of
-// which (half a page's block) two bulk copies bring into a ring of the warp's
-// own.  Q's fragments are kept in shared memory, a sequence at a time, so that
-// up to 256 query rows pass over a page that is read once.
+// per CTA of a KV head; its warps take every fourth page.  A lane's codes are what
+// it needs of 16 keys as fragments, so that they go from device memory to
+// registers; the warps of an SM hide one another's loads, and the page after the
+// next is on its way to the second-level cache.  Q's fragments are kept in shared
+// memory, a sequence at a time, so that up to 256 query rows pass over a page that
+// is read once.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -23,8 +25,8 @@ namespace esd {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStages = 4;
 constexpr int kResident = kCacheWeighResident;     // CTAs per SM that the registers are held to
+constexpr int kAhead = 1;             // pages that a warp has on their way to the second-level cache
 constexpr int kMostGroups = 32;       // of eight query rows in shared memory: more pass over the pages again
 
 // What two rows of Q bring, row r and r + 1: p = exp2(f s + add) for the keys below lim.
@@ -35,19 +37,13 @@ struct __align__(16) RowTerms {
 template <int DH, int DV>
 struct WeighCfg {
   static constexpr int GK = DH / kQuantGroup;
-  static constexpr int kCodes = kPageTokens * DH / 2, kWords = kPageTokens * GK * 4;
-  static constexpr int kStage = kCodes + kWords;
   static constexpr int kBlock = page_head_bytes(DH, DV);
-  static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kOffBar = kRing;
-  static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
-  static constexpr int kOffRows = (kOffAbort + 8 + 127) / 128 * 128;
+  static constexpr int kCodes = kPageTokens * DH / 2, kWords = kPageTokens * GK * 4;
   // Eight query rows: their terms, their limits and, of each group of 64 dims, two
   // 16-byte chunks of fp16 fragments per lane.
   static constexpr int kLimits = 4 * static_cast<int>(sizeof(RowTerms)), kFragments = kLimits + 64;
   static constexpr int kRowBytes = kFragments + GK * 2 * 32 * 16;
-  static_assert(kCodes % 16 == 0 && kWords % 16 == 0 && kStage % 16 == 0, "bulk copies");
-  static int smem_bytes(int row_groups) { return kOffRows + row_groups * kRowBytes; }
+  static int smem_bytes(int row_groups) { return row_groups * kRowBytes; }
 };
 
 template <int DH, int DV>
@@ -55,19 +51,10 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
   using C = WeighCfg<DH, DV>;
   constexpr int GK = C::GK;
   extern __shared__ __align__(128) uint8_t smem[];
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
+  if (__syncthreads_or(status_blocks(p.status))) return;
   const uint32_t warp = warp_id(), lane = lane_id();
   const int g = static_cast<int>(lane >> 2), t = static_cast<int>(lane & 3);
-  const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
-  const uint8_t* ring_ptr = smem + warp * kStages * C::kStage;
-  const uint32_t bars = smem_u32(smem) + C::kOffBar + warp * kStages * 8;
-  if (threadIdx.x == 0) *abort_flag = status_blocks(p.status) ? 2 : 0;
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
-    fence_mbar_init();
-  }
   const Ranges rg = page_ranges(p, lane);
-  __syncthreads();
 
   const int h = static_cast<int>(blockIdx.x) / p.ranges;
   const int range = static_cast<int>(blockIdx.x) - h * p.ranges;
@@ -77,9 +64,16 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
   int b = p.B, seq0 = 0;           // the sequence that `begin` lies in, and its first page's place
   if (begin < rg.total) b = sequence_at(p, begin, lane, seq0);
 
-  uint32_t st = 0, parity = 0;
-  auto after = [](uint32_t s) { return s + 1 == kStages ? 0u : s + 1; };
-  for (; b < p.B && *abort_flag != 2; ++b) {
+  // This head's blocks: codes and words of this lane's keys, and the line it prefetches.
+  const uint32_t page_stride = static_cast<uint32_t>(p.Hkv) * C::kBlock;
+  const uint8_t* const head = p.pool + static_cast<int64_t>(h) * C::kBlock;
+  const uint8_t* const codes_at = head + off_k_codes() + g * (DH / 2) + t * 8;
+  const uint8_t* const words_at = head + off_k_words(DH, DV) + g * (GK * 4);
+  constexpr int kLines = (C::kCodes + 127) / 128;
+  static_assert(kLines < 30, "a lane per line");
+  const uint8_t* const line_at = static_cast<int>(lane) < kLines ? head + 128 * lane : head + off_k_words(DH, DV) + 128 * (lane - kLines);
+  const bool has_line = static_cast<int>(lane) < kLines + (C::kWords + 127) / 128;
+  for (; b < p.B; ++b) {
     int len;
     const int npages = pages_of(p, b, len);
     if (seq0 >= end) break;
@@ -94,28 +88,25 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
     const int mine = (last - first - static_cast<int>(warp) + kWarps - 1) / kWarps;
     const int n = mine > 0 ? mine : 0;
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages + first + warp;
-    uint32_t bad = 0u;             // bit s: stage s stands for a page outside the pool
-    int issued = 0, ids = 0;
-    auto issue = [&](uint32_t s) {
-      if ((issued & 31) == 0) ids = issued + static_cast<int>(lane) < n ? table[(issued + static_cast<int>(lane)) * kWarps] : 0;
-      const int id = __shfl_sync(0xffffffffu, ids, issued & 31);
-      const bool in_pool = id >= 0 && id < p.pages;
-      bad = in_pool ? bad & ~(1u << s) : bad | (1u << s);
-      if (lane == 0) {
-        if (in_pool) {
-          const uint8_t* src = p.pool + (static_cast<int64_t>(id) * p.Hkv + h) * C::kBlock;
-          mbar_arrive_expect_tx(bars + 8 * s, C::kStage);
-          bulk_load(ring + s * C::kStage, src + off_k_codes(), C::kCodes, bars + 8 * s);
-          bulk_load(ring + s * C::kStage + C::kCodes, src + off_k_words(DH, DV), C::kWords, bars + 8 * s);
-        } else {
-          record_status(p.status, ATTN_ERR_PAGE);
-          mbar_arrive(bars + 8 * s);
-        }
+    // Page numbers of 32 of them, one per lane; -1 outside the pool.
+    auto numbers = [&](int from) {
+      const int at = from + static_cast<int>(lane);
+      int id = at < n ? table[at * kWarps] : 0;
+      if (id < 0 || id >= p.pages) {
+        record_status(p.status, ATTN_ERR_PAGE);
+        id = -1;
       }
-      ++issued;
+      return id;
     };
-    for (uint32_t s = st; issued < kStages && issued < n; s = after(s)) issue(s);
-
+    int ids = numbers(0), ids_next = 0;
+    // Page i of this warp's, the window of 32 that `done` is in or the next.
+    auto number = [&](int i, int done) {
+      return __shfl_sync(0xffffffffu, ((i ^ done) & ~31) ? ids_next : ids, i & 31);
+    };
+    auto prefetch = [&](int id) {
+      if (has_line && id >= 0)
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(line_at + static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_stride));
+    };
     // ---- Q's fragments and the rows' terms, eight rows a warp at a time ----
     // (dims of a lane as in the attention: k-step 4 gk + 2 w + e holds the dims
     // 64 gk + 16 t + 8 w + {2e, 2e+4} and {2e+1, 2e+5}.)
@@ -123,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
       const int r = 8 * (g0 + nt) + g;
       const int64_t row = (static_cast<int64_t>(b) * p.Hkv + h) * R + (r < R ? r : 0);
       const uint4* q = reinterpret_cast<const uint4*>(p.Q) + row * (DH / 8);
+      const float lse = r < R ? p.LSE[row] : -INFINITY;
       uint4 qv[GK][2];
       uint32_t m = 0u;
 #pragma unroll
@@ -139,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
       int e = 0;                                               // 2^14 <= mx 2^e < 2^15
       if (mx > 0.f && mx < INFINITY) e = 14 - ilogbf(mx);
       e = e > 120 ? 120 : e;
-      uint8_t* to = smem + C::kOffRows + nt * C::kRowBytes;
+      uint8_t* to = smem + nt * C::kRowBytes;
       uint4* frag = reinterpret_cast<uint4*>(to + C::kFragments) + lane;
 #pragma unroll
       for (int gk = 0; gk < GK; ++gk)
@@ -153,7 +145,6 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
         float fac = fmaxf(p.scale_log2 * exp2_int(-e) * 512.0f, 0x1p-126f);
         if (!(mx < INFINITY)) fac = __uint_as_float(0x7FC00000u);
         const int lim = r < R ? len - p.n_q + 1 + r % p.n_q : 0;
-        const float lse = r < R ? p.LSE[row] : -INFINITY;
         float add = -lse * kLog2e;
         // Rows without a key, and none at all, add nothing.
         if (lim <= 0 || lse == -INFINITY) fac = 0x1p-126f, add = -INFINITY;
@@ -163,42 +154,50 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
         reinterpret_cast<int*>(to + C::kLimits)[g] = lim;
       }
     }
+    for (int i = 0; i < kAhead && i < n; ++i) prefetch(number(i, 0));
     __syncthreads();
 
     float* const wrow = p.weights + (static_cast<int64_t>(b) * p.Hkv + h) * p.max_pages * kPageTokens;
     for (int done = 0; done < n; ++done) {
       const int key0 = (first + static_cast<int>(warp) + done * kWarps) * kPageTokens;
+      if ((done & 31) == 0) {
+        if (done > 0) ids = ids_next;
+        if (done + 32 < n) ids_next = numbers(done + 32);
+      }
+      const int id = number(done, done);
+      if (done + kAhead < n) prefetch(number(done + kAhead, done));
+      if (id < 0) continue;
+      const uint64_t page = static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_stride;
+      // ---- this lane's codes and words: keys 8 i + g ----
+      uint2 codes[4][GK];
+      uint32_t words[4][GK];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int gk = 0; gk < GK; ++gk)
+          codes[i][gk] = __ldg(reinterpret_cast<const uint2*>(codes_at + page + 8 * i * (DH / 2) + gk * 32));
+        if constexpr (GK == 2) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(words_at + page + 8 * i * 8));
+          words[i][0] = w.x, words[i][1] = w.y;
+        } else {
+          words[i][0] = __ldg(reinterpret_cast<const uint32_t*>(words_at + page + 8 * i * 4));
+        }
+      }
       // The key that the page's sums over rows end with in this lane.
       const int key = key0 + 8 * t + g;
-      const bool mine_here = key < len && !((bad >> st) & 1u);
+      const bool mine_here = key < len;
       const float was = mine_here ? wrow[key] : 0.f;
-      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, parity, abort_flag, p.wait_limit_ns))) {
-        // Every copy already in flight must land before the CTA can exit.
-        int no_abort = 0;
-        for (; done < issued; ++done) {
-          mbar_wait(bars + 8 * st, parity, &no_abort, p.wait_limit_ns);
-          st = after(st);
-          parity ^= st == 0 ? 1u : 0u;
-        }
-        break;
-      }
-      const uint8_t* blk = ring_ptr + st * C::kStage;
       const bool edge = key0 + kPageTokens > len - p.n_q + 1;   // some row does not see all of the page
       float sum[4] = {0.f, 0.f, 0.f, 0.f};                      // of the lane's rows: keys 8 i + g
-      // (A loop, so that the fragments of 16 keys are in registers and not of 32.)
-#pragma unroll 1
+#pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         // ---- 16 keys' codes as fragments, (c - z) 2^-9 ----
         uint32_t a[GK][4][4];
         float sa[GK], sb[GK];
-        const int ka = 16 * kb + g;
-        uint32_t pa[GK], pb[GK];
-        lds_words<GK>(blk + C::kCodes + ka * (GK * 4), pa);
-        lds_words<GK>(blk + C::kCodes + (ka + 8) * (GK * 4), pb);
+        const uint32_t(&pa)[GK] = words[2 * kb], (&pb)[GK] = words[2 * kb + 1];
 #pragma unroll
         for (int gk = 0; gk < GK; ++gk) {
-          const uint8_t* kc = blk + gk * 32 + t * 8;
-          const uint2 wa = lds64(kc + ka * (DH / 2)), wb = lds64(kc + (ka + 8) * (DH / 2));
+          const uint2 wa = codes[2 * kb][gk], wb = codes[2 * kb + 1][gk];
           const uint32_t za = hfma2_bits(__byte_perm(pa[gk], 0u, 0x4040), kMinusTwo15, 0u);
           const uint32_t zb = hfma2_bits(__byte_perm(pb[gk], 0u, 0x4040), kMinusTwo15, 0u);
 #pragma unroll
@@ -213,16 +212,10 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
           sa[gk] = bf16_hi(pa[gk]);
           sb[gk] = bf16_hi(pb[gk]);
         }
-        if (kb == 1) {
-          __syncwarp();          // every lane has read the stage
-          if (issued < n) issue(st);
-          st = after(st);
-          parity ^= st == 0 ? 1u : 0u;
-        }
         // ---- the sums over all rows, eight at a time ----
         float s0 = 0.f, s1 = 0.f;
         for (int nt = 0; nt < g_end; ++nt) {
-          const uint8_t* from = smem + C::kOffRows + nt * C::kRowBytes;
+          const uint8_t* from = smem + nt * C::kRowBytes;
           const uint4* frag = reinterpret_cast<const uint4*>(from + C::kFragments) + lane;
           const float4 x = *reinterpret_cast<const float4*>(from + t * sizeof(RowTerms));
           float s[4];
@@ -258,8 +251,7 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
             (i == 0 ? s0 : s1) += p0 + p1;
           }
         }
-        sum[0] = kb == 0 ? s0 : sum[0], sum[1] = kb == 0 ? s1 : sum[1];
-        sum[2] = s0, sum[3] = s1;
+        sum[2 * kb] = s0, sum[2 * kb + 1] = s1;
       }
       // Over the four lanes of a key; lane t ends with the keys 8 t + g.
       const float keep0 = t & 2 ? sum[2] : sum[0], keep1 = t & 2 ? sum[3] : sum[1];
@@ -270,10 +262,8 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
       if (mine_here) wrow[key] = was + all;
     }
     __syncthreads();           // the rows' fragments are free for the next ones
-    if (*abort_flag) break;
     }
   }
-  if (threadIdx.x == 0 && *abort_flag == 1) record_status(p.status, ATTN_ERR_TIMEOUT);
 }
 
 template <int DH, int DV>

@@ -415,7 +415,7 @@ struct PrefixMergeParams {
 
 // Attention weights added up per cached token (cache_weigh.cu): resident CTAs
 // per SM (fewer where a KV head has over 64 query rows).
-constexpr int kCacheWeighResident = 5;
+constexpr int kCacheWeighResident = 4;
 struct CacheWeighParams {
   int32_t B, Hkv, group, n_q, max_pages;
   int64_t pages;

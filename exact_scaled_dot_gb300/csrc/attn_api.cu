@@ -960,14 +960,15 @@ int cache_io(const attn_cache* c, int64_t tokens, const attn_strides* strides, c
 // and one launch less for the host (20 us a call from Python against 14).  Eight
 // warps against four: 1 sequence of 32 pages 7.4 us against 9.3, but 512 CTAs of
 // 16 pages 21.3 us against 13.1.
-constexpr int kFewPages = 32, kManyPages = 64;
+constexpr int kFewPages = 32, kManyPages = 64, kOwnPages = 32;
 struct DecodeCachePlan {
   int tile_rows, chunks, ranges;
   bool whole_seqs, wide;
   size_t opart_bytes, lpart_bytes, bytes;
 };
 
-DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int max_pages) {
+// merged: the caller merges parts anyway, so that ranges cost no launch.
+DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int max_pages, bool merged = false) {
   DecodeCachePlan d;
   const int64_t R = static_cast<int64_t>(Hq / c->Hkv) * n_q;
   d.tile_rows = R > 8 ? 16 : 8;
@@ -978,6 +979,7 @@ DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
   d.ranges = static_cast<int>(std::max<int64_t>(1, std::min(resident / tiles, most)));
   const int64_t ctas = tiles * B;
   d.whole_seqs = d.ranges == 1 || max_pages <= std::min<int64_t>(std::max<int64_t>(ctas, kFewPages), kManyPages);
+  if (merged) d.whole_seqs = d.ranges == 1 || max_pages <= kOwnPages;
   d.wide = d.whole_seqs && max_pages > kDecodeCacheWarps && ctas <= 152;
   if (d.whole_seqs) d.ranges = B;
   const size_t rows = static_cast<size_t>(tiles) * d.ranges * 2 * d.tile_rows;
@@ -1001,7 +1003,7 @@ struct PrefixCachePlan {
 
 PrefixCachePlan prefix_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int prefix_pages, int max_pages) {
   PrefixCachePlan d;
-  d.own = decode_cache_plan(c, B, Hq, n_q, max_pages);
+  d.own = decode_cache_plan(c, B, Hq, n_q, max_pages, true);
   const int64_t R = static_cast<int64_t>(B) * (Hq / c->Hkv) * n_q;
   d.row_tiles = R > kFewPrefixRows ? (R > 128 ? 2 : 1) : 0;
   d.tile_rows = d.row_tiles > 0 ? 128 * d.row_tiles : R > 8 ? 16 : 8;

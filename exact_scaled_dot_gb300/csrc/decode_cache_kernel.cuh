@@ -152,6 +152,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::kBlock;
   const uint8_t* ring_ptr = smem + warp * kStages * C::kBlock;
   const uint32_t bars = smem_u32(smem) + C::kOffBar + warp * kStages * 8;
+  if (KIND == kOwn) cudaTriggerProgrammaticLaunchCompletion();   // the prefix's kernel may start: it needs nothing of this one
   if (threadIdx.x == 0) *abort_flag = status_blocks(p.status) ? 2 : 0;
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
@@ -558,7 +559,7 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
         parity ^= st == 0 ? 1u : 0u;
       }
     }
-    if (!WHOLE && next0 >= end) cudaTriggerProgrammaticLaunchCompletion();   // the merge kernel may start (it waits for this grid)
+    if (KIND != kOwn && !WHOLE && next0 >= end) cudaTriggerProgrammaticLaunchCompletion();   // the merge kernel may start (it waits for this grid)
     __syncthreads();
 
     // ---- merge of the warps (over the ring) ----
@@ -638,6 +639,8 @@ decode_cache_kernel(const __grid_constant__ DecCacheParams p) {
     __syncthreads();
   }
   if (threadIdx.x == 0 && *abort_flag == 1) record_status(p.status, ATTN_ERR_TIMEOUT);
+  // The merge waits for this grid alone, and needs the own keys' too.
+  if (KIND == kShared) cudaGridDependencySynchronize();
 }
 
 }  // namespace

@@ -115,8 +115,18 @@ cudaError_t launch_part(const DecCacheParams& p, cudaStream_t stream) {
   auto kern = decode_cache_kernel<KIND, DH, DV, NT, WARPS, WHOLE>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.Hkv * p.chunks * p.ranges), C::kThreads, C::kSmemBytes, stream>>>(p);
-  return cudaGetLastError();
+  // The prefix starts while the own keys' kernel drains.
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.Hkv * p.chunks * p.ranges));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = KIND == kShared ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int DH, int DV>
@@ -135,11 +145,11 @@ cudaError_t launch_own(const DecCacheParams& p, cudaStream_t stream) {
 template <int DH, int DV>
 cudaError_t launch_all(const DecCacheParams& prefix, const PrefixTileParams& tile, const PrefixMergeParams& m,
                        cudaStream_t stream) {
-  cudaError_t e = tile.row_tiles > 0 ? launch_prefix_tile(DH, DV, tile, stream)
-                  : prefix.tile_rows == 8 ? launch_part<kShared, DH, DV, 1, kDecodeCacheWarps, false>(prefix, stream)
-                                        : launch_part<kShared, DH, DV, 2, kDecodeCacheWarps, false>(prefix, stream);
+  cudaError_t e = launch_own<DH, DV>(m.own, stream);
   if (e != cudaSuccess) return e;
-  e = launch_own<DH, DV>(m.own, stream);
+  e = tile.row_tiles > 0        ? launch_prefix_tile(DH, DV, tile, stream)
+      : prefix.tile_rows == 8 ? launch_part<kShared, DH, DV, 1, kDecodeCacheWarps, false>(prefix, stream)
+                              : launch_part<kShared, DH, DV, 2, kDecodeCacheWarps, false>(prefix, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -157,6 +157,12 @@ __device__ __forceinline__ uint4 times(uint4 x, uint32_t s) {
   return make_uint4(hmul2_bits(x.x, s), hmul2_bits(x.y, s), hmul2_bits(x.z, s), hmul2_bits(x.w, s));
 }
 
+// A row's power of two, from the bits of its largest magnitude: 2^14 <= max 2^e <
+// 2^15; less below 2^-106, and 0 for 0 and what is not finite.
+__device__ __forceinline__ int row_exponent(uint32_t bits) {
+  return bits == 0u || bits >= 0x7F800000u ? 0 : min(14 + 127 - static_cast<int>(bits >> 23), 120);
+}
+
 // K-major tile without a swizzle: 8 x 8 matrices of 128 bytes, the two of a
 // 16-element row next to each other.
 __device__ __forceinline__ SmemDesc plain_desc(uint32_t saddr) {
@@ -229,7 +235,10 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
   if (item == 0 && threadIdx.x == 0) *p.used = each > 0 ? (tiles + each - 1) / each : 0;
   const int t0 = split * each;
   const int n = tiles - t0 < each ? tiles - t0 : each;
-  if (n <= 0) return;          // (the whole CTA, before it owns anything)
+  if (n <= 0) {                // (the whole CTA, before it owns anything)
+    cudaGridDependencySynchronize();
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kRawStages; ++s) {
@@ -267,6 +276,62 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
   auto tile_of = [](int t, int k) { return NT == 2 ? k : 2 * k + t; };
   auto count_of = [&](int t) { return NT == 2 ? n : (n + 1 - t) / 2; };
   auto phase = [](int t, int stages) { return static_cast<uint32_t>((t / stages) & 1); };
+
+  // ---- Q: each row's power of two, its fp16 operands and sums, by warps 4-19 ----
+  // 16 bytes a lane, 128 / D rows of a warp at a time, put down swizzled; then a
+  // softmax thread takes its own row into tensor memory.
+  if (warp >= 4) {
+    constexpr int kLanes = DH / 8, kAt = 32 / kLanes, kWarpRows = 128 * NT / 16, kTimes = kWarpRows / kAt;
+    const int c = static_cast<int>(lane) % kLanes;
+    const int first = (static_cast<int>(warp) - 4) * kWarpRows + static_cast<int>(lane) / kLanes;
+    uint4 v[kTimes];
+    int of = (r0 + first) / p.per, rem = r0 + first - of * p.per;
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      const int64_t at = (static_cast<int64_t>(of) * p.Hkv + h) * p.per + rem;
+      v[i] = r0 + first + i * kAt < R ? reinterpret_cast<const uint4*>(p.Q)[at * kLanes + c] : make_uint4(0u, 0u, 0u, 0u);
+      rem += kAt;
+#pragma unroll
+      for (int o = 0; o < kAt; ++o)
+        if (rem >= p.per) rem -= p.per, ++of;
+    }
+    // (Each step for all rows, so that their shuffles overlap.)
+    uint32_t mb[kTimes];
+    float sum[kTimes];
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) mb[i] = __float_as_uint(bf16_absmax_value(bf16_absmax_fold(0u, v[i])));
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) mb[i] = max(mb[i], __shfl_xor_sync(0xffffffffu, mb[i], off));
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      const int rr = first + i * kAt, in_tile = rr & 127;
+      const float times_e = exp2_int(row_exponent(mb[i]));
+      const uint4 u = bf16x8_to_f16x8_scaled(v[i], times_e);
+      *reinterpret_cast<uint4*>(smem + C::kOffQ + rr / 128 * C::kQTile + c / 8 * (128 * 128) + in_tile * 128 +
+                                (((c & 7) ^ (rr & 7)) * 16)) =
+          make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                     __byte_perm(u.y, u.w, 0x7632));
+      const uint32_t xs[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int o = 0; o < 4; ++o) a = fmaf(bf16_lo(xs[o]), times_e, a), b = fmaf(bf16_hi(xs[o]), times_e, b);
+      sum[i] = a + b;
+    }
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
+    // Of each row: sum q_g and the largest magnitude.
+    float(*rows_of)[4] = reinterpret_cast<float(*)[4]>(smem + C::kOffState);
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      if ((c & 7) == 0) rows_of[first + i * kAt][c / 8] = sum[i];
+      if (c == 0) rows_of[first + i * kAt][2] = __uint_as_float(mb[i]);
+    }
+    fence_proxy_async_smem();
+  }
 
   if (warp < 4) {
     setmaxnreg_to<C::kRegsControl, C::kRegsLaunch>();
@@ -473,6 +538,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     }
   } else if (warp >= 12) {
     // ================= codes into operands =================
+    asm volatile("bar.arrive 2, 512;" ::: "memory");
     setmaxnreg_to<C::kRegsOperands, C::kRegsLaunch>();
     const int tid = static_cast<int>(threadIdx.x) - 384, w8 = static_cast<int>(warp) - 12;
     // The second half of the sums' inner step is 0.
@@ -553,77 +619,17 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     const bool valid = r < R;
     const uint32_t lane_base = (quad * 32u) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + 256 + 128 * t;
-    // ---- Q: each row's power of two, its fp16 operands and sums ----
-    // The warp's rows (with one row tile the streams share its rows) are read
-    // 16 bytes a lane, 128 / D rows at a time, and put down swizzled; then a
-    // thread takes its own row into tensor memory.
+    // ---- this thread's row of Q: its factor, its sums' operand, tensor memory ----
     float f;
     {
-      constexpr int kLanes = DH / 8, kAt = 32 / kLanes, kWarpRows = NT == 2 ? 32 : 16, kTimes = kWarpRows / kAt;
-      constexpr int kBatch = kTimes < 8 ? kTimes : 8;
-      uint8_t* tile = smem + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile;
-      // Of each row: sum q_g and the largest magnitude.
-      float(*rows_of)[4] = reinterpret_cast<float(*)[4]>(smem + C::kOffState) + (NT == 2 ? 128 * t : 0);
-      const int c = static_cast<int>(lane) % kLanes;
-      const int first = static_cast<int>(quad) * 32 + (NT == 2 ? 0 : 16 * t) + static_cast<int>(lane) / kLanes;
-#pragma unroll 1
-      for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int rr = tile0 + first + (i0 + i) * kAt;
-          const int of = rr < R ? rr / p.per : 0;
-          const int64_t at = (static_cast<int64_t>(of) * p.Hkv + h) * p.per + (rr < R ? rr - of * p.per : 0);
-          v[i] = rr < R ? reinterpret_cast<const uint4*>(p.Q)[at * kLanes + c] : make_uint4(0u, 0u, 0u, 0u);
-        }
-        // (Each step for all rows of the batch, so that their shuffles overlap.)
-        uint32_t mb[kBatch];
-        float sum[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) mb[i] = __float_as_uint(bf16_absmax_value(bf16_absmax_fold(0u, v[i])));
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1)
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) mb[i] = max(mb[i], __shfl_xor_sync(0xffffffffu, mb[i], off));
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int rr = first + (i0 + i) * kAt;
-          // 2^14 <= max 2^e < 2^15; below 2^-106, and for 0 and what is not finite, less.
-          const int ex = static_cast<int>(mb[i] >> 23) - 127;
-          const int e = ex == 128 || mb[i] == 0u ? 0 : min(14 - ex, 120);
-          const float times_e = exp2_int(e);
-          const uint4 u = bf16x8_to_f16x8_scaled(v[i], times_e);
-          *reinterpret_cast<uint4*>(tile + c / 8 * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) * 16)) =
-              make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
-                         __byte_perm(u.y, u.w, 0x7632));
-          const uint32_t xs[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          float a = 0.f, b = 0.f;
-#pragma unroll
-          for (int o = 0; o < 4; ++o) a = fmaf(bf16_lo(xs[o]), times_e, a), b = fmaf(bf16_hi(xs[o]), times_e, b);
-          sum[i] = a + b;
-        }
-#pragma unroll
-        for (int off = 4; off > 0; off >>= 1)
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if ((c & 7) == 0) rows_of[first + (i0 + i) * kAt][c / 8] = sum[i];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if (c == 0) rows_of[first + (i0 + i) * kAt][2] = __uint_as_float(mb[i]);
-      }
-      fence_proxy_async_smem();
-      if (NT == 1) named_bar_sync(1, 256);
-      else __syncwarp();
+      named_bar_sync(2, 512);                              // (all rows are there)
+      const uint8_t* tile = smem + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile;
       {
-        const float4 of = *reinterpret_cast<const float4*>(rows_of[row]);
+        const float4 of = reinterpret_cast<const float4*>(smem + C::kOffState)[(NT == 2 ? 128 * t : 0) + row];
         const uint32_t mb = __float_as_uint(of.z);
-        const int ex = static_cast<int>(mb >> 23) - 127;
-        const int e = ex == 128 || mb == 0u ? 0 : min(14 - ex, 120);
         // (Not 0, which a masked -inf must not meet; NaN for a row that is not finite.)
-        f = fmaxf(p.scale_log2 * exp2_int(-e), 0x1p-126f);
-        if (ex == 128) f = __uint_as_float(0x7FC00000u);
+        f = fmaxf(p.scale_log2 * exp2_int(-row_exponent(mb)), 0x1p-126f);
+        if (mb >= 0x7F800000u) f = __uint_as_float(0x7FC00000u);
         if (NT == 2 || t == 0) {                           // sum q_g 2^-6: three fp16 numbers of each group
           uint32_t h16[6] = {0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
@@ -857,6 +863,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
       mbar_arrive(bar(C::kBarP + t));
     }
     if (folded) l_sum *= exp2_int(-kFastBits);
+    cudaTriggerProgrammaticLaunchCompletion();     // the merge kernel may start (it waits for this grid)
     if (ok && mine > 0) ok = wait_all(C::kBarPV + t, static_cast<uint32_t>((mine - 1) & 1));
     tc_fence_after_sync();
     if (seen == 0u) l_sum = 0.f;
@@ -937,6 +944,9 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort_flag == 1) record_status(p.status, ATTN_ERR_TIMEOUT);
+  // The sequences' own keys, whose kernel may still run, are the merge's too: it
+  // waits for this grid alone.
+  cudaGridDependencySynchronize();
 }
 
 template <int DH, int DV, int NT>
@@ -945,8 +955,17 @@ cudaError_t launch_t(const PrefixTileParams& p, cudaStream_t stream) {
   auto kern = prefix_tile_kernel<DH, DV, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.Hkv * p.row_blocks * p.splits), C::kThreads, C::kSmemBytes, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.Hkv * p.row_blocks * p.splits));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int DH, int DV>

@@ -991,9 +991,18 @@ DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
 
 // How attn_fwd_prefix_cache divides the work: the sequences' own keys as
 // attn_fwd_decode_cache does, and the prefix among row tiles (of the rows of
-// the whole batch) and ranges of its pages.
-constexpr int kFewPrefixRows = 16;
-constexpr int kMinPrefixTilePages = 4;
+// the whole batch) and ranges of its pages.  The rows are tiles of 8 or 16 on
+// warps (decode_cache_kernel.cuh), or of 128 on the tensor core's (prefix_tile.cu),
+// whose CTA takes longer to begin and to end: from 65 rows a head on, where the
+// warps would pass over 8192 pages (one for each head, page and 16 rows), all
+// counted.  Measured, warps against tiles, us a call (widths 128, 32 own keys):
+//   8 KV heads, prefix 2048:  64 rows 16.7, 19.3; 128 rows 18.8, 20.2; 256 rows 24.7, 22.3
+//   8 KV heads, prefix 16384: 64 rows 31.2, 33.7; 128 rows 46.9, 34.5; 256 rows 90.5, 39.8
+//   1 KV head, prefix 16384:  128 rows 22.4, 22.7; 256 rows 23.5, 25.3; 512 rows 30.4, 29.5
+// and at least eight pages a tile's range (four: 28.3 and 33.9 us in the last line).
+constexpr int kPrefixTileRows = 65;
+constexpr int64_t kPrefixTilePasses = 8192;
+constexpr int kMinPrefixTilePages = 8;
 struct PrefixCachePlan {
   DecodeCachePlan own;
   int row_tiles;               // of prefix_tile.cu, or 0
@@ -1005,7 +1014,8 @@ PrefixCachePlan prefix_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
   PrefixCachePlan d;
   d.own = decode_cache_plan(c, B, Hq, n_q, max_pages, true);
   const int64_t R = static_cast<int64_t>(B) * (Hq / c->Hkv) * n_q;
-  d.row_tiles = R > kFewPrefixRows ? (R > 128 ? 2 : 1) : 0;
+  const bool tile = R >= kPrefixTileRows && c->Hkv * ((R + 15) / 16) * prefix_pages >= kPrefixTilePasses;
+  d.row_tiles = tile ? (R > 128 ? 2 : 1) : 0;
   d.tile_rows = d.row_tiles > 0 ? 128 * d.row_tiles : R > 8 ? 16 : 8;
   d.chunks = static_cast<int>((R + d.tile_rows - 1) / d.tile_rows);
   const int64_t tiles = static_cast<int64_t>(c->Hkv) * d.chunks;
@@ -2121,9 +2131,9 @@ int attn_cache_weigh(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q
 size_t attn_cache_evict_workspace_bytes(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep,
                                         int32_t first, int32_t recent) {
   if (check_cache_evict(cache, B, max_pages, keep, first, recent) != ATTN_OK) return 0;
+  if (evict_most_moves(max_pages, keep, first, recent) <= kEvictFewMoves) return 0;
   return evict_lists_bytes(cache, B, max_pages, keep, first, recent) +
-         round256(static_cast<size_t>(B) * cache->Hkv * sizeof(int32_t)) *
-             (evict_most_moves(max_pages, keep, first, recent) > 0 ? 1 : 0);
+         round256(static_cast<size_t>(B) * cache->Hkv * sizeof(int32_t));
 }
 
 int attn_cache_evict(const attn_cache* cache, int32_t B, int32_t max_pages, int32_t keep, int32_t first, int32_t recent,
@@ -2161,7 +2171,7 @@ int attn_cache_evict(const attn_cache* cache, int32_t B, int32_t max_pages, int3
   p.new_lengths = new_lengths;
   p.new_weights = new_weights;
   p.kept = kept;
-  p.lists = static_cast<int32_t*>(workspace);
+  p.lists = need > 0 ? static_cast<int32_t*>(workspace) : nullptr;
   p.counts = need > 0 ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) +
                                                    evict_lists_bytes(cache, B, max_pages, keep, first, recent))
                       : nullptr;

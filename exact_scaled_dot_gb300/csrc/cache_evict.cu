@@ -328,7 +328,9 @@ cache_evict_kernel(const __grid_constant__ CacheEvictParams p) {
   }
   int hole = 0, move = 0, total;            // before the step
   before_me(moves, total);
-  int32_t* from = p.lists + static_cast<int64_t>(bh) * 2 * p.most_moves;      // tokens that move, and where to
+  // Tokens that move, and where to: in shared memory where they are few.
+  int32_t* from = p.lists ? p.lists + static_cast<int64_t>(bh) * 2 * p.most_moves
+                          : reinterpret_cast<int32_t*>(smem_words) + p.held_weights;
   int32_t* to = from + p.most_moves;
   eq = 0;
   for (int i = 0; i < steps; ++i) {
@@ -430,9 +432,10 @@ cudaError_t launch_t(CacheEvictParams p, cudaStream_t stream) {
   const int most = THREADS == kFewThreads ? kFewWeights : kManyWeights;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * kPageTokens;
   p.held_weights = cap <= most ? static_cast<int32_t>(cap) : 0;
-  const int bytes = p.held_weights * 4;
+  const int bytes = (p.held_weights + (p.lists ? 0 : 2 * p.most_moves)) * 4;
   auto kern = cache_evict_kernel<DH, DV, THREADS>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), (most + 2 * kEvictFewMoves) * 4, done);
   if (e != cudaSuccess) return e;
   // (In two kernels: most_moves are the places past the budget, if not fewer are chosen.)
   const bool two = THREADS == kManyThreads && p.most_moves >= kMoveLeast;

@@ -272,7 +272,8 @@ cudaError_t launch_t(const CacheWeighParams& p, cudaStream_t stream) {
   const int groups = (p.group * p.n_q + 7) / 8;
   const int bytes = C::smem_bytes(groups < kMostGroups ? groups : kMostGroups);
   auto kern = cache_weigh_kernel<DH, DV>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::smem_bytes(kMostGroups), done);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(p.Hkv * p.ranges), kThreads, bytes, stream>>>(p);
   return cudaGetLastError();

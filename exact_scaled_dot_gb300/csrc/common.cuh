@@ -14,6 +14,7 @@
 // makes whole-tile classification a pair of comparisons.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 
@@ -431,7 +432,9 @@ struct CacheWeighParams {
   unsigned int* status;
 };
 
-// Tokens chosen by their weights and moved to the front (cache_evict.cu).
+// Tokens chosen by their weights and moved to the front (cache_evict.cu).  Up to
+// kEvictFewMoves of a head that may move, their lists are in shared memory.
+constexpr int kEvictFewMoves = 1024;
 struct CacheEvictParams {
   int32_t B, Hkv, dh, dv, max_pages, keep, first, recent;
   int64_t pages;
@@ -442,7 +445,7 @@ struct CacheEvictParams {
   int32_t* new_lengths;        // [B]
   float* new_weights;          // fp32 [B][Hkv][32 max_pages], may be weights
   int32_t* kept;               // [B][Hkv][keep], or nullptr
-  int32_t* lists;              // [B][Hkv][2][most_moves]: tokens that move, and their places
+  int32_t* lists;              // [B][Hkv][2][most_moves]: tokens that move, and their places (or nullptr)
   int32_t most_moves;
   int32_t* counts;             // [B][Hkv] tokens that move: workspace (nullptr: one kernel does all)
   int32_t held_weights;        // weights kept in shared memory (by the launcher)
@@ -451,6 +454,20 @@ struct CacheEvictParams {
 
 // Default limit of every bounded wait inside the kernels.
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s
+
+// Let a kernel use up to `bytes` of dynamic shared memory on the current device:
+// once per device and kernel (`done`: the devices it was done on), since the call
+// costs the host about as much as a launch's arguments.
+inline cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Kernel launchers (defined next to their kernels).
 cudaError_t launch_attn_fwd(int dh, int dv, const CUtensorMap& tmQ, const CUtensorMap& tmK,

@@ -113,7 +113,8 @@ template <CacheKind KIND, int DH, int DV, int NT, int WARPS, bool WHOLE>
 cudaError_t launch_part(const DecCacheParams& p, cudaStream_t stream) {
   using C = CacheCfg<DH, DV, NT, WARPS, WHOLE>;
   auto kern = decode_cache_kernel<KIND, DH, DV, NT, WARPS, WHOLE>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   // The prefix starts while the own keys' kernel drains.
   cudaLaunchAttribute early{};

@@ -953,7 +953,8 @@ template <int DH, int DV, int NT>
 cudaError_t launch_t(const PrefixTileParams& p, cudaStream_t stream) {
   using C = TileCfg<DH, DV, NT>;
   auto kern = prefix_tile_kernel<DH, DV, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

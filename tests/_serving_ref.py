@@ -38,6 +38,15 @@ class Paged:
         return self.table[b][j // PAGE].astype(np.int64) * PAGE + j % PAGE
 
 
+def behind(rng, prefix, lengths, **kw):
+    """A cache whose first sequence is `prefix` (a Paged of one), and which has others of `lengths`."""
+    c = Paged(rng, prefix.Hkv, prefix.dh, prefix.dv, lengths, **kw)
+    c.pool = np.concatenate([c.pool, prefix.pool])
+    c.prefix_table = (prefix.table[0] + (len(c.pool) - len(prefix.pool))).astype(np.int32)
+    c.K, c.V, c.lengths = prefix.K + c.K, prefix.V + c.V, prefix.lengths + c.lengths
+    return c
+
+
 def attend_prefix(q, Kp, Vp, K, V, length, scale):
     """q [Hq, n_q, dh] over the prefix and `length` own keys: O, LSE and bounds on
     the kernel's error, as _qk_cache_ref.attend has them.  The parts are put

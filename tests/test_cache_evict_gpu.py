@@ -192,7 +192,9 @@ def test_serving_loop(B):
     lengths = [int(x) for x in rng.integers(30, keep + 1, B)]
     c = srv.Paged(rng, Hkv, dh, dv, [prefix] + lengths, max_pages=4)
     cache = esd.QuantCache(_dev(c.pool), dh, dv)
-    ptab, plen, table = _dev(c.table[0]), _dev(np.array([prefix], np.int32)), _dev(c.table[1:])
+    # (as wide as a prefix that is worked on in tiles of 128 rows, where there are many rows)
+    ptab = _dev(np.concatenate([c.table[0], np.zeros(220 if B > 30 else 0, np.int32)]))
+    plen, table = _dev(np.array([prefix], np.int32)), _dev(c.table[1:])
     n = _dev(np.array(lengths, np.int32))
     n2, wts = torch.empty_like(n), torch.zeros((B, Hkv, 4 * PAGE), device="cuda")
     Q = torch.empty((B, Hq, nq, dh), dtype=torch.bfloat16, device="cuda")

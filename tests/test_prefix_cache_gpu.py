@@ -33,15 +33,34 @@ def _queries(rng, B, Hq, nq, dh, scale=1.0):
     return bf16(rng.normal(size=(B, Hq, nq, dh)) * scale)
 
 
-def _case(seed, B, Hq, Hkv, nq, dh, dv, prefix, lengths, spread=0.0, more_pages=0):
-    """The cache with the prefix as its first row, Q, and what the library gets."""
+def _tile_pages(B, Hq, Hkv, nq):
+    """Pages of a prefix table from which on a prefix is worked on in tiles of 128 rows."""
+    return -(-8192 // (Hkv * -(-B * (Hq // Hkv) * nq // 16)))
+
+
+def _prefix_table(table, B, Hq, Hkv, nq, tiles):
+    """The prefix's table, its width what the rule on sizes goes by (what is behind the prefix is not read)."""
+    rows, width = B * (Hq // Hkv) * nq, len(table)
+    if tiles:
+        assert rows > 64
+        width = max(width, _tile_pages(B, Hq, Hkv, nq))
+    else:
+        assert rows <= 64 or width < _tile_pages(B, Hq, Hkv, nq)
+    return np.concatenate([table, np.full(width - len(table), -7, np.int32)])
+
+
+def _case(seed, B, Hq, Hkv, nq, dh, dv, prefix, lengths, spread=0.0, more_pages=0, tiles=None):
+    """The cache with the prefix as its first row, Q, and what the library gets.  tiles: whether
+    the prefix goes to the tensor core's tiles (None: where there are rows for it)."""
+    tiles = B * (Hq // Hkv) * nq > 64 if tiles is None else tiles
     rng = np.random.default_rng(seed)
     lengths = [lengths] * B if isinstance(lengths, int) else lengths
     wide = max(1, max(-(-n // PAGE) for n in [prefix] + lengths)) + more_pages
     c = srv.Paged(rng, Hkv, dh, dv, [prefix] + lengths, max_pages=wide, spread=spread)
     q = _queries(rng, B, Hq, nq, dh)
     own = max(1, max(-(-n // PAGE) for n in lengths)) + more_pages
-    args = dict(prefix_table=_dev(c.table[0]), prefix_length=_dev(np.array([prefix], np.int32)),
+    args = dict(prefix_table=_dev(_prefix_table(c.table[0], B, Hq, Hkv, nq, tiles)),
+                prefix_length=_dev(np.array([prefix], np.int32)),
                 page_table=_dev(c.table[1:, :own]), lengths=_dev(np.array(lengths, np.int32)))
     return c, q, args
 
@@ -77,17 +96,19 @@ def _run(c, q, args, dh, dv, **kw):
     (2, 32, 1, 16, 129, [16, 50]),                        # 1024 rows of one head
 ])
 def test_against_64_bits(B, Hq, Hkv, nq, prefix, lengths, dh, dv):
-    c, q, args = _case(B * 100 + prefix, B, Hq, Hkv, nq, dh, dv, prefix, lengths)
-    O, LSE = _run(c, q, args, dh, dv)
-    torch.cuda.synchronize()
-    _check(c, q, O, LSE, nq, dh)
+    for tiles in (False, True) if B * (Hq // Hkv) * nq > 64 else (False,):
+        c, q, args = _case(B * 100 + prefix, B, Hq, Hkv, nq, dh, dv, prefix, lengths, tiles=tiles)
+        O, LSE = _run(c, q, args, dh, dv)
+        torch.cuda.synchronize()
+        _check(c, q, O, LSE, nq, dh)
 
 
 @pytest.mark.parametrize("prefix", [2047, 2048, 4100])
-def test_long_prefix(prefix):
+@pytest.mark.parametrize("B,dv", [(3, 128), (19, 128), (19, 64)])
+def test_long_prefix(prefix, B, dv):
     """Many splits of the prefix, long own sequences that several CTAs share, wide tables."""
-    c, q, args = _case(prefix, 3, 8, 2, 2, 128, 128, prefix, [2, 1500, 3000 - 7], more_pages=90)
-    O, LSE = _run(c, q, args, 128, 128)
+    c, q, args = _case(prefix, B, 8, 2, 2, 128, dv, prefix, [2, 1500, 2993] + [40] * (B - 3), more_pages=90)
+    O, LSE = _run(c, q, args, 128, dv)
     torch.cuda.synchronize()
     _check(c, q, O, LSE, 2, 128)
 
@@ -123,41 +144,71 @@ def test_values_of_very_different_sizes(B, spread):
             assert_within(O[b, r, 0], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "O")
 
 
-@pytest.mark.parametrize("Hq", [4, 16])
+def _many_heads(seed, B, group, dh, dv, prefix, lengths):
+    """19 KV heads: eight ranges of the prefix, each of many of its tiles."""
+    rng = np.random.default_rng(seed)
+    p = srv.Paged(rng, 19, dh, dv, [prefix])
+    return rng, p, lambda: srv.behind(rng, p, lengths), _queries(rng, B, 19 * group, 1, dh)
+
+
+def _many_args(c, B, group):
+    return dict(prefix_table=_dev(_prefix_table(c.prefix_table, B, 19 * group, 19, 1, True)),
+                prefix_length=_dev(np.array(c.lengths[:1], np.int32)), page_table=_dev(c.table),
+                lengths=_dev(np.array(c.lengths[1:], np.int32)))
+
+
+@pytest.mark.parametrize("dh,dv", [(64, 64), (128, 128), (128, 64)])
+@pytest.mark.parametrize("B,group", [(40, 2), (40, 4), (20, 5)])
+@pytest.mark.parametrize("prefix", [1100, 4100])
+def test_many_tiles_in_a_range(B, group, prefix, dh, dv):
+    """Rows of 80 (one row tile), 160 and 100 a head; ranges of two to nine tiles of 64 keys."""
+    _, _, cache, q = _many_heads(prefix + B, B, group, dh, dv, prefix, [1 + i for i in range(B)])
+    c = cache()
+    O, LSE = _run(c, q, _many_args(c, B, group), dh, dv)
+    torch.cuda.synchronize()
+    O, LSE = f64(O), f64(LSE)
+    for b in (0, B // 2, B - 1):
+        for h in (0, 7, 18):
+            at = slice(h * group, (h + 1) * group)
+            rO, rL, eO, eL = srv.attend_prefix(q[b, at], c.K[0][:, h:h + 1], c.V[0][:, h:h + 1], c.K[b + 1][:, h:h + 1],
+                                               c.V[b + 1][:, h:h + 1], c.lengths[b + 1], dh ** -0.5)
+            assert_within(O[b, at], rO, eO + 2.0 ** -8 * (np.abs(rO) + eO), "O")
+            assert_within(LSE[b, at], rL, eL, "LSE")
+
+
+@pytest.mark.parametrize("group", [4, 16])
 @pytest.mark.parametrize("at", [40, 700])
 @pytest.mark.parametrize("of", ["k", "v", "both"])
-def test_scales_that_change_along_the_prefix(Hq, at, of):
+def test_scales_that_change_along_the_prefix(group, at, of):
     """Keys or values whose scales leave what went before, from one token on: some tiles are
     taken with their scales in the operands, the others with the scales beside them."""
     dh = dv = 128
-    rng = np.random.default_rng(at)
-    B, Hkv, prefix = 24, 1, 1200
-    c = srv.Paged(rng, Hkv, dh, dv, [prefix] + [2] * B)
+    B, prefix = 24, 2300
+    rng, p, cache, q = _many_heads(at, B, group, dh, dv, prefix, [2] * B)
     size = np.where(np.arange(prefix) < at, 1.0, np.exp2(rng.integers(-15, 12, prefix)))[:, None, None]
-    K, V = rng.normal(size=(prefix, Hkv, dh)), rng.normal(size=(prefix, Hkv, dv))
+    K, V = rng.normal(size=(prefix, 19, dh)), rng.normal(size=(prefix, 19, dv))
     # (large keys would leave one score each row: they get small ones)
     K, V = bf16(K * (np.minimum(size, 2.0) if of != "v" else 1.0)), bf16(V * (size if of != "k" else 1.0))
     if of != "v":
         K[at + 5] *= 2.0 ** -14                     # further apart than a tile's scales may be
     K[:, :, 64:] = np.abs(K[:, :, 64:])             # a zero point of 0
-    ref.store(c.pool, c.slots(0, prefix), K, V)
-    c.K[0], c.V[0] = ref.load(c.pool, c.slots(0, prefix), dh, dv)
-    q = _queries(rng, B, Hq, 1, dh)
-    args = dict(prefix_table=_dev(c.table[0]), prefix_length=_dev(np.array([prefix], np.int32)),
-                page_table=_dev(c.table[1:, :1]), lengths=_dev(np.array([2] * B, np.int32)))
-    O, LSE = _run(c, q, args, dh, dv)
+    ref.store(p.pool, p.slots(0, prefix), K, V)
+    p.K[0], p.V[0] = ref.load(p.pool, p.slots(0, prefix), dh, dv)
+    c = cache()
+    O, LSE = _run(c, q, _many_args(c, B, group), dh, dv)
     torch.cuda.synchronize()
     O, LSE = f64(O), f64(LSE)
-    for b in range(B):
-        K, V = np.concatenate([c.K[0], c.K[b + 1]])[:, 0], np.concatenate([c.V[0], c.V[b + 1]])[:, 0]
-        _, rL, _, eL = srv.attend_prefix(q[b], c.K[0], c.V[0], c.K[b + 1], c.V[b + 1], 2, dh ** -0.5)
-        assert_within(LSE[b], rL, eL, "LSE")
-        for r in range(Hq):
-            s = K @ q[b, r, 0] * dh ** -0.5
-            A = np.exp(s - s.max())
-            A /= A.sum()
-            want, bound = A @ V, _weighted_bound(A, s, K, V, q[b, r, 0], dh)
-            assert_within(O[b, r, 0], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "O")
+    for b in (0, 13, 23):
+        for h in (0, 18):
+            K, V = (np.concatenate([x[0], x[b + 1]])[:, h] for x in (c.K, c.V))
+            for r in range(h * group, (h + 1) * group, 3):
+                _, rL, _, eL = ref.attend(q[b, r:r + 1], K[:, None], V[:, None], len(K), dh ** -0.5)
+                assert_within(LSE[b, r], rL[0], eL[0] + 258 * 2.0 ** -23, "LSE")
+                s = K @ q[b, r, 0] * dh ** -0.5
+                A = np.exp(s - s.max())
+                A /= A.sum()
+                want, bound = A @ V, _weighted_bound(A, s, K, V, q[b, r, 0], dh)
+                assert_within(O[b, r, 0], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "O")
 
 
 def _weighted_bound(A, s, K, V, q, dh):

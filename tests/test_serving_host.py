@@ -87,10 +87,12 @@ def test_evict_refuses(lib):
         assert call(**kw) == N, kw
     for kw in (dict(table=ctypes.c_void_p(258)), dict(w=ctypes.c_void_p(258)), dict(kept=ctypes.c_void_p(258))):
         assert call(**kw) == A, kw
-    need = lib.attn_cache_evict_workspace_bytes(_cache(), 2, 4, 64, 4, 8)
+    # few tokens that may move need no workspace, many do
+    assert lib.attn_cache_evict_workspace_bytes(_cache(), 2, 4, 64, 4, 8) == 0
+    need = lib.attn_cache_evict_workspace_bytes(_cache(), 2, 400, 4096, 4, 8)
     assert need > 0 and need % 256 == 0
     for kw in (dict(ws=None), dict(n=need - 1), dict(ws=ctypes.c_void_p(512 + 16))):
-        assert call(**kw) == bnd.ATTN_ERR_WORKSPACE
+        assert call(pages=400, keep=4096, **kw) == bnd.ATTN_ERR_WORKSPACE
     assert lib.attn_cache_evict_workspace_bytes(_cache(), 2, 4, 0, 0, 0) == 0
 
 

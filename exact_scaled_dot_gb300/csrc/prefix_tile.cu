@@ -16,7 +16,7 @@
 // fp16 numbers (33 bits).  So the scores are exact products summed in fp32, and
 // nothing is left to multiply per key.
 //
-// Values.  O += P V with V = fp16(s (c - z) 2^E_g) and P = fp16(2^10 exp(..)): two
+// Values.  O += P V with V = fp16(s (c - z) 2^E_g) and P = fp16(2^7 exp(..)): two
 // roundings of 2^-12.  One E_g per CTA serves while V's scales of a group lie
 // within four octaves.  (Scales as factors of the weights or scores cost a
 // shared-memory word per row and key each: 2.5 times the time, measured.)
@@ -36,12 +36,13 @@
 // at the end.  The softmax takes its scores into registers at once, so that the
 // next tile's are made while it works.
 //
-// Tensor memory, stream t, from column 128 t: the scores in 64; Q's first 64 dims
-// in the next 32 (through shared memory Q is read again for every 64 keys) and
-// the weights in 32 more, or, with O 64 wide, Q's second half there and the
-// weights behind O.  O in [256 + 128 t, + d_v).  In the other way S_0, S_1 in the
+// Tensor memory, stream t, from column 128 t: the scores in 64, the weights in 32
+// and another 32, so that a tile's are put down while the product with the ones
+// before still runs.  O in [256 + 128 t, + d_v).  In the other way S_0, S_1 in the
 // 128 columns, then the scores over S_0 and W_0, W_1 over S_1, one tile after the
-// other.
+// other.  (Q's rows there, and one place for the weights: the softmax waited 400
+// cycles of 2600 a tile for it; a product of 64 columns takes some 54 cycles
+// either way.)
 //
 // A 32-bit word of codes becomes four pairs of operands by one AND-OR and two
 // fp16 operations each (0x6400 | c is 1024 + c); the pairs are the dims (k, k + 4)
@@ -64,7 +65,11 @@ constexpr int kLeastTop = -118, kMostTop = 126;
 // 2^(X + 2), X the exponent of the CTA's first; K's of a tile 2^12 apart; neither
 // beyond 2^+-100.
 constexpr int kBelow = 2, kAbove = 1, kSpreadK = 12, kMostExp = 100;
-constexpr int kFastBits = 10;       // P 2^10 is at most 2^15
+// P 2^kFastBits is fp16: a row's reference moves when a tile's sum of them passes
+// 2^15.  (The sum is needed anyway; a maximum of every tile took a seventh of the
+// kernel's time.)
+constexpr int kFastBits = 7;
+constexpr float kMostSum = 32768.0f;
 constexpr int kScaleK = 4;          // K's largest scale becomes 2^4 to 2^5
 constexpr int kSumShift = 6;        // sum q_g 2^-6 and s (8 - z) 2^6 are fp16
 constexpr int kKeys = 64;           // keys of a tile: two pages
@@ -90,9 +95,7 @@ struct TileCfg {
   static constexpr int kOp = kK16 + kV16 + kKx;
   static constexpr int kScales = (GK + GV) * kKeys * 4;
   static constexpr int kPrep = kScales + kKeys * 4;          // and K's sums' factors
-  // Tensor memory of a stream: groups of Q there are, and where the weights are.
-  static constexpr int kTmemQ = DV == 64 ? GK : 1;
-  static constexpr uint32_t kColQ = 64, kColW = DV == 64 ? 256 + 64 : 96;
+  static constexpr uint32_t kColW = 64;      // of a stream's weights in tensor memory: 32 columns, two of them
   static constexpr int kOffQ = 0;
   static constexpr int kOffOp = kOffQ + NT * kQTile;         // [stage] K16, V16, K's sums
   static constexpr int kOffQx = kOffOp + kStages * kOp;      // [row tile]
@@ -113,8 +116,8 @@ struct TileCfg {
   static constexpr int kBarS = kBarEmpty + kStages;          // [2]
   static constexpr int kBarSFree = kBarS + 2;                // [2]
   static constexpr int kBarP = kBarSFree + 2;                // [2]
-  static constexpr int kBarPV = kBarP + 2;                   // [2]
-  static constexpr int kBarQ = kBarPV + 2;
+  static constexpr int kBarPV = kBarP + 2;                   // [2][2], of each place of the weights
+  static constexpr int kBarQ = kBarPV + 4;
   static constexpr int kBarDrain = kBarQ + 1;                // [2]
   static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
@@ -254,7 +257,8 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
       mbar_init(bar(C::kBarS + t), 1);
       mbar_init(bar(C::kBarP + t), 128);
       mbar_init(bar(C::kBarSFree + t), 128);
-      mbar_init(bar(C::kBarPV + t), 1);
+      mbar_init(bar(C::kBarPV + 2 * t), 1);
+      mbar_init(bar(C::kBarPV + 2 * t + 1), 1);
       mbar_init(bar(C::kBarDrain + t), 1);
     }
     mbar_init(bar(C::kBarQ), 256);
@@ -397,8 +401,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
 #pragma unroll
             for (int g = 0; g < GK; ++g) {
               const SmemDesc dkg = desc_step(dk, g * kKeys * 128);
-              if (g < C::kTmemQ) umma_ts_four<32>(tS, tS + C::kColQ + 32 * g, dkg, kIdQK, g > 0 ? 1u : 0u);
-              else umma_ss_four(tS, desc_step(dq, g * 128 * 128), dkg, kIdQK, 1u);
+              umma_ss_four(tS, desc_step(dq, g * 128 * 128), dkg, kIdQK, g > 0 ? 1u : 0u);
             }
             umma_ss_we(tS, dqx, desc_step(dx0, st * C::kOp), kIdQK, 1u);
           } else {
@@ -438,13 +441,13 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
           tc_fence_after_sync();
           const SmemDesc dv = desc_step(dv0, st * C::kOp);
           if (fast) {
-            umma_ts_four<2048>(tO, tS + C::kColW, dv, kIdPV, k > 0 ? 1u : 0u);
+            umma_ts_four<2048>(tO, tS + C::kColW + 32 * (k & 1), dv, kIdPV, k > 0 ? 1u : 0u);
           } else {
 #pragma unroll 1
             for (int g = 0; g < GV; ++g)
               umma_ts_four<2048>(tO + 64 * g, tS + 64 + 32 * g, desc_step(dv, g * kKeys * 128), kIdPVg, k > 0 ? 1u : 0u);
           }
-          umma_commit_we(bar(C::kBarPV + t));
+          umma_commit_we(bar(C::kBarPV + 2 * t + (k & 1)));
           umma_commit_we(bar(C::kBarEmpty + st));
           if (k + 1 < count && !next_fast) scores(next, false);     // (over the weights just used)
           st = next, ph = next_ph, fast = next_fast;
@@ -623,7 +626,6 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     float f;
     {
       named_bar_sync(2, 512);                              // (all rows are there)
-      const uint8_t* tile = smem + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile;
       {
         const float4 of = reinterpret_cast<const float4*>(smem + C::kOffState)[(NT == 2 ? 128 * t : 0) + row];
         const uint32_t mb = __float_as_uint(of.z);
@@ -648,18 +650,6 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
         }
         fence_proxy_async_smem();
       }
-#pragma unroll 1
-      for (int k = 0; k < C::kTmemQ * 8; k += 2) {
-        uint32_t q16[8];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(tile + k / 8 * (128 * 128) + row * 128 +
-                                                          (((k + i) & 7) ^ (row & 7)) * 16);
-          q16[4 * i] = x.x, q16[4 * i + 1] = x.y, q16[4 * i + 2] = x.z, q16[4 * i + 3] = x.w;
-        }
-        tmem_st8_nowait(tS + C::kColQ + 4 * k, q16);
-      }
-      tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(bar(C::kBarQ));
     }
@@ -677,7 +667,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     bool ok = *abort_flag == 0;
     // O's columns of each group times a factor, once the products before have been added.
     auto rescale = [&](int k, float back0, float back1) {
-      if (!wait_all(C::kBarPV + t, static_cast<uint32_t>((k - 1) & 1))) return false;
+      if (!wait_all(C::kBarPV + 2 * t + ((k - 1) & 1), static_cast<uint32_t>(((k - 1) >> 1) & 1))) return false;
       tc_fence_after_sync();
 #pragma unroll 1
       for (int c = 0; c < DV; c += 16) {
@@ -692,19 +682,26 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
       return true;
     };
     auto row_max = [](const float* s) {
-      float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
+      float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int i = 4; i < kKeys; i += 4) {
-        a = fmax3(a, s[i], s[i + 1]);
-        b = fmax3(b, s[i + 2], s[i + 3]);
-      }
-      return fmaxf(a, b);
+      for (int i = 4; i < kKeys - 4; i += 8)
+#pragma unroll
+        for (int o = 0; o < 4; ++o) m[o] = fmax3(m[o], s[i + 2 * o], s[i + 2 * o + 1]);
+      return fmax3(fmax3(m[0], m[1], s[kKeys - 1]), fmax3(m[2], m[3], s[kKeys - 2]), fmaxf(s[kKeys - 3], s[kKeys - 4]));
     };
-    auto hide = [](uint2 mask, float* s) {
-      if ((mask.x & mask.y) == 0xFFFFFFFFu) return;
+    // -inf for the keys that are not there.
+    auto hide = [&](uint2 mask) {
+#pragma unroll 1
+      for (int c = 0; c < kKeys; c += 16) {
+        uint32_t a[16];
+        tmem_ld16_nowait(tS + c, a);
+        tmem_wait_ld16(a);
+        const uint32_t bits = (c < 32 ? mask.x : mask.y) >> (c & 31);
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (!(((i < 32 ? mask.x : mask.y) >> (i & 31)) & 1u)) s[i] = -INFINITY;
+        for (int i = 0; i < 16; ++i) a[i] = (bits >> i) & 1u ? a[i] : 0xFF800000u;
+        tmem_st16_nowait(tS + c, a);
+      }
+      tmem_wait_st();
     };
     int st = NT == 2 ? -1 : t - 2;             // stage of the tile at hand, and its phase
     uint32_t ph = 0;
@@ -719,6 +716,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
       seen |= mask.x | mask.y;
       if (__shfl_sync(0xffffffffu, head.fast, 0)) {
         // ---- scales in the operands ----
+        if ((mask.x & mask.y) != 0xFFFFFFFFu) hide(mask);
         float s[kKeys];
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) tmem_ld32_nowait(tS + c, reinterpret_cast<uint32_t(&)[32]>(s[c]));
@@ -726,44 +724,50 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
         for (int c = 0; c < kKeys; c += 32) tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(s[c]));
         tc_fence_before_sync();
         mbar_arrive(bar(C::kBarSFree + t));
-        hide(mask, s);
         float fk = f * head.unscale;              // (not 0, as f)
         fk = fk < 0x1p-126f ? 0x1p-126f : fk;
-        const float mx = row_max(s) * fk;
-        if (__any_sync(0xffffffffu, mx + shift > static_cast<float>(kLazy))) {
-          const float m = ceilf(mx);
+        // The reference to the row's maximum, where that is above it.
+        auto move_reference = [&] {
+          const float m = ceilf(row_max(s) * fk);
           float alpha = 1.f;
-          if (m + shift > static_cast<float>(kLazy)) {     // (whole octaves: alpha is a power of two)
+          if (m + shift > 0.f) {                           // (whole octaves: alpha is a power of two)
             alpha = fast_exp2(-shift - m);
             shift = -m;
           }
           l_sum *= alpha;
-          if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            ok = rescale(k, alpha, alpha);
-            if (!ok) break;
-          }
-        }
-        if (k > 0) {                             // the weights before have been used
-          ok = wait_all(C::kBarPV + t, static_cast<uint32_t>((k - 1) & 1));
+          return k == 0 || !__any_sync(0xffffffffu, alpha != 1.f) || rescale(k, alpha, alpha);
+        };
+        if (k == 0) move_reference();
+        if (k > 1) {                             // the weights two tiles before have been used
+          ok = wait_all(C::kBarPV + 2 * t + (k & 1), static_cast<uint32_t>(((k >> 1) - 1) & 1));
           if (!ok) break;
           tc_fence_after_sync();
         }
-        const float add = shift + static_cast<float>(kFastBits);
-        float l[2] = {0.f, 0.f};
+        float l[2];
+#pragma unroll 1
+        for (int again = 0; again < 2; ++again) {
+          const float add = shift + static_cast<float>(kFastBits);
+          l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 32) {
-          uint32_t w[16];
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float e0, e1;
-            ffma2(e0, e1, s[c + i], s[c + i + 1], fk, fk, add, add);
-            e0 = fast_exp2(e0);
-            e1 = fast_exp2(e1);
-            fadd2(l[0], l[1], e0, e1);
-            w[i / 2] = pack_half2(e0, e1);
+            for (int i = 0; i < 32; i += 2) {
+              float e0, e1;
+              ffma2(e0, e1, s[c + i], s[c + i + 1], fk, fk, add, add);
+              e0 = fast_exp2(e0);
+              e1 = fast_exp2(e1);
+              fadd2(l[0], l[1], e0, e1);
+              w[i / 2] = pack_half2(e0, e1);
+            }
+            tmem_st16_nowait(tS + C::kColW + 32 * (k & 1) + c / 2, w);
           }
-          tmem_st16_nowait(tS + C::kColW + c / 2, w);
+          // (Once more at most: with the reference at its maximum a row's sum is at most 2^13.)
+          if (!__any_sync(0xffffffffu, l[0] + l[1] > kMostSum)) break;
+          ok = move_reference();
+          if (!ok) break;
         }
+        if (!ok) break;
         l_sum += l[0] + l[1];
 #pragma unroll
         for (int g = 0; g < GV; ++g) up[g] = head.up[g];
@@ -864,7 +868,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     }
     if (folded) l_sum *= exp2_int(-kFastBits);
     cudaTriggerProgrammaticLaunchCompletion();     // the merge kernel may start (it waits for this grid)
-    if (ok && mine > 0) ok = wait_all(C::kBarPV + t, static_cast<uint32_t>((mine - 1) & 1));
+    if (ok && mine > 0) ok = wait_all(C::kBarPV + 2 * t + ((mine - 1) & 1), static_cast<uint32_t>(((mine - 1) >> 1) & 1));
     tc_fence_after_sync();
     if (seen == 0u) l_sum = 0.f;
     float weight = 1.f, other = 0.f;           // of this stream's sums and of the other's (NT = 1)

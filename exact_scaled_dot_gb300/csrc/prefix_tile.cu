@@ -79,7 +79,7 @@ constexpr int kTilePages = kKeys / kPageTokens;
 struct __align__(16) TileHead {
   uint32_t mask[2];       // the keys there are, of each page
   float unscale;          // 2^-e of K's operands
-  int32_t fast;           // 1: scales in the operands
+  int32_t fast;           // 1: scales in the operands (these four are read as one)
   float up[2];            // fast: the weights' and V's power of two of each group
   float pad[2];
   float most[2][2];       // else: the largest of V's scales, [group][page]
@@ -708,13 +708,21 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     for (int k = 0; k < mine && ok; ++k) {
       st += NT == 2 ? 1 : 2;
       if (st >= C::kStages) st -= C::kStages, ph ^= 1u;
-      ok = wait_all(C::kBarS + t, static_cast<uint32_t>(k & 1)) && wait_all(C::kBarFull + st, ph);
+      ok = wait_all(C::kBarFull + st, ph);
+      if (!ok) break;
+      // What is known of the tile is read before its scores are there: the tensor
+      // core's operands fill shared memory's pipe, and a word takes hundreds of cycles.
+      const TileHead& head = reinterpret_cast<const TileHead*>(smem + C::kOffHead)[st];
+      const uint4 known = *reinterpret_cast<const uint4*>(&head);
+      const float2 tile_up = *reinterpret_cast<const float2*>(head.up);
+      const uint2 mask = make_uint2(known.x, known.y);
+      const float unscale = __uint_as_float(known.z);
+      const bool fast = __shfl_sync(0xffffffffu, known.w, 0) != 0u;
+      seen |= mask.x | mask.y;
+      ok = wait_all(C::kBarS + t, static_cast<uint32_t>(k & 1));
       if (!ok) break;
       tc_fence_after_sync();
-      const TileHead& head = reinterpret_cast<const TileHead*>(smem + C::kOffHead)[st];
-      const uint2 mask = *reinterpret_cast<const uint2*>(head.mask);
-      seen |= mask.x | mask.y;
-      if (__shfl_sync(0xffffffffu, head.fast, 0)) {
+      if (fast) {
         // ---- scales in the operands ----
         if ((mask.x & mask.y) != 0xFFFFFFFFu) hide(mask);
         float s[kKeys];
@@ -724,7 +732,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
         for (int c = 0; c < kKeys; c += 32) tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(s[c]));
         tc_fence_before_sync();
         mbar_arrive(bar(C::kBarSFree + t));
-        float fk = f * head.unscale;              // (not 0, as f)
+        float fk = f * unscale;              // (not 0, as f)
         fk = fk < 0x1p-126f ? 0x1p-126f : fk;
         // The reference to the row's maximum, where that is above it.
         auto move_reference = [&] {
@@ -769,8 +777,8 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
         }
         if (!ok) break;
         l_sum += l[0] + l[1];
-#pragma unroll
-        for (int g = 0; g < GV; ++g) up[g] = head.up[g];
+        up[0] = tile_up.x;
+        if (GV == 2) up[GV - 1] = tile_up.y;
       } else {
         // ---- scales beside the operands ----
         const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale + st * C::kScales);

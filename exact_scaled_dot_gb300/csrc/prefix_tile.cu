@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
   int len = *p.length;
   if (item == 0 && threadIdx.x == 0 && len > cap) record_status(p.status, ATTN_ERR_PAGE);
   len = len < 0 ? 0 : (len > cap ? cap : len);
-  const int tiles = (len + kKeys - 1) / kKeys;
+  const int tiles = len / kKeys + (len % kKeys != 0);
   const int each = (tiles + p.splits - 1) / p.splits;
   if (item == 0 && threadIdx.x == 0) *p.used = each > 0 ? (tiles + each - 1) / each : 0;
   const int t0 = split * each;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
           int bytes = 0;
 #pragma unroll
           for (int i = 0; i < kTilePages; ++i) {
-            const int page = (t0 + j) * kTilePages + i, left = len - page * kPageTokens;
+            const int64_t left = len - static_cast<int64_t>(page) * kPageTokens;
             src[i] = nullptr;
             mask[i] = left >= kPageTokens ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
             if (left <= 0) continue;

@@ -78,7 +78,7 @@ def test_evict_refuses(lib):
         return lib.attn_cache_evict(c, B, pages, keep, first, recent, table, lengths, w, nl, nw, kept, ws,
                                     ctypes.c_size_t(n), None)
 
-    for kw in (dict(B=0), dict(pages=0), dict(pages=1 << 26), dict(keep=0), dict(keep=-1), dict(first=-1),
+    for kw in (dict(B=0), dict(pages=0), dict(pages=(1 << 25) + 1), dict(keep=0), dict(keep=-1), dict(first=-1),
                dict(recent=-1), dict(first=60, recent=5), dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), dict(nl=P),
                dict(B=2 ** 31 - 1)):
         assert call(**kw) == S, kw

@@ -115,8 +115,9 @@ struct TileCfg {
   static constexpr int kBarEmpty = kBarFull + kStages;
   static constexpr int kBarS = kBarEmpty + kStages;          // [2]
   static constexpr int kBarSFree = kBarS + 2;                // [2]
-  static constexpr int kBarP = kBarSFree + 2;                // [2]
-  static constexpr int kBarPV = kBarP + 2;                   // [2][2], of each place of the weights
+  // [2][2], of each place of the weights: a warp may be a tile ahead of the others.
+  static constexpr int kBarP = kBarSFree + 2;
+  static constexpr int kBarPV = kBarP + 4;
   static constexpr int kBarQ = kBarPV + 4;
   static constexpr int kBarDrain = kBarQ + 1;                // [2]
   static constexpr int kNumBars = kBarDrain + 2;
@@ -255,10 +256,11 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(C::kBarS + t), 1);
-      mbar_init(bar(C::kBarP + t), 128);
       mbar_init(bar(C::kBarSFree + t), 128);
-      mbar_init(bar(C::kBarPV + 2 * t), 1);
-      mbar_init(bar(C::kBarPV + 2 * t + 1), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(C::kBarP + 2 * t + i), 128);
+        mbar_init(bar(C::kBarPV + 2 * t + i), 1);
+      }
       mbar_init(bar(C::kBarDrain + t), 1);
     }
     mbar_init(bar(C::kBarQ), 256);
@@ -351,6 +353,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
           int bytes = 0;
 #pragma unroll
           for (int i = 0; i < kTilePages; ++i) {
+            const int page = (t0 + j) * kTilePages + i;
             const int64_t left = len - static_cast<int64_t>(page) * kPageTokens;
             src[i] = nullptr;
             mask[i] = left >= kPageTokens ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
               scores(next, true);
             }
           }
-          ok = wait_all(C::kBarP + t, static_cast<uint32_t>(k & 1));
+          ok = wait_all(C::kBarP + 2 * t + (k & 1), static_cast<uint32_t>((k >> 1) & 1));
           if (!ok) break;
           tc_fence_after_sync();
           const SmemDesc dv = desc_step(dv0, st * C::kOp);
@@ -772,6 +775,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
           }
           // (Once more at most: with the reference at its maximum a row's sum is at most 2^13.)
           if (!__any_sync(0xffffffffu, l[0] + l[1] > kMostSum)) break;
+          tmem_wait_st();                        // (two stores to one place have no order of their own)
           ok = move_reference();
           if (!ok) break;
         }
@@ -872,7 +876,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
       }
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::kBarP + t));
+      mbar_arrive(bar(C::kBarP + 2 * t + (k & 1)));
     }
     if (folded) l_sum *= exp2_int(-kFastBits);
     cudaTriggerProgrammaticLaunchCompletion();     // the merge kernel may start (it waits for this grid)

@@ -176,6 +176,37 @@ def test_many_tiles_in_a_range(B, group, prefix, dh, dv):
             assert_within(LSE[b, at], rL, eL, "LSE")
 
 
+@pytest.mark.parametrize("B,group", [(40, 4), (20, 4)])
+@pytest.mark.parametrize("dh,dv", [(64, 64), (128, 128), (128, 64)])
+def test_scores_that_climb_for_some_rows(B, group, dh, dv):
+    """Two sequences' scores rise by 11 octaves every 64 keys, so that those rows' sums of
+    weights pass what a tile may hold again and again while the others' never do."""
+    rng, p, cache, q = _many_heads(B + dv, B, group, dh, dv, 4100, [3] * B)
+    u = np.sign(rng.normal(size=(19, dh)))
+    climb = 8.0 * (np.arange(4100) // 64 % 9) / dh ** 0.5
+    K = bf16(rng.normal(size=(4100, 19, dh)) * 0.25 + climb[:, None, None] * u)
+    ref.store(p.pool, p.slots(0, 4100), K, bf16(rng.normal(size=(4100, 19, dv))))
+    p.K[0], p.V[0] = ref.load(p.pool, p.slots(0, 4100), dh, dv)
+    c = cache()
+    q = bf16(q * 0.01)
+    few = (9, B - 3)
+    for b in few:
+        q[b, :, 0] = bf16(np.repeat(u, group, 0) * (1 + np.arange(19 * group)[:, None] % 3 * 0.25))
+    args = _many_args(c, B, group)
+    O, LSE = _run(c, q, args, dh, dv)
+    for _ in range(5):
+        again = _run(c, q, args, dh, dv)
+        assert torch.equal(O, again[0]) and torch.equal(LSE, again[1])
+    O, LSE = f64(O), f64(LSE)
+    for b in (*few, 0):
+        for h in (0, 7, 18):
+            at = slice(h * group, (h + 1) * group)
+            rO, rL, eO, eL = srv.attend_prefix(q[b, at], c.K[0][:, h:h + 1], c.V[0][:, h:h + 1], c.K[b + 1][:, h:h + 1],
+                                               c.V[b + 1][:, h:h + 1], c.lengths[b + 1], dh ** -0.5)
+            assert_within(O[b, at], rO, eO + 2.0 ** -8 * (np.abs(rO) + eO), "O")
+            assert_within(LSE[b, at], rL, eL, "LSE")
+
+
 @pytest.mark.parametrize("group", [4, 16])
 @pytest.mark.parametrize("at", [40, 700])
 @pytest.mark.parametrize("of", ["k", "v", "both"])

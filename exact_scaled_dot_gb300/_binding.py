@@ -1296,7 +1296,14 @@ def attn_cache_weigh(Q, cache: QuantCache, page_table, lengths, LSE, weights, *,
     return weights
 
 
+def _evict_sizes(keep, first, recent) -> bool:
+    # (as the call checks them, before they become 32-bit numbers)
+    return 0 < keep <= 1 << 30 and first >= 0 and recent >= 0 and first + recent <= keep
+
+
 def attn_cache_evict_workspace_bytes(cache: QuantCache, B, max_pages, keep, *, first=0, recent=0) -> int:
+    if not _evict_sizes(keep, first, recent):
+        return 0
     return int(load().attn_cache_evict_workspace_bytes(cache.arg(), int(B), int(max_pages), int(keep), int(first),
                                                        int(recent)))
 
@@ -1315,14 +1322,14 @@ def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int,
     if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D [B, max_pages]")
     B, max_pages = page_table.shape
-    dev, keep = cache.device, int(keep)
+    dev, keep, first, recent = cache.device, int(keep), int(first), int(recent)
+    if not _evict_sizes(keep, first, recent):
+        raise AttnError(ATTN_ERR_SHAPE, "attn_cache_evict")
     ws = (B, cache.Hkv, max_pages * ATTN_CACHE_PAGE_TOKENS)
     ks = (B, cache.Hkv, keep)
     _check_flat(page_table, "page_table", torch.int32, (B, max_pages), dev)
     _check_flat(lengths, "lengths", torch.int32, (B,), dev)
     _check_flat(weights, "weights", torch.float32, ws, dev)
-    if keep <= 0:
-        raise AttnError(ATTN_ERR_SHAPE, "attn_cache_evict")
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
@@ -1339,7 +1346,7 @@ def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int,
         workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
     else:
         size = workspace.numel() * workspace.element_size()
-    _check(load().attn_cache_evict(cache.arg(), B, max_pages, keep, int(first), int(recent), page_table.data_ptr(),
+    _check(load().attn_cache_evict(cache.arg(), B, max_pages, keep, first, recent, page_table.data_ptr(),
                                    lengths.data_ptr(), weights.data_ptr(), new_lengths.data_ptr(),
                                    new_weights.data_ptr(), kept.data_ptr(), _addr(workspace), size,
                                    torch._C._cuda_getCurrentRawStream(dev.index)), "attn_cache_evict")

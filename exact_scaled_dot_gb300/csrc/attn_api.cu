@@ -1092,7 +1092,8 @@ int check_cache_evict(const attn_cache* c, int B, int max_pages, int keep, int f
   if (rc) return rc;
   if (B <= 0 || max_pages <= 0 || max_pages > 1 << 25) return ATTN_ERR_SHAPE;     // places are int32, with room
   if (static_cast<int64_t>(B) * c->Hkv * 8 > (int64_t{1} << 31) - 1) return ATTN_ERR_SHAPE;
-  if (keep <= 0 || first < 0 || recent < 0 || static_cast<int64_t>(first) + recent > keep) return ATTN_ERR_SHAPE;
+  if (keep <= 0 || keep > 1 << 30 || first < 0 || recent < 0 || static_cast<int64_t>(first) + recent > keep)
+    return ATTN_ERR_SHAPE;
   return ATTN_OK;
 }
 

@@ -158,3 +158,20 @@ def test_reference_weights_sum_to_one():
     _, L, _, _ = ref.attend(q, K, K, 9, 0.125)
     w, _ = srv.weigh(q, K, L, 9, np.zeros((2, 32)), 0.125)
     assert np.allclose(w.sum(-1), 4.0) and (w[:, 9:] == 0).all()
+
+
+@pytest.mark.parametrize("first,recent,keep", [(0, 0, (1 << 30) + 1), (0, 0, 0), ((1 << 32) + 1, 0, 16), (0, -1, 16),
+                                               (9, 8, 16), (0, 0, (1 << 32) + 16)])
+def test_eviction_sizes_are_checked_before_they_are_32_bits(lib, first, recent, keep):
+    class Fake:
+        device, Hkv, d_h, d_v, pages = torch.device("cpu"), 2, 64, 64, 4
+
+        @staticmethod
+        def arg():
+            return _cache()
+    t, n = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(esd.AttnError):
+        esd.attn_cache_evict(Fake, t, n, torch.zeros((2, 2, 96)), keep, first=first, recent=recent)
+    assert esd.attn_cache_evict_workspace_bytes(Fake, 2, 1 << 20, keep, first=first, recent=recent) == 0
+    if keep < 1 << 31 and first < 1 << 31:
+        assert lib.attn_cache_evict_workspace_bytes(_cache(), 2, 1 << 20, keep, first, recent) == 0

@@ -665,7 +665,6 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
 #pragma unroll
     for (int g = 0; g < GV; ++g) up[g] = exp2_int(-kLeastTop), s_lim[g] = 0.f;
     bool folded = true;
-    uint32_t seen = 0u;                        // keys there were
     const int mine = count_of(t);
     bool ok = *abort_flag == 0;
     // O's columns of each group times a factor, once the products before have been added.
@@ -721,7 +720,6 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
       const uint2 mask = make_uint2(known.x, known.y);
       const float unscale = __uint_as_float(known.z);
       const bool fast = __shfl_sync(0xffffffffu, known.w, 0) != 0u;
-      seen |= mask.x | mask.y;
       ok = wait_all(C::kBarS + t, static_cast<uint32_t>(k & 1));
       if (!ok) break;
       tc_fence_after_sync();
@@ -882,7 +880,6 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     cudaTriggerProgrammaticLaunchCompletion();     // the merge kernel may start (it waits for this grid)
     if (ok && mine > 0) ok = wait_all(C::kBarPV + 2 * t + ((mine - 1) & 1), static_cast<uint32_t>(((mine - 1) >> 1) & 1));
     tc_fence_after_sync();
-    if (seen == 0u) l_sum = 0.f;
     float weight = 1.f, other = 0.f;           // of this stream's sums and of the other's (NT = 1)
     float* theirs = reinterpret_cast<float*>(smem + C::kOffOp);        // [dim][row], over the operand tiles
     if constexpr (NT == 1) {

@@ -630,9 +630,16 @@ int attn_fwd_decode_cache(const attn_cache* cache, int32_t B, int32_t Hq, int32_
  * the call runs, like page_table [B][max_pages] and lengths [B].  A length of
  * 0 (of the prefix, of a sequence's own keys, of both) leaves those keys out;
  * rows without a visible key, rows of Q that are not finite, page numbers and
- * lengths out of range are as in attn_fwd_decode_cache, and so is the
- * precision.  (A prefix of several batches stays in its pages: its tokens are
- * not among those that attn_cache_evict moves.)
+ * lengths out of range are as in attn_fwd_decode_cache.  (Where every page of a
+ * row's keys is outside the pool, a row that is not finite gives NaN in both.)
+ * Precision: scores and sums as in attn_fwd_decode_cache.  Its weights are
+ * rounded as there for the own keys and where the batch has few query rows; for
+ * many, the weights over the prefix are fp16 relative to the row's
+ * largest (11 bits down to 2^-20 of it, multiples of 2^-30 of it below) and the
+ * values' elements have 11 bits, while the values' scales of a group of 64 dims
+ * lie within four octaves; where they do not, it is as there again.
+ * A prefix of several batches stays in its pages: its tokens are not among
+ * those that attn_cache_evict moves.
  * `workspace`: attn_fwd_prefix_cache_workspace_bytes() bytes, 256-byte
  * aligned; it depends on the sizes only. */
 size_t attn_fwd_prefix_cache_workspace_bytes(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q,
@@ -677,8 +684,8 @@ int attn_cache_weigh(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q
  *   kept [B][Hkv][keep]        (or NULL) the place that the token at each place had; -1 past
  *                              the new length
  * All device memory; lengths and page_table [B][max_pages] are read when the
- * call runs.  new_lengths must not be lengths (ATTN_ERR_SHAPE).  first + recent <=
- * keep (ATTN_ERR_SHAPE).  Pages that a token moves in or out of belong to one
+ * call runs.  new_lengths must not be lengths, first + recent <= keep <= 2^30,
+ * max_pages <= 2^25 (else ATTN_ERR_SHAPE).  Pages that a token moves in or out of belong to one
  * sequence only: tokens below `first` do not move, so that shared pages at the
  * front are safe below it.  The pages behind the new length are free
  * for other use when the call has run.  A page number outside the pool leaves

@@ -72,6 +72,7 @@ struct Moving {
 template <int DH, int DV, int THREADS, typename Block, typename Get, typename Put>
 __device__ __forceinline__ void copy_tokens(Moving& mv, int tid, int count, bool between, Block&& block_of, Get&& get,
                                             Put&& put) {
+  static_assert(THREADS >= kBatch, "a thread per token of a batch");
   // K codes, V codes, K words, V words: pieces of a token, and where they are.
   constexpr int kPieces[4] = {DH / 32, DV / 32, DH / kQuantGroup, DV / kQuantGroup};
   constexpr int kAt[4] = {off_k_codes(), off_v_codes(DH), off_k_words(DH, DV), off_v_words(DH, DV)};
@@ -407,13 +408,17 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const __grid_c
   auto block_of = [&](int j) { return block_at<DH, DV>(p, table, h, j); };
   if (__syncthreads_or(status_blocks(p.status))) return;
   const int total = p.counts[bh];
-  // The lists ascend: the first `near` tokens come from places below m.
-  int near = 0, above = total;
-  while (near < above) {
-    const int mid = (near + above) / 2;
-    if (from[mid] < m) near = mid + 1;
-    else above = mid;
-  }
+  // The list ascends: its first `near` tokens come from places below m, where the
+  // newest go (at most `recent`; a search by halves would wait for every step's load).
+  __shared__ int near_s;
+  if (tid == 0) near_s = 0;
+  __syncthreads();
+  int mine = 0;
+  for (int i = tid; i < total && i < p.recent; i += kMoveThreads) mine += from[i] < m;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane_id() == 0 && mine > 0) atomicAdd(&near_s, mine);
+  __syncthreads();
+  const int near = near_s;
   if (part == 0) {
     copy_tokens<DH, DV, kMoveThreads>(mv, tid, near, false, block_of, [&](int k) { return from[k]; },
                                       [&](int k) { return to[k]; });

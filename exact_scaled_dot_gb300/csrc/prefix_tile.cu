@@ -105,7 +105,7 @@ struct TileCfg {
   static constexpr int kOffScale = kOffRawHead + kRawStages * static_cast<int>(sizeof(TileHead));   // [stage]
   static constexpr int kOffHead = kOffScale + kStages * kScales;                 // [stage]
   static constexpr int kOffRawMask = kOffHead + kStages * static_cast<int>(sizeof(TileHead));       // [raw stage][2]
-  // Of each row, while Q is put down; (l, shift) of stream 1 (NT = 1).
+  // Of each row, while Q is put down; (l, shift) of both streams (NT = 1).
   static constexpr int kOffState = (kOffRawMask + kRawStages * 8 + 15) / 16 * 16;
   static constexpr int kOffBar = kOffState + NT * 128 * 16;
   static constexpr int kBarRawFull = 0;
@@ -131,7 +131,8 @@ struct TileCfg {
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(kBlock % 16 == 0 && kOffRaw % 16 == 0 && kOffScale % 16 == 0 && kOffBar % 8 == 0, "alignment");
   static_assert(kOp % 1024 == 0 && kOffOp % 1024 == 0, "swizzled tiles");
-  static_assert(NT == 2 || 128 * DV * 4 <= kStages * kOp, "stream 1's sums over the operand tiles");
+  static_assert(NT == 2 || 128 * DV * 4 <= kStages * kOp, "the streams' sums over the operand tiles");
+  static_assert(kQTile >= 16384 && kRawStages * kTilePages * kBlock >= 16384, "32 dims of 128 rows on their way out");
 };
 
 __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
@@ -882,44 +883,40 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     tc_fence_after_sync();
     float weight = 1.f, other = 0.f;           // of this stream's sums and of the other's (NT = 1)
     float* theirs = reinterpret_cast<float*>(smem + C::kOffOp);        // [dim][row], over the operand tiles
+    // The columns of O that this stream writes: NT = 1, half of them.
+    const int c0 = NT == 2 ? 0 : t * (DV / 2), c1 = NT == 2 ? DV : c0 + DV / 2;
     if constexpr (NT == 1) {
-      // Both streams' products are done: stream 1 hands its sums to stream 0.
+      // Both streams' products are done: each hands the other its sums of the other's half.
       named_bar_sync(1, 256);
       float2* state = reinterpret_cast<float2*>(smem + C::kOffState);
-      if (t == 1) {
-        state[row] = make_float2(l_sum, shift);
-        if (mine > 0) {
-          const float down0 = inverse_power(up[0]), down1 = inverse_power(up[GV - 1]);
+      state[t * 128 + row] = make_float2(l_sum, shift);
+      const float down = inverse_power(up[t == 0 ? GV - 1 : 0]);
 #pragma unroll 1
-          for (int c = 0; c < DV; c += 16) {
-            uint32_t o[16];
-            tmem_ld16_nowait(tO + c, o);
-            tmem_wait_ld16(o);
+      for (int c = DV / 2 - c0; c < DV - c0; c += 16) {
+        uint32_t o[16];
+        tmem_ld16_nowait(tO + c, o);
+        tmem_wait_ld16(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              theirs[(c + i) * 128 + row] = __uint_as_float(o[i]) * (c < 64 ? down0 : down1);
-          }
-        }
+        for (int i = 0; i < 16; ++i) theirs[(c + i) * 128 + row] = mine > 0 ? __uint_as_float(o[i]) * down : 0.f;
       }
       named_bar_sync(1, 256);
-      if (t == 0 && count_of(1) > 0) {
-        const float2 x = state[row];
-        const float ref = fminf(shift, x.y);   // less the larger reference
-        weight = fast_exp2(ref - shift);
-        other = fast_exp2(ref - x.y);
-        l_sum = l_sum * weight + x.x * other;
-        shift = ref;
-      }
+      const float2 x = state[(1 - t) * 128 + row];
+      const float ref = fminf(shift, x.y);     // less the larger reference
+      weight = fast_exp2(ref - shift);
+      other = fast_exp2(ref - x.y);
+      l_sum = t == 0 ? l_sum * weight + x.x * other : x.x * other + l_sum * weight;
+      shift = ref;
     }
-    if ((NT == 2 || t == 0) && __all_sync(0xffffffffu, *abort_flag == 0)) {
+    if (__all_sync(0xffffffffu, *abort_flag == 0)) {
       const float inv = l_sum > 0.f ? 1.0f / l_sum : (l_sum == 0.f ? 0.f : l_sum);    // (NaN stays NaN)
       const int64_t out = static_cast<int64_t>(item) * 128 * NT + r - r0;
-      if (valid) p.Lpart[out] = l_sum == 0.f ? -INFINITY : (fast_log2(l_sum) - shift) * kLn2;
+      if (valid && (NT == 2 || t == 0)) p.Lpart[out] = l_sum == 0.f ? -INFINITY : (fast_log2(l_sum) - shift) * kLn2;
       const float down0 = inverse_power(up[0]) * weight, down1 = inverse_power(up[GV - 1]) * weight;
-      // 32 dims at a time over this tile's Q, then whole lines out of there.
-      uint8_t* mine_at = smem + C::kOffQ + (NT == 2 ? t : 0) * C::kQTile + quad * 4096;
+      // 32 dims at a time over this tile's Q (NT = 1: stream 1's over the pages), then
+      // whole lines out of there.
+      uint8_t* mine_at = smem + (NT == 2 || t == 0 ? C::kOffQ + t * C::kQTile : C::kOffRaw) + quad * 4096;
 #pragma unroll 1
-      for (int c = 0; c < DV; c += 32) {
+      for (int c = c0; c < c1; c += 32) {
         uint32_t o[32];
         tmem_ld32_nowait(tO + c, o);
         tmem_wait_ld32(o);
@@ -927,7 +924,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float x = __uint_as_float(o[i]) * mul;
-          if (NT == 1 && count_of(1) > 0) x = fmaf(theirs[(c + i) * 128 + row], other, x);
+          if (NT == 1) x = fmaf(theirs[(c + i) * 128 + row], other, mine > 0 ? x : 0.f);
           o[i] = __float_as_uint(x * inv);
         }
 #pragma unroll

@@ -1301,11 +1301,17 @@ def _evict_sizes(keep, first, recent) -> bool:
     return 0 < keep <= 1 << 30 and first >= 0 and recent >= 0 and first + recent <= keep
 
 
-def attn_cache_evict_workspace_bytes(cache: QuantCache, B, max_pages, keep, *, first=0, recent=0) -> int:
+@functools.lru_cache(maxsize=256)
+def _evict_bytes(Hkv, d_h, d_v, pages, B, max_pages, keep, first, recent) -> int:
     if not _evict_sizes(keep, first, recent):
         return 0
-    return int(load().attn_cache_evict_workspace_bytes(cache.arg(), int(B), int(max_pages), int(keep), int(first),
-                                                       int(recent)))
+    cache = AttnCache(Hkv, d_h, d_v, pages, None)
+    return int(load().attn_cache_evict_workspace_bytes(ctypes.byref(cache), B, max_pages, keep, first, recent))
+
+
+def attn_cache_evict_workspace_bytes(cache: QuantCache, B, max_pages, keep, *, first=0, recent=0) -> int:
+    return _evict_bytes(cache.Hkv, cache.d_h, cache.d_v, cache.pages, int(B), int(max_pages), int(keep), int(first),
+                        int(recent))
 
 
 def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int, *, first: int = 0, recent: int = 0,
@@ -1342,7 +1348,7 @@ def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int,
     kept = (torch.empty(ks, dtype=torch.int32, device=dev) if kept is None
             else _check_flat(kept, "kept", torch.int32, ks, dev))
     if workspace is None:
-        size = attn_cache_evict_workspace_bytes(cache, B, max_pages, keep, first=first, recent=recent)
+        size = _evict_bytes(cache.Hkv, cache.d_h, cache.d_v, cache.pages, B, max_pages, keep, first, recent)
         workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
     else:
         size = workspace.numel() * workspace.element_size()

@@ -967,7 +967,10 @@ struct DecodeCachePlan {
   size_t opart_bytes, lpart_bytes, bytes;
 };
 
-// merged: the caller merges parts anyway, so that ranges cost no launch.
+// merged: the caller merges parts anyway, so that ranges cost no launch: whole
+// sequences up to 32 pages.  Measured (the calls of attn_fwd_prefix_cache, ranges
+// against whole): 32 sequences of 16, 32 pages, 8 KV heads 32.9, 35.8 us against 28.2,
+// 31.9; of 64 pages 41.2, 39.2; of 1 to 64 72.6, 77.8; 8 of 128 29.7, 35.4.
 DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int max_pages, bool merged = false) {
   DecodeCachePlan d;
   const int64_t R = static_cast<int64_t>(Hq / c->Hkv) * n_q;

@@ -23,6 +23,15 @@
 // for each does: one for the tokens between `front` and m, whose places the
 // newest take, and then the newest, the others for those from m on, in whose
 // way nothing is.
+//
+// Measured (GB300, device time).  64 sequences of up to 4128 tokens, 8 heads, widths
+// 128, cut to 4096: 20 us for 66 MB, 3.2 TB/s (its floor 9.7).  8 of 16-32 thousand cut
+// to 4096: 45 us for 81 MB, 25 and 20 in the two kernels (12).  4 of 513 cut to 512: 9.
+// In the first the chain of passes over the keys with a barrier each, the schedulers
+// issuing in half of the cycles; in the second 64 CTAs make the lists, and 3000 tokens
+// a head are moved 16 bytes here and 8 there (DRAM 42 %, warps that wait for loads).
+// A cluster of eight CTAs per head, its histograms added over distributed shared
+// memory, was slower than one CTA: a barrier of the cluster for every pass.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -38,15 +47,24 @@ namespace {
 constexpr int kBins = 2048, kPasses = 3;
 constexpr int kRun = 8;                   // tokens that a thread decides on at a time
 constexpr int kUnroll = 4, kUnrollFirst = 8;
-// Threads of a CTA: few where there are many sequences and heads (four CTAs per
-// SM), many where there are not.  Weights kept in shared memory, beside histograms
-// of 24 KB: longer sequences are read from device memory each time.
+// Threads of a CTA: few where there are many sequences and heads (four CTAs per SM),
+// many where there are not.  Weights kept in shared memory, beside histograms of 24
+// KB: longer sequences are read from device memory each time.  Measured, many against
+// few, us (widths 128):
+//   4100 tokens cut to 4096: 64 heads 11.0, 13.5; 152 heads 12.0, 13.8; 304 heads 22.0,
+//   15.5; 512 heads 40.6, 20.2
+//   2048 cut to 1024: 152 heads 13.7, 15.3; 304 heads 25.4, 17.7
+//   16384 cut to 1400, past what few threads keep: 152 heads 33.5, 76 and 256 heads 64, 81
+// so few from 153 heads on, from 305 on where sequences can be that long.
 constexpr int kFewThreads = 256, kManyThreads = 1024;
 constexpr int kFewResident = 4, kManyResident = 1;
 constexpr int kFewWeights = 6144, kManyWeights = 45056;
-constexpr int kManyCtas = 304;            // up to here, many threads
-// The second kernel's CTAs per sequence and head and their threads, and the tokens
-// past the budget from which on it is worth a launch.
+constexpr int kManyCtas = 152, kManyLongCtas = 304;
+// The second kernel's CTAs per sequence and head and their threads (16 CTAs: 50 us for
+// the second case above instead of 45), and the tokens that may move from which on it is
+// worth a launch: 16384 cut to 1400, 64 heads, one kernel 23.7 us, two 22.6; 2800 to
+// 1400 14.4, 18.6; 16384 to 2400 31.6, 25.5; 4800 to 2400 19.4, 19.8; 16384 to 4096
+// 44.7, 30.9.  (With few threads it saves nothing: 304 heads 131, 134 in the last.)
 constexpr int kMoveParts = 8, kMoveThreads = 256, kMoveLeast = 2048;
 
 // Weights as integers that order like them: NaN above all, -0 as 0.
@@ -442,7 +460,6 @@ cudaError_t launch_t(CacheEvictParams p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), (most + 2 * kEvictFewMoves) * 4, done);
   if (e != cudaSuccess) return e;
-  // (In two kernels: most_moves are the places past the budget, if not fewer are chosen.)
   const bool two = THREADS == kManyThreads && p.most_moves >= kMoveLeast;
   if (!two) p.counts = nullptr;
   kern<<<static_cast<unsigned>(p.B * p.Hkv), THREADS, bytes, stream>>>(p);
@@ -462,8 +479,9 @@ cudaError_t launch_t(CacheEvictParams p, cudaStream_t stream) {
 
 template <int DH, int DV>
 cudaError_t launch_heads(const CacheEvictParams& p, cudaStream_t stream) {
-  return static_cast<int64_t>(p.B) * p.Hkv <= kManyCtas ? launch_t<DH, DV, kManyThreads>(p, stream)
-                                                        : launch_t<DH, DV, kFewThreads>(p, stream);
+  const int64_t heads = static_cast<int64_t>(p.B) * p.Hkv, cap = static_cast<int64_t>(p.max_pages) * kPageTokens;
+  return heads <= (cap <= kFewWeights ? kManyCtas : kManyLongCtas) ? launch_t<DH, DV, kManyThreads>(p, stream)
+                                                                   : launch_t<DH, DV, kFewThreads>(p, stream);
 }
 
 }  // namespace

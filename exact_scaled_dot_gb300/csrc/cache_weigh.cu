@@ -16,6 +16,15 @@
 // next is on its way to the second-level cache.  Q's fragments are kept in shared
 // memory, a sequence at a time, so that up to 256 query rows pass over a page that
 // is read once.
+//
+// Measured (GB300, device time).  8 sequences of 16-32 thousand keys, 32 heads on 8,
+// widths 128: 36 us for 126 MB, 3.5 TB/s (its floor 18.6).  48 of 4-12000 keys, 4
+// queries, 16 heads on 4, widths 128 and 64: 31 us for 93 MB (13.7).  One of 700 keys:
+// 3.9.  Bound by the issue of instructions and their latencies: some 456 a page and
+// head, a third of them codes into fragments, which eight rows' products then use
+// once; the schedulers issue in 51 % of the cycles with four warps each (128
+// registers), ALU 41, tensor pipe 18, DRAM 47 %.  (Pages by bulk copies through shared
+// memory, as the attention has them: 43 and 34 us.)
 #include <cstdint>
 #include <cuda_runtime.h>
 

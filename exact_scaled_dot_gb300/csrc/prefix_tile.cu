@@ -33,8 +33,9 @@
 // (thread = row), for which warps 1 and 3 issue the products.  With two row tiles
 // (NT = 2) stream t has tile t and both use every key tile; with one (NT = 1) the
 // streams take the key tiles in turn, each with accumulators of its own, merged
-// at the end.  The softmax takes its scores into registers at once, so that the
-// next tile's are made while it works.
+// at the end, half of the columns by each (the first alone: 31.7 us for the first
+// case below, not 30.6).  The softmax takes its scores into registers at once, so
+// that the next tile's are made while it works.
 //
 // Tensor memory, stream t, from column 128 t: the scores in 64, the weights in 32
 // and another 32, so that a tile's are put down while the product with the ones
@@ -48,6 +49,23 @@
 // fp16 operations each (0x6400 | c is 1024 + c); the pairs are the dims (k, k + 4)
 // of eight, an order that Q's rows are given too and that O's columns lose again
 // when they are written.
+//
+// Measured (GB300, device time of the whole call, and of this kernel beside the
+// others').  Widths 128 except the last: 32 sequences of 64-1024 own keys behind
+// 8192, 32 heads on 8 (128 rows a head): 30.6 us, 17; the same calls on the warps of
+// decode_cache_kernel.cuh 39.7.  64 sequences behind 32768 keys (256 rows): 73 us, 55
+// from the end of the own keys' kernel into which it runs; on the warps 190.  16
+// sequences, 64 heads on one, behind 16384 (1024 rows): 31.7 us, 19; 51.8.  24
+// sequences, 4 queries, 16 heads on 4, behind 5001, widths 128 and 64 (384 rows):
+// 32.4 us, 18; 40.4.  The tensor pipe is busy in 11 and 19 % of the cycles of the
+// first and the third, the schedulers issue in 39 and 42, and no pipe is above 30:
+// a tile takes a stream some 2300 cycles whatever its products take (260), the
+// chain of barrier, scores, exponentials (64 of a thread), weights and barrier with
+// five warps a scheduler; and a CTA 8000 cycles before its first and 8000 behind
+// its last, half of a range of 7 tiles.
+// Tried and left out: page numbers 32 at a time and the first pages earlier (0);
+// half of O written by the operands' warps (2 % slower); a maximum in place of the
+// sum (a seventh slower).
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <type_traits>
@@ -285,8 +303,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
   auto phase = [](int t, int stages) { return static_cast<uint32_t>((t / stages) & 1); };
 
   // ---- Q: each row's power of two, its fp16 operands and sums, by warps 4-19 ----
-  // 16 bytes a lane, 128 / D rows of a warp at a time, put down swizzled; then a
-  // softmax thread takes its own row into tensor memory.
+  // 16 bytes a lane, 256 / D rows of a warp at a time, put down swizzled.
   if (warp >= 4) {
     constexpr int kLanes = DH / 8, kAt = 32 / kLanes, kWarpRows = 128 * NT / 16, kTimes = kWarpRows / kAt;
     const int c = static_cast<int>(lane) % kLanes;
@@ -626,7 +643,7 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
     const bool valid = r < R;
     const uint32_t lane_base = (quad * 32u) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + 256 + 128 * t;
-    // ---- this thread's row of Q: its factor, its sums' operand, tensor memory ----
+    // ---- this thread's row of Q: its factor and its sums' operand ----
     float f;
     {
       named_bar_sync(2, 512);                              // (all rows are there)

@@ -121,6 +121,32 @@ def test_long(n, keep, recent):
     assert np.array_equal(nw.cpu().numpy(), want[1]) and np.array_equal(cache.pool.cpu().numpy(), want[0])
 
 
+@pytest.mark.parametrize("B,pages,lengths,keep,recent", [
+    (160, 205, [6500, 6401, 6560], 1500, 40),        # many heads of sequences past shared memory
+    (100, 20, [600, 640, 513], 512, 64),             # many heads
+    (100, 205, [6500, 1501, 6560], 1500, 40),        # fewer of them, long
+    (2, 210, [4100, 4097], 4096, 600),               # room for many moves, but few and the newest by a few places
+    (2, 210, [6000, 4700], 4096, 600),               # the newest by more and by little more than they are
+])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_divisions_of_the_work(B, pages, lengths, keep, recent, in_place):
+    """The sequences behind those of `lengths` stay as they are."""
+    import exact_scaled_dot_gb300 as esd
+    rng = np.random.default_rng(B + keep)
+    pool, first_rows = _pool(rng, len(lengths), 2, 64, 64, pages)
+    table = np.full((B, pages), -1, np.int32)
+    table[:len(lengths)] = first_rows
+    lengths = np.concatenate([lengths, rng.integers(0, keep + 1, B - len(lengths))])
+    w = _weights(rng, (B, 2, pages * PAGE), "ties")
+    want = _expected(pool, table, lengths, w, keep, 5, recent, 64, 64)
+    cache, W = esd.QuantCache(_dev(pool), 64, 64), _dev(w)
+    got, nw, kept = esd.attn_cache_evict(cache, _dev(table), _dev(lengths.astype(np.int32)), W, keep, first=5,
+                                         recent=recent, new_weights=W if in_place else None)
+    torch.cuda.synchronize()
+    assert np.array_equal(kept.cpu().numpy(), want[3]) and np.array_equal(got.cpu().numpy(), want[2])
+    assert np.array_equal(nw.cpu().numpy(), want[1]) and np.array_equal(cache.pool.cpu().numpy(), want[0])
+
+
 def test_budget_past_the_table_and_no_workspace():
     """A budget that no sequence reaches changes nothing and needs no workspace."""
     import exact_scaled_dot_gb300 as esd

@@ -385,3 +385,37 @@ def test_repeatable_and_on_another_stream(B):
     torch.cuda.synchronize()
     assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
     _check(c, q, O, LSE, 2, 64)
+
+
+def test_two_streams_at_once():
+    """Calls of both divisions, weights and evictions that overlap on the GPU, each with buffers of
+    its own: the bits of the same calls one after the other."""
+    import exact_scaled_dot_gb300 as esd
+    jobs = []
+    for seed, B, nq in ((51, 40, 2), (52, 48, 1), (53, 3, 2)):
+        c, q, args = _case(seed, B, 8, 2, nq, 128, 128, 3000, [nq + 21 * i for i in range(B)])
+        w = torch.rand((B, 2, args["page_table"].shape[1] * PAGE), device="cuda")
+        jobs.append((_dev(c.pool), _dev(q).to(torch.bfloat16), args, w))
+
+    def run(pool, Q, args, w):
+        cache, w = esd.QuantCache(pool, 128, 128), w.clone()
+        O, LSE = esd.attn_fwd_prefix_cache(Q, cache, **args)
+        own = dict(page_table=args["page_table"], lengths=args["lengths"])
+        esd.attn_cache_weigh(Q, cache, **own, LSE=LSE, weights=w)
+        return O, LSE, w, *esd.attn_cache_evict(cache, **own, weights=w, keep=40, first=4, recent=8), pool
+
+    want = []
+    for pool, *rest in jobs:
+        want.append(run(pool.clone(), *rest))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(4):
+        pools = [pool.clone() for pool, *_ in jobs]
+        torch.cuda.synchronize()
+        got = []
+        for s, pool, (_, *rest) in zip(streams, pools, jobs):
+            with torch.cuda.stream(s):
+                got.append(run(pool, *rest))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))

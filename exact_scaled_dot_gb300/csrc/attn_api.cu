@@ -2121,7 +2121,6 @@ int attn_cache_weigh(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q
   p.table = page_table;
   p.lengths = lengths;
   p.scale_log2 = scale * kLog2e;
-  p.wait_limit_ns = kDefaultWaitLimitNs;
   p.Q = Q;
   p.LSE = LSE;
   p.weights = weights;

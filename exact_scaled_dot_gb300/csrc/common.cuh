@@ -424,7 +424,6 @@ struct CacheWeighParams {
   const int32_t* table;        // [B][max_pages]
   const int32_t* lengths;      // [B]
   float scale_log2;            // scale * log2(e)
-  uint64_t wait_limit_ns;
   const void* Q;               // bf16 [B][Hq][n_q][d_h]
   const float* LSE;            // fp32 [B][Hq][n_q]
   float* weights;              // fp32 [B][Hkv][32 max_pages]
@@ -504,8 +503,8 @@ cudaError_t launch_qk_bwd(QkParams p, float* dgq, float* dgk, cudaStream_t strea
 cudaError_t launch_cache_append(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheIoParams& p, cudaStream_t stream);
 cudaError_t launch_decode_cache(int dh, int dv, const DecCacheParams& p, cudaStream_t stream);
-// The prefix (as one sequence), then the sequences' own keys, then their merge.
-// (tile.row_tiles > 0: by prefix_tile.cu.)
+// The sequences' own keys, the prefix (as one sequence, or by prefix_tile.cu where
+// tile.row_tiles > 0), then their merge.
 cudaError_t launch_prefix_cache(int dh, int dv, const DecCacheParams& prefix, const PrefixTileParams& tile,
                                 const PrefixMergeParams& merge, cudaStream_t stream);
 cudaError_t launch_prefix_tile(int dh, int dv, const PrefixTileParams& p, cudaStream_t stream);

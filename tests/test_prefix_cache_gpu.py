@@ -419,3 +419,25 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("B", [3, 40])
+def test_pages_past_32_bits(B):
+    """The last pages of a pool of 4.7 GB give the bits that those of a small one do."""
+    import exact_scaled_dot_gb300 as esd
+    c, q, args = _case(61, B, 8, 2, 1, 64, 64, 900, [1 + 13 * i for i in range(B)])
+    pool, Q = _dev(c.pool), _dev(q).to(torch.bfloat16)
+    far = (4_700_000_000 // pool[0].numel()) - len(pool)
+    large = torch.empty((far + len(pool), *pool.shape[1:]), dtype=torch.uint8, device="cuda")
+    large[far:] = pool
+    w = torch.rand((B, 2, args["page_table"].shape[1] * PAGE), device="cuda")
+    got = []
+    for p, by in ((pool, 0), (large, far)):
+        cache, weights = esd.QuantCache(p, 64, 64), w.clone()
+        table, prefix = args["page_table"] + by, args["prefix_table"] + by
+        O, LSE = esd.attn_fwd_prefix_cache(Q, cache, prefix, args["prefix_length"], table, args["lengths"])
+        esd.attn_cache_weigh(Q, cache, table, args["lengths"], LSE, weights)
+        got.append((O, LSE, weights, *esd.attn_cache_evict(cache, table, args["lengths"], weights, 20, first=2, recent=4)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert torch.equal(large[far:], pool)

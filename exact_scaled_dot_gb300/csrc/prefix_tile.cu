@@ -88,6 +88,11 @@ constexpr int kBelow = 2, kAbove = 1, kSpreadK = 12, kMostExp = 100;
 // kernel's time.)
 constexpr int kFastBits = 7;
 constexpr float kMostSum = 32768.0f;
+// Where scales come beside the operands O's rows are handed over with their largest
+// element below 2^(kHandOver + 1): it is at most 15 times the sum of the weights' products
+// of up to 2^31 keys, so that top is at most 2^-5 of the largest of these (2^31 15 2^5 <
+// 2^kHandOver), as it is where the weights have been so from the first tile on, or finer.
+constexpr int kHandOver = 40;
 constexpr int kScaleK = 4;          // K's largest scale becomes 2^4 to 2^5
 constexpr int kSumShift = 6;        // sum q_g 2^-6 and s (8 - z) 2^6 are fp16
 constexpr int kKeys = 64;           // keys of a tile: two pages
@@ -701,6 +706,47 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
       }
       return true;
     };
+    // The first tile with its scales beside the operands: the power of two that O carries
+    // becomes each row's top, as low as O's largest element allows.  (It says nothing of
+    // what a row has weighed: its values may have been 0, or its reference have risen since.)
+    auto hand_over = [&](int k) {
+      if (!wait_all(C::kBarPV + 2 * t + ((k - 1) & 1), static_cast<uint32_t>(((k - 1) >> 1) & 1))) return false;
+      tc_fence_after_sync();
+      float most[GV], times[GV], again[GV];
+#pragma unroll
+      for (int g = 0; g < GV; ++g) most[g] = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < DV; c += 16) {
+        uint32_t o[16];
+        tmem_ld16_nowait(tO + c, o);
+        tmem_wait_ld16(o);
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(__uint_as_float(o[i])));
+        if (c < 64) most[0] = fmaxf(most[0], m);
+        else most[GV - 1] = fmaxf(most[GV - 1], m);
+      }
+#pragma unroll
+      for (int g = 0; g < GV; ++g) {
+        const int was = static_cast<int>(__float_as_uint(up[g]) >> 23) - 127;
+        const int room = kHandOver + 127 - static_cast<int>(__float_as_uint(most[g]) >> 23);
+        const int by = max(0, min(most[g] > 0.f ? room : -kLeastTop - was, -kLeastTop - was));
+        times[g] = exp2_int(min(by, 100)), again[g] = exp2_int(by - min(by, 100));      // (up to 211 octaves)
+        up[g] = exp2_int(was + by);
+      }
+#pragma unroll 1
+      for (int c = 0; c < DV; c += 16) {
+        const float times_b = c < 64 ? times[0] : times[GV - 1], again_b = c < 64 ? again[0] : again[GV - 1];
+        uint32_t o[16];
+        tmem_ld16_nowait(tO + c, o);
+        tmem_wait_ld16(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * times_b * again_b);
+        tmem_st16_nowait(tO + c, o);
+      }
+      tmem_wait_st();                          // (rescale may read it next)
+      return true;
+    };
     auto row_max = [](const float* s) {
       float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -806,6 +852,8 @@ __global__ void __launch_bounds__(640, 1) prefix_tile_kernel(const __grid_consta
         if (folded) {
           folded = false;
           l_sum *= exp2_int(-kFastBits);
+          ok = k == 0 || hand_over(k);
+          if (!ok) break;
         }
         // The scores put together, over S_0, and their maximum; then W in the next
         // 64 columns.  (Loops: this is not where the time goes.)

@@ -441,3 +441,68 @@ def test_pages_past_32_bits(B):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(*got))
     assert torch.equal(large[far:], pool)
+
+
+def _phases(seed, group, K, V, phase):
+    """A prefix of eight ranges of 7 tiles of 64 keys for 19 KV heads, without own keys: K(n, u, phase) and
+    V(n, phase) give the keys and values [n, 19, 128] of each phase of a range (tile i of it is in phase(i)),
+    the first key of the last phase is far smaller than the others of its tile, so that scales are beside
+    the operands from there on.  Rows are alike up to a factor, along u."""
+    B, dh, tiles = 24, 128, 7
+    rng, p, cache, q = _many_heads(seed, B, group, dh, dh, 8 * tiles * 64, [0] * B)
+    u = np.sign(rng.normal(size=(19, dh)))
+    of = np.repeat([phase(i % tiles) for i in range(8 * tiles)], 64)
+    keys, values = np.zeros((len(of), 19, dh)), np.zeros((len(of), 19, dh))
+    for x in np.unique(of):
+        n = int((of == x).sum())
+        keys[of == x], values[of == x] = K(rng, n, u, x), V(rng, n, x)
+    first = np.flatnonzero((of == of.max()) & (np.roll(of, 1) != of.max()))
+    keys[first] *= 2.0 ** -16
+    ref.store(p.pool, p.slots(0, len(of)), bf16(keys), bf16(values))
+    p.K[0], p.V[0] = ref.load(p.pool, p.slots(0, len(of)), dh, dh)
+    c = cache()
+    q = bf16(u[None].repeat(group, 1)[:, :, None] * (1 + np.arange(B)[:, None, None, None] % 3 * 0.25)
+             + 0.01 * q)
+    O, LSE = _run(c, q, _many_args(c, B, group), dh, dh)
+    torch.cuda.synchronize()
+    O, LSE = f64(O), f64(LSE)
+    for b in (0, 13, 23):
+        for h in (0, 18):
+            K, V = c.K[0][:, h], c.V[0][:, h]
+            for r in range(h * group, (h + 1) * group, 3):
+                _, rL, _, eL = ref.attend(q[b, r:r + 1], K[:, None], V[:, None], len(K), dh ** -0.5)
+                assert_within(LSE[b, r], rL[0], eL[0] + 258 * 2.0 ** -23, "LSE")
+                s = K @ q[b, r, 0] * dh ** -0.5
+                A = np.exp(s - s.max())
+                A /= A.sum()
+                want, bound = A @ V, _weighted_bound(A, s, K, V, q[b, r, 0], dh)
+                assert_within(O[b, r, 0], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "O")
+
+
+@pytest.mark.parametrize("group", [4, 16])
+@pytest.mark.parametrize("octaves", [20, 30, 60, 90])
+@pytest.mark.parametrize("groups", [(1,), (0, 1)])
+def test_no_values_before_the_scales_part(group, octaves, groups):
+    """A group of 64 dims has no value but 0 while scales are in the operands, and small ones behind."""
+    def values(rng, n, phase):
+        V = rng.normal(size=(n, 19, 128))
+        for g in groups:
+            V[:, :, 64 * g:64 * g + 64] *= 2.0 ** -octaves if phase else 0.0
+        return V
+    _phases(group + octaves, group, lambda rng, n, u, phase: 0.3 * rng.normal(size=(n, 19, 128)), values,
+            lambda tile: int(tile > 2))
+
+
+@pytest.mark.parametrize("group", [4, 16])
+@pytest.mark.parametrize("octaves", [25, 35, 80, 120])
+def test_values_that_no_longer_weigh_before_the_scales_part(group, octaves):
+    """Scores rise by more octaves than the values fall while scales are in the operands, at keys whose
+    values are 0; behind, what there was before weighs less than the small values."""
+    climb = (octaves + 8) * np.log(2.0) * 128 ** -0.5
+
+    def keys(rng, n, u, phase):
+        return 0.02 * rng.normal(size=(n, 19, 128)) + (climb if phase else 0.0) * u
+
+    def values(rng, n, phase):
+        return rng.normal(size=(n, 19, 128)) * (2.0 ** 40, 0.0, 2.0 ** (40 - octaves))[phase]
+    _phases(group + octaves, group, keys, values, lambda tile: 0 if tile < 2 else 1 if tile < 4 else 2)

@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(kThreads, kResident) cache_weigh_kernel(const 
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           qv[gk][w] = r < R ? q[gk * 8 + 2 * t + w] : make_uint4(0u, 0u, 0u, 0u);
+          // (Adds nothing, whatever it holds: a NaN would pass the -inf below.)
+          if (lse == -INFINITY) qv[gk][w] = make_uint4(0u, 0u, 0u, 0u);
           m = bf16_absmax_fold(m, qv[gk][w]);
         }
       uint32_t mb = __float_as_uint(bf16_absmax_value(m));     // (as bits, so that a NaN is the largest)

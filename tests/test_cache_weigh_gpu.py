@@ -154,3 +154,21 @@ def test_captured_and_repeated():
     esd.attn_cache_weigh(*args, two, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(two, one)
+
+
+@pytest.mark.parametrize("nq", [1, 3])
+def test_rows_without_a_log_sum_exp_add_nothing_whatever_they_hold(nq):
+    """LSE = -inf beside an infinity or a NaN in the row of Q, at keys that the row sees."""
+    import exact_scaled_dot_gb300 as esd
+    dh = 64
+    c, q, w, lse = _case(23 + nq, 2, 4, 2, nq, dh, dh, [70, 33])
+    lse[0, 1, nq - 1] = lse[1, 2] = -np.inf
+    want = [srv.weigh(q[b], c.K[b], lse[b].astype(np.float64), c.lengths[b], w[b], dh ** -0.5) for b in range(2)]
+    q[0, 1, nq - 1, 7] = np.nan
+    q[1, 2, :, 3] = np.inf
+    W = _dev(w)
+    esd.attn_cache_weigh(_dev(q).to(torch.bfloat16), esd.QuantCache(_dev(c.pool), dh, dh), _dev(c.table),
+                         _dev(np.array(c.lengths, np.int32)), _dev(lse), W)
+    torch.cuda.synchronize()
+    for b in range(2):
+        assert_within(f64(W)[b], *want[b], "weights")

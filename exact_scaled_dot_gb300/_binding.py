@@ -1323,8 +1323,8 @@ def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int,
     where it is, and the last `recent` keep their order.  page_table int32
     [B, max_pages], lengths int32 [B].  Returns (new_lengths int32 [B], new_weights
     like weights, kept int32 [B, Hkv, keep]: the place that the token at each
-    place had, -1 past the new length).  new_weights may be weights; new_lengths
-    may not be lengths."""
+    place had, -1 past the new length).  new_weights may be weights;
+    outputs overlap neither one another nor inputs otherwise."""
     if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D [B, max_pages]")
     B, max_pages = page_table.shape

@@ -1121,6 +1121,20 @@ int check_words(std::initializer_list<const void*> ptrs) {
   return ATTN_OK;
 }
 
+// Arrays of 32-bit elements; whether one of the first shares a byte with one of the second.
+struct Words {
+  const void* at;
+  size_t count;
+};
+bool share_bytes(std::initializer_list<Words> a, std::initializer_list<Words> b) {
+  for (const Words& x : a)
+    for (const Words& y : b) {
+      const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.at), y0 = reinterpret_cast<uintptr_t>(y.at);
+      if (x.count > 0 && y.count > 0 && (x0 <= y0 ? y0 - x0 < 4 * x.count : x0 - y0 < 4 * y.count)) return true;
+    }
+  return false;
+}
+
 }  // namespace
 }  // namespace esd
 
@@ -2153,6 +2167,16 @@ int attn_cache_evict(const attn_cache* cache, int32_t B, int32_t max_pages, int3
   const size_t need = attn_cache_evict_workspace_bytes(cache, B, max_pages, keep, first, recent);
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need))
     return ATTN_ERR_WORKSPACE;
+  // CTAs write outputs while others still read: only the weights may be their own
+  // output, place for place.
+  const size_t heads = static_cast<size_t>(B) * cache->Hkv;
+  const Words table_w{page_table, static_cast<size_t>(B) * max_pages}, lengths_w{lengths, static_cast<size_t>(B)};
+  const Words weights_w{weights, heads * max_pages * kPageTokens}, new_lengths_w{new_lengths, lengths_w.count};
+  const Words new_weights_w{new_weights, weights_w.count}, kept_w{kept, kept ? heads * keep : 0};
+  if (share_bytes({new_lengths_w, kept_w}, {table_w, lengths_w, weights_w, new_weights_w}) ||
+      share_bytes({new_weights_w}, {table_w, lengths_w}) || share_bytes({new_lengths_w}, {kept_w}) ||
+      (new_weights != weights && share_bytes({new_weights_w}, {weights_w})))
+    return ATTN_ERR_SHAPE;
   // ---- CUDA from here on ----
   unsigned int* status = nullptr;
   rc = device_status_ptr(&status);

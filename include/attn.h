@@ -684,7 +684,8 @@ int attn_cache_weigh(const attn_cache* cache, int32_t B, int32_t Hq, int32_t n_q
  *   kept [B][Hkv][keep]        (or NULL) the place that the token at each place had; -1 past
  *                              the new length
  * All device memory; lengths and page_table [B][max_pages] are read when the
- * call runs.  new_lengths must not be lengths, first + recent <= keep <= 2^30,
+ * call runs.  The outputs overlap neither one another nor lengths, page_table
+ * or weights, but for new_weights == weights; first + recent <= keep <= 2^30,
  * max_pages <= 2^25 (else ATTN_ERR_SHAPE).  Pages that a token moves in or out of belong to one
  * sequence only: tokens below `first` do not move, so that shared pages at the
  * front are safe below it.  The pages behind the new length are free

@@ -286,3 +286,26 @@ def test_serving_loop(B):
     # the prefix's pages are as they were
     pages = c.table[0, :-(-prefix // PAGE)]
     assert np.array_equal(cache.pool.cpu().numpy()[pages], c.pool[pages])
+
+
+def test_outputs_next_to_inputs():
+    """Arrays that are parts of one buffer, one right behind the other, are not refused; one element nearer
+    they are."""
+    import exact_scaled_dot_gb300 as esd
+    rng = np.random.default_rng(8)
+    pool, table = _pool(rng, 2, 1, 64, 64, 3)
+    w, lengths, keep = _weights(rng, (2, 1, 96), "plain"), np.array([90, 50], np.int32), 40
+    want = _expected(pool, table, lengths, w, keep, 4, 8, 64, 64)
+    cache, both = esd.QuantCache(_dev(pool), 64, 64), torch.zeros(2 * 192, device="cuda")
+    n = _dev(np.concatenate([lengths, lengths]))
+    both[:192] = _dev(w).flatten()
+    W = both[:192].view(2, 1, 96)
+    for out in (dict(new_lengths=n[1:3]), dict(new_weights=both[1:193].view(2, 1, 96)),
+                dict(new_weights=both[191:383].view(2, 1, 96))):
+        with pytest.raises(esd.AttnError):
+            esd.attn_cache_evict(cache, _dev(table), n[:2], W, keep, first=4, recent=8, **out)
+    got, nw, kept = esd.attn_cache_evict(cache, _dev(table), n[:2], W, keep, first=4, recent=8, new_lengths=n[2:],
+                                         new_weights=both[192:].view(2, 1, 96))
+    torch.cuda.synchronize()
+    assert np.array_equal(kept.cpu().numpy(), want[3]) and np.array_equal(n.cpu().numpy()[2:], want[2])
+    assert np.array_equal(nw.cpu().numpy(), want[1]) and np.array_equal(cache.pool.cpu().numpy(), want[0])

@@ -175,3 +175,32 @@ def test_eviction_sizes_are_checked_before_they_are_32_bits(lib, first, recent, 
     assert esd.attn_cache_evict_workspace_bytes(Fake, 2, 1 << 20, keep, first=first, recent=recent) == 0
     if keep < 1 << 31 and first < 1 << 31:
         assert lib.attn_cache_evict_workspace_bytes(_cache(), 2, 1 << 20, keep, first, recent) == 0
+
+
+def test_eviction_refuses_outputs_over_its_inputs(lib):
+    """An output that shares a byte with an input or with another output, but for the weights in place.
+    (Every call here is refused: none reaches a device.)"""
+    B, Hkv, pages, keep = 3, 2, 4, 64
+    size = dict(table=4 * B * pages, lengths=4 * B, weights=4 * B * Hkv * 32 * pages, new_lengths=4 * B,
+                new_weights=4 * B * Hkv * 32 * pages, kept=4 * B * Hkv * keep)
+    at, free = {}, 4096
+    for name, n in size.items():
+        at[name], free = free, free + n                    # one right behind the other
+
+    def call(**moved):
+        a = {**at, **moved}
+        return lib.attn_cache_evict(_cache(Hkv), B, pages, keep, 4, 8, *(ctypes.c_void_p(a[k]) for k in (
+            "table", "lengths", "weights", "new_lengths", "new_weights", "kept")), None, ctypes.c_size_t(0), None)
+
+    outputs = ("new_lengths", "new_weights", "kept")
+    for out in outputs:
+        for other in size:
+            if other == out:
+                continue
+            for to in (at[other] + 4, at[other] + size[other] - 4, at[other] - size[out] + 4):
+                assert call(**{out: to}) == S, (out, other, to)
+            if (out, other) != ("new_weights", "weights"):
+                assert call(**{out: at[other]}) == S, (out, other)
+    # in place, the others are checked as well
+    assert call(new_weights=at["weights"], kept=at["weights"]) == S
+    assert call(new_weights=at["weights"], new_lengths=at["lengths"] + 4) == S

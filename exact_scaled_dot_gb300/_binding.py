@@ -1323,8 +1323,10 @@ def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int,
     where it is, and the last `recent` keep their order.  page_table int32
     [B, max_pages], lengths int32 [B].  Returns (new_lengths int32 [B], new_weights
     like weights, kept int32 [B, Hkv, keep]: the place that the token at each
-    place had, -1 past the new length).  new_weights may be weights;
-    outputs overlap neither one another nor inputs otherwise."""
+    place had, -1 past the new length).  kept=False leaves these places out (None
+    comes back): they take 4 B Hkv keep bytes, however short the sequences are.
+    new_weights may be weights; outputs overlap neither one another nor inputs
+    otherwise."""
     if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D [B, max_pages]")
     B, max_pages = page_table.shape
@@ -1345,8 +1347,11 @@ def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int,
                    else _check_flat(new_lengths, "new_lengths", torch.int32, (B,), dev))
     new_weights = (torch.empty(ws, dtype=torch.float32, device=dev) if new_weights is None
                    else _check_flat(new_weights, "new_weights", torch.float32, ws, dev))
-    kept = (torch.empty(ks, dtype=torch.int32, device=dev) if kept is None
-            else _check_flat(kept, "kept", torch.int32, ks, dev))
+    if kept is False:
+        kept = None
+    else:
+        kept = (torch.empty(ks, dtype=torch.int32, device=dev) if kept is None
+                else _check_flat(kept, "kept", torch.int32, ks, dev))
     if workspace is None:
         size = _evict_bytes(cache.Hkv, cache.d_h, cache.d_v, cache.pages, B, max_pages, keep, first, recent)
         workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
@@ -1354,6 +1359,6 @@ def attn_cache_evict(cache: QuantCache, page_table, lengths, weights, keep: int,
         size = workspace.numel() * workspace.element_size()
     _check(load().attn_cache_evict(cache.arg(), B, max_pages, keep, first, recent, page_table.data_ptr(),
                                    lengths.data_ptr(), weights.data_ptr(), new_lengths.data_ptr(),
-                                   new_weights.data_ptr(), kept.data_ptr(), _addr(workspace), size,
+                                   new_weights.data_ptr(), _addr(kept), _addr(workspace), size,
                                    torch._C._cuda_getCurrentRawStream(dev.index)), "attn_cache_evict")
     return new_lengths, new_weights, kept

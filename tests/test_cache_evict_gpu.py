@@ -309,3 +309,22 @@ def test_outputs_next_to_inputs():
     torch.cuda.synchronize()
     assert np.array_equal(kept.cpu().numpy(), want[3]) and np.array_equal(n.cpu().numpy()[2:], want[2])
     assert np.array_equal(nw.cpu().numpy(), want[1]) and np.array_equal(cache.pool.cpu().numpy(), want[0])
+
+
+@pytest.mark.parametrize("keep,lengths", [(40, [90, 50]), (2500, [5000, 2501]), (1 << 30, [60, 0])])
+def test_without_the_places_kept(keep, lengths):
+    """kept=False: the same tokens, weights and lengths; also with the largest budget, whose places would take
+    4 GiB a head."""
+    import exact_scaled_dot_gb300 as esd
+    rng = np.random.default_rng(keep)
+    pages = -(-max(lengths) // PAGE)
+    pool, table = _pool(rng, 2, 2, 64, 64, pages)
+    w, lengths = _weights(rng, (2, 2, pages * PAGE), "ties"), np.array(lengths, np.int32)
+    want = _expected(pool, table, lengths, w, min(keep, pages * PAGE), 4, 8, 64, 64)
+    cache = esd.QuantCache(_dev(pool), 64, 64)
+    before = torch.cuda.memory_allocated()
+    got, nw, kept = esd.attn_cache_evict(cache, _dev(table), _dev(lengths), _dev(w), keep, first=4, recent=8, kept=False)
+    torch.cuda.synchronize()
+    assert kept is None and torch.cuda.memory_allocated() - before < 1 << 24
+    assert np.array_equal(got.cpu().numpy(), want[2]) and np.array_equal(nw.cpu().numpy(), want[1])
+    assert np.array_equal(cache.pool.cpu().numpy(), want[0])

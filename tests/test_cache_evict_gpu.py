@@ -288,6 +288,28 @@ def test_serving_loop(B):
     assert np.array_equal(cache.pool.cpu().numpy()[pages], c.pool[pages])
 
 
+@pytest.mark.parametrize("n", [50000, 200003])
+@pytest.mark.parametrize("keep", [300, 9000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_weights_past_shared_memory(n, keep, in_place):
+    """One head of more tokens than its CTA keeps weights of, and of more than it keeps decisions of; of equal
+    weights only some stay.  Moves below and above what takes a second kernel."""
+    import exact_scaled_dot_gb300 as esd
+    rng = np.random.default_rng(n + keep)
+    pages = -(-n // PAGE)
+    pool, table = _pool(rng, 1, 1, 64, 64, pages)
+    w = np.minimum(_weights(rng, (1, 1, pages * PAGE), "ties"), 8.0)
+    want = _expected(pool, table, np.array([n]), w, keep, 3, 40, 64, 64)
+    least = want[1][0, 0, 3:keep - 40].min()
+    assert 0 < (want[1][0, 0, 3:keep - 40] == least).sum() < (w[0, 0, 3:n - 40] == least).sum()
+    cache, W = esd.QuantCache(_dev(pool), 64, 64), _dev(w)
+    got, nw, kept = esd.attn_cache_evict(cache, _dev(table), _dev(np.array([n], np.int32)), W, keep, first=3, recent=40,
+                                         new_weights=W if in_place else None)
+    torch.cuda.synchronize()
+    assert np.array_equal(kept.cpu().numpy(), want[3]) and np.array_equal(got.cpu().numpy(), want[2])
+    assert np.array_equal(nw.cpu().numpy(), want[1]) and np.array_equal(cache.pool.cpu().numpy(), want[0])
+
+
 def test_outputs_next_to_inputs():
     """Arrays that are parts of one buffer, one right behind the other, are not refused; one element nearer
     they are."""

@@ -156,6 +156,22 @@ def test_captured_and_repeated():
     assert torch.equal(two, one)
 
 
+def test_lengths_past_the_table_and_below_zero():
+    """A length past the table is cut to it; a sequence of negative length is left alone."""
+    import exact_scaled_dot_gb300 as esd
+    dh = 128
+    c, q, w, lse = _case(19, 2, 4, 1, 1, dh, dh, [96, 64], max_pages=3)
+    W = _dev(w)
+    esd.attn_cache_weigh(_dev(q).to(torch.bfloat16), esd.QuantCache(_dev(c.pool), dh, dh), _dev(c.table),
+                         _dev(np.array([1 << 30, -4], np.int32)), _dev(lse), W)
+    torch.cuda.synchronize()
+    assert esd.attn_get_status() == esd.ATTN_ERR_PAGE
+    esd.attn_clear_status()
+    want, err = srv.weigh(q[0], c.K[0], lse[0].astype(np.float64), 96, w[0], dh ** -0.5)
+    assert_within(f64(W)[0], want, err, "weights")
+    assert np.array_equal(W.cpu().numpy()[1], w[1])
+
+
 @pytest.mark.parametrize("nq", [1, 3])
 def test_rows_without_a_log_sum_exp_add_nothing_whatever_they_hold(nq):
     """LSE = -inf beside an infinity or a NaN in the row of Q, at keys that the row sees."""

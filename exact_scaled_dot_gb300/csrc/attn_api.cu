@@ -970,7 +970,8 @@ struct DecodeCachePlan {
 // merged: the caller merges parts anyway, so that ranges cost no launch: whole
 // sequences up to 32 pages.  Measured (the calls of attn_fwd_prefix_cache, ranges
 // against whole): 32 sequences of 16, 32 pages, 8 KV heads 32.9, 35.8 us against 28.2,
-// 31.9; of 64 pages 41.2, 39.2; of 1 to 64 72.6, 77.8; 8 of 128 29.7, 35.4.
+// 31.9; of 64 pages 41.2, 39.2; of 1 to 64 72.6, 77.8; 8 of 128 29.7, 35.4.  (At 64
+// pages full sequences would gain 2 us by being whole, ragged ones lose 5.)
 DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, int max_pages, bool merged = false) {
   DecodeCachePlan d;
   const int64_t R = static_cast<int64_t>(Hq / c->Hkv) * n_q;
@@ -1003,6 +1004,8 @@ DecodeCachePlan decode_cache_plan(const attn_cache* c, int B, int Hq, int n_q, i
 //   8 KV heads, prefix 16384: 64 rows 31.2, 33.7; 128 rows 46.9, 34.5; 256 rows 90.5, 39.8
 //   1 KV head, prefix 16384:  128 rows 22.4, 22.7; 256 rows 23.5, 25.3; 512 rows 30.4, 29.5
 // and at least eight pages a tile's range (four: 28.3 and 33.9 us in the last line).
+// At 8192 passes themselves the tiles gain 2 us with eight KV heads and lose 2 with one
+// (the 256 rows of the first and of the last line).
 constexpr int kPrefixTileRows = 65;
 constexpr int64_t kPrefixTilePasses = 8192;
 constexpr int kMinPrefixTilePages = 8;

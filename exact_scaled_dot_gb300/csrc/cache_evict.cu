@@ -18,9 +18,9 @@
 // places free and those that move their ranks, without atomics on the lists.
 //
 // Work: a CTA per sequence and head, with the weights as integers in its shared
-// memory where they fit.  It moves the tokens too; or, where there are few
-// sequences and heads and many tokens to move, a second kernel with several CTAs
-// for each does: one for the tokens between `front` and m, whose places the
+// memory where the page table's places fit.  It moves the tokens too; or, where there
+// are few sequences and heads and many tokens may have to move, by the table's places,
+// a second kernel with several CTAs for each does: one for the tokens between `front` and m, whose places the
 // newest take, and then the newest, the others for those from m on, in whose
 // way nothing is.
 //
@@ -49,7 +49,11 @@ constexpr int kRun = 8;                   // tokens that a thread decides on at 
 constexpr int kUnroll = 4, kUnrollFirst = 8;
 // Threads of a CTA: few where there are many sequences and heads (four CTAs per SM),
 // many where there are not.  Weights kept in shared memory, beside histograms of 24
-// KB: longer sequences are read from device memory each time.  Measured, many against
+// KB: those of sequences in wider page tables are read from device memory each time,
+// short ones too, since the launch knows the table alone.  (Cut from up to 4128 tokens to 4096
+// in tables of 129, 192, 193, 512, 1024 pages: 512 heads 19.7, 20.7, 25.1, 27.9, 36.2 us,
+// of which the zeros behind the budget are up to 67 MB; 64 heads 11.1, 17.7, 17.7, 18.3,
+// 19.3, from 192 pages on with the second kernel.)  Measured, many against
 // few, us (widths 128):
 //   4100 tokens cut to 4096: 64 heads 11.0, 13.5; 152 heads 12.0, 13.8; 304 heads 22.0,
 //   15.5; 512 heads 40.6, 20.2

@@ -13,9 +13,9 @@
 // kernel too or, for many rows, prefix_tile.cu) and the merge.  The first is the one
 // with short and with long CTAs, so it goes first: the prefix's CTAs take the places
 // that it leaves and wait for its end before they exit, and the merge waits for
-// them.  The plan in attn_api.cu has the rules.  Two sequences of up to 40 keys behind 500: 7.4 us, three short
-// chains of launch, lengths, pages; the call's 28 us are host time, 9 of them the
-// launches, as many the three tensors.
+// them.  The plan in attn_api.cu has the rules.  Two sequences of up to 40 keys
+// behind 500: 7.4 us, three short chains of launch, lengths, pages; the call's 26 to
+// 28 us are host time, 9 of them the launches, as many the three tensors.
 #include <cstdint>
 #include <cuda_runtime.h>
 

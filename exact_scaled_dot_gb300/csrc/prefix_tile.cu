@@ -25,7 +25,11 @@
 // a CTA goes on with operands c - z alone: S_g = Q_g (c - z)_g^T, s_ij = f_i sum_g
 // sk_gj S_g,ij in fp32, O_g += W_g (c - z)_g with W_g,ij = fp16(P_ij sv_gj /
 // top_gi), and the powers of two `top` per row and group of the attention of a
-// few rows over this cache (decode_cache_kernel.cuh, where they are explained).
+// few rows over this cache (decode_cache_kernel.cuh, where they are explained).  At the
+// first such tile O goes over from E_g to a `top` that its own size allows, since E_g
+// says nothing of what the row has weighed.  (With a key 2^-14 of the others in each 700,
+// the first two cases below take 36 and 115 us; 35 and 112 with E_g as the first top,
+// which lost the weights of small values behind zeros.)
 //
 // CTA: 640 threads, one per SM.  Warp 0 brings pages into a ring (bulk copies),
 // warp 2 looks at a tile's scales, warps 12-19 turn it into K-major and MN-major

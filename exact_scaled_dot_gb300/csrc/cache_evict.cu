@@ -52,7 +52,7 @@ constexpr int kUnroll = 4, kUnrollFirst = 8;
 // KB: those of sequences in wider page tables are read from device memory each time,
 // short ones too, since the launch knows the table alone.  (Cut from up to 4128 tokens to 4096
 // in tables of 129, 192, 193, 512, 1024 pages: 512 heads 19.7, 20.7, 25.1, 27.9, 36.2 us,
-// of which the zeros behind the budget are up to 67 MB; 64 heads 11.1, 17.7, 17.7, 18.3,
+// with up to 59 MB of zeros behind the budget; 64 heads 11.1, 17.7, 17.7, 18.3,
 // 19.3, from 192 pages on with the second kernel.)  Measured, many against
 // few, us (widths 128):
 //   4100 tokens cut to 4096: 64 heads 11.0, 13.5; 152 heads 12.0, 13.8; 304 heads 22.0,
